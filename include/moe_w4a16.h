@@ -220,6 +220,88 @@ int moe_w4a16_forward_partial(moe_w4a16_t h, const uint16_t* hidden, const int32
                               void* workspace, size_t workspace_bytes, void* stream);
 int moe_w4a16_finalize(const float* acc, uint16_t* out, long long n, void* stream);
 
+/* ---- operators around the routed experts ------------------------------- */
+
+/* Element types of the floating inputs and outputs below. */
+enum { MOE_W4A16_F32 = 0, MOE_W4A16_BF16 = 1 };
+
+/* Scores of moe_w4a16_route_scored. */
+enum { MOE_W4A16_SCORE_SOFTMAX = 0, MOE_W4A16_SCORE_SIGMOID = 1 };
+
+/* Router with scores, a balance bias and expert groups; its ids and weights are the
+ * inputs of moe_w4a16_forward (moe_w4a16_route is the softmax-of-the-selected form
+ * without these). For every token, in fp32:
+ *   s = sigmoid(l), or softmax(l) over all E
+ *   c = s + bias                               (for the selection only)
+ *   the E experts are n_group groups of E / n_group consecutive ones; a group counts
+ *   its largest c (group_top 1) or the sum of its two largest (group_top 2), and only
+ *   the experts of the topk_group best groups stay
+ *   topk_ids = the topk largest c that stay, in descending order
+ *   topk_weights = s of those, divided by their sum if `renormalize`, times `scale`
+ * Equal values: the lower group, the lower expert id. A logit of -infinity or NaN
+ * marks an expert that is not to be chosen: it ranks behind every other one of the
+ * groups that stay, counts nothing in its group's value, and where a row holds too few
+ * others it fills the remaining places with weight 0 (a row of nothing else gives
+ * weights of 0, not NaN). +infinity counts as the largest number. The type's lowest
+ * number is an ordinary logit.
+ *   logits        fp32 or bf16 (logits_type) [M, E], rows row_stride elements apart
+ *   bias          fp32 [E] or NULL
+ *   topk_ids      int32 [M, topk], topk_weights fp32 [M, topk]   out
+ * 1 <= E <= 1024, 1 <= topk <= min(32, topk_group * E / n_group), n_group <= 32 and a
+ * divisor of E. M == 0 is a no-op. One launch on `stream`, no host synchronisation. */
+int moe_w4a16_route_scored(const void* logits, int logits_type, long long row_stride, int M, int E, int topk,
+                           int scoring, const float* bias, int n_group, int topk_group, int group_top,
+                           int renormalize, float scale, int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* Block quantisers: 8-bit floating point (e4m3: 4 exponent and 3 fraction bits,
+ * largest value 448) with one fp32 scale for each 128 columns,
+ *   s = max(amax / 448, 2^-126),  q = e4m3(x / s)  (nearest, ties to even),
+ * the last block of a row being what is left of it. The value stored is q * s. A block
+ * with a NaN gets a NaN scale and NaN values, one with an infinity an infinite scale.
+ *   x   fp32 or bf16 (x_type) [M, K], rows row_stride elements apart
+ *   q   [M, K] bytes, s fp32 [M, ceil(K / 128)]   out, contiguous
+ * swiglu_quantize: x = rows [g | u] of 2 N values, quantises h = g / (1 + exp(-g)) * u
+ * (computed in fp32): q [M, N], s [M, ceil(N / 128)].
+ * quantize_weight: one scale for each block of 128 rows x 128 columns of w [N, K]:
+ * s [ceil(N / 128), ceil(K / 128)].
+ * M == 0 (N == 0) is a no-op. One launch on `stream`, no host synchronisation. */
+int moe_w4a16_fp8_quantize(const void* x, int x_type, long long row_stride, int M, int K, uint8_t* q, float* s,
+                           void* stream);
+int moe_w4a16_fp8_swiglu_quantize(const void* gate_up, int x_type, long long row_stride, int M, int N, uint8_t* q,
+                                  float* s, void* stream);
+int moe_w4a16_fp8_quantize_weight(const void* w, int w_type, long long row_stride, int N, int K, uint8_t* q, float* s,
+                                  void* stream);
+
+/* 8-bit block-scaled matrix product:
+ *   out[m, n] = sum_k a[m, k] a_s[m, k / 128] b[n, k] b_s[n / 128, k / 128]  (+ add[m, n])
+ * e4m3 operands, the sums in fp32, rounded once to the output's type.
+ *   a    [M, K] bytes, rows lda bytes apart;  a_s fp32 [M, ceil(K / 128)]
+ *   b    [N, K] bytes, rows ldb bytes apart;  b_s fp32 [ceil(N / 128), ceil(K / 128)]
+ *   add  bf16 [M, N] or NULL; may be `out` itself when out_type is bf16
+ *   out  bf16 or fp32 (out_type) [M, N]
+ * Any M, N >= 0 and K >= 1, contiguous scales, add and out. M == 0 or N == 0 is a
+ * no-op. One launch on `stream`, no workspace, no host synchronisation, and the same
+ * result in every run (no atomics). */
+int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, const uint8_t* b, long long ldb,
+                         const float* b_s, const uint16_t* add, void* out, int out_type, int M, int N, int K,
+                         void* stream);
+
+/* Shared expert: the dense SwiGLU feed-forward that every token takes next to its
+ * routed experts, with 8-bit block-scaled weights and activations:
+ *   q1, s1 = quantize(hidden)              [g | u] = q1 s1 . (w1 w1_s)^T   (fp32)
+ *   q2, s2 = quantize(SiLU(g) * u)         out = bf16(q2 s2 . (w2 w2_s)^T + add)
+ *   hidden bf16 [M, K];  w1 [2N, K] (gate rows, then up rows), w1_s [2N/128, K/128];
+ *   w2 [K, N], w2_s [K/128, N/128];  add bf16 [M, K] (the routed experts' output) or
+ *   NULL, may be `out`;  out bf16 [M, K];  all contiguous
+ *   workspace  >= moe_w4a16_shared_expert_workspace_size(M, K, N) bytes (0 for a shape
+ *   that is not supported), 256-byte aligned; holds nothing between calls
+ * K % 128 == 0, N % 128 == 0. M == 0 is a no-op. Launches on `stream`, allocates
+ * nothing, no host synchronisation. */
+size_t moe_w4a16_shared_expert_workspace_size(int M, int K, int N);
+int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const float* w1_s, const uint8_t* w2,
+                            const float* w2_s, const uint16_t* add, uint16_t* out, int M, int K, int N,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
 /* Read the device status word of the last forward that used `workspace`
  * (bits MOE_W4A16_STATUS_*; 0 = clean). Synchronises `stream`. */
 int moe_w4a16_status(moe_w4a16_t h, const void* workspace, int32_t* status, void* stream);

@@ -23,6 +23,9 @@ __all__ = [
     "OPT_NUM_CTAS", "OPT_PROFILE", "OPT_PDL", "OPT_STEP_COST_GATEUP", "OPT_STEP_COST_DOWN",
     "OPT_WAIT_LIMIT_US", "OPT_TEST_WAIT_NEVER_COMPLETES", "OPT_FUSED_SMALL_BATCH", "OPT_GEMV_SMALL_BATCH", "OPT_GEMV_ONE_LAUNCH", "STATUS_BAD_EXPERT_ID", "STATUS_TIMEOUT", "STATUS_H_SATURATED",
     "STATUS_BAD_SCHEDULE",
+    "moe_w4a16_route_scored", "moe_w4a16_fp8_quantize", "moe_w4a16_fp8_swiglu_quantize",
+    "moe_w4a16_fp8_quantize_weight", "moe_w4a16_fp8_matmul", "moe_w4a16_shared_expert_workspace_size",
+    "moe_w4a16_shared_expert", "F32", "BF16", "SCORE_SOFTMAX", "SCORE_SIGMOID",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libmoe_w4a16.so")
@@ -38,8 +41,11 @@ OPT_FUSED_SMALL_BATCH = 8
 OPT_GEMV_SMALL_BATCH = 9
 OPT_GEMV_ONE_LAUNCH = 10
 NOALLOC_WORKSPACE_BYTES = 48 << 20
+F32, BF16 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_c_ll = ctypes.c_longlong
 
 # name -> (restype, argtypes); mirrors include/moe_w4a16.h
 _SIGNATURES = {
@@ -68,6 +74,15 @@ _SIGNATURES = {
     "moe_w4a16_schedule_debug": (_c_int, [_vp, _vp, _c_int, ctypes.POINTER(ctypes.c_int64), _c_int,
                                           ctypes.POINTER(_c_int), _vp]),
     "moe_w4a16_forward_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _vp]),
+    "moe_w4a16_route_scored": (_c_int, [_vp, _c_int, _c_ll, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _c_int,
+                                        _c_int, _c_int, ctypes.c_float, _vp, _vp, _vp]),
+    "moe_w4a16_fp8_quantize": (_c_int, [_vp, _c_int, _c_ll, _c_int, _c_int, _vp, _vp, _vp]),
+    "moe_w4a16_fp8_swiglu_quantize": (_c_int, [_vp, _c_int, _c_ll, _c_int, _c_int, _vp, _vp, _vp]),
+    "moe_w4a16_fp8_quantize_weight": (_c_int, [_vp, _c_int, _c_ll, _c_int, _c_int, _vp, _vp, _vp]),
+    "moe_w4a16_fp8_matmul": (_c_int, [_vp, _c_ll, _vp, _vp, _c_ll, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                      _vp]),
+    "moe_w4a16_shared_expert_workspace_size": (_c_size, [_c_int, _c_int, _c_int]),
+    "moe_w4a16_shared_expert": (_c_int, [_vp] * 7 + [_c_int, _c_int, _c_int, _vp, _c_size, _vp]),
 }
 
 _LIB = None
@@ -275,6 +290,42 @@ def moe_w4a16_forward_noalloc(h, hidden, topk_ids, topk_weights, out, M, stream=
     is a fixed array inside the library (see include/moe_w4a16.h)."""
     _check(lib().moe_w4a16_forward_noalloc(h, _ptr(hidden), _ptr(topk_ids), _ptr(topk_weights),
                                            _ptr(out), M, _stream(stream)))
+
+
+def moe_w4a16_route_scored(logits, logits_type, row_stride, M, E, topk, scoring, bias, n_group, topk_group,
+                           group_top, renormalize, scale, topk_ids, topk_weights, stream=None):
+    _check(lib().moe_w4a16_route_scored(_ptr(logits), logits_type, row_stride, M, E, topk, scoring, _ptr(bias),
+                                        n_group, topk_group, group_top, renormalize, scale, _ptr(topk_ids),
+                                        _ptr(topk_weights), _stream(stream)))
+
+
+def moe_w4a16_fp8_quantize(x, x_type, row_stride, M, K, q, s, stream=None):
+    _check(lib().moe_w4a16_fp8_quantize(_ptr(x), x_type, row_stride, M, K, _ptr(q), _ptr(s), _stream(stream)))
+
+
+def moe_w4a16_fp8_swiglu_quantize(gate_up, x_type, row_stride, M, N, q, s, stream=None):
+    _check(lib().moe_w4a16_fp8_swiglu_quantize(_ptr(gate_up), x_type, row_stride, M, N, _ptr(q), _ptr(s),
+                                               _stream(stream)))
+
+
+def moe_w4a16_fp8_quantize_weight(w, w_type, row_stride, N, K, q, s, stream=None):
+    _check(lib().moe_w4a16_fp8_quantize_weight(_ptr(w), w_type, row_stride, N, K, _ptr(q), _ptr(s),
+                                               _stream(stream)))
+
+
+def moe_w4a16_fp8_matmul(a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K, stream=None):
+    _check(lib().moe_w4a16_fp8_matmul(_ptr(a), lda, _ptr(a_s), _ptr(b), ldb, _ptr(b_s), _ptr(add), _ptr(out),
+                                      out_type, M, N, K, _stream(stream)))
+
+
+def moe_w4a16_shared_expert_workspace_size(M: int, K: int, N: int) -> int:
+    return int(lib().moe_w4a16_shared_expert_workspace_size(M, K, N))
+
+
+def moe_w4a16_shared_expert(hidden, w1, w1_s, w2, w2_s, add, out, M, K, N, workspace, stream=None):
+    _check(lib().moe_w4a16_shared_expert(_ptr(hidden), _ptr(w1), _ptr(w1_s), _ptr(w2), _ptr(w2_s), _ptr(add),
+                                         _ptr(out), M, K, N, _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 class MoEW4A16:

@@ -1,0 +1,66 @@
+// Launchers of the operators around the routed experts: the scored router, the 8-bit
+// block quantisers and the 8-bit block-scaled product (each in its own translation
+// unit; argument checks are in ops_api.cu).
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "kernels.cuh"
+
+namespace moe {
+
+// Element types of the operators' floating inputs and outputs (as in the header).
+constexpr int kTypeF32 = 0;
+constexpr int kTypeBf16 = 1;
+
+constexpr int kScaleBlock = 128;  // values that share a scale along the reduction axis
+constexpr int kMaxGroups = 32;
+
+// Records `msg` as this thread's last error and returns `code` (api.cu).
+int report_error(int code, const char* msg);
+
+struct RouteScoredArgs {
+  const void* logits;  // [M, E], rows row_stride elements apart
+  int logits_type;
+  long long row_stride;
+  int M, E, topk;
+  int softmax;         // 1: softmax over E, 0: sigmoid
+  const float* bias;   // [E] added for the selection only, or null
+  int n_group, topk_group, group_top;
+  int renormalize;
+  float scale;
+  int32_t* ids;        // [M, topk]
+  float* weights;      // [M, topk]
+};
+cudaError_t launch_route_scored(const RouteScoredArgs& a, int num_sms, cudaStream_t stream);
+
+// Block quantiser: x [M, N] (or, for the SwiGLU form, rows [g | u] of 2N) -> q e4m3
+// [M, N], s fp32 [M, ceil(N / 128)].
+struct QuantArgs {
+  const void* x;
+  int x_type;
+  long long row_stride;
+  int M, N;
+  uint8_t* q;
+  float* s;
+};
+cudaError_t launch_quantize(const QuantArgs& a, bool swiglu, cudaStream_t stream);
+// The same over blocks of 128 rows x 128 columns: s [ceil(M / 128), ceil(N / 128)].
+cudaError_t launch_quantize_weight(const QuantArgs& a, cudaStream_t stream);
+
+// out[m, n] = sum_k a[m, k] a_s[m, k/128] b[n, k] b_s[n/128, k/128] (+ add[m, n])
+struct Fp8MatmulArgs {
+  const uint8_t* a;
+  long long lda;
+  const float* a_s;
+  const uint8_t* b;
+  long long ldb;
+  const float* b_s;
+  const uint16_t* add;  // bf16 [M, N] or null
+  void* out;            // [M, N]
+  int out_type;
+  int M, N, K;
+};
+cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
+
+}  // namespace moe
