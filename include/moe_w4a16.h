@@ -286,6 +286,12 @@ int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, cons
                          const float* b_s, const uint16_t* add, void* out, int out_type, int M, int N, int K,
                          void* stream);
 
+/* Status of the 8-bit products that ran on the current device since the last call of
+ * this function: 0, or MOE_W4A16_STATUS_TIMEOUT when a pipeline wait gave up (the output
+ * of that product is invalid). Clears it. Synchronises `stream`; products on other
+ * streams count once they have finished. */
+int moe_w4a16_fp8_status(int32_t* status, void* stream);
+
 /* Shared expert: the dense SwiGLU feed-forward that every token takes next to its
  * routed experts, with 8-bit block-scaled weights and activations:
  *   q1, s1 = quantize(hidden)              [g | u] = q1 s1 . (w1 w1_s)^T   (fp32)

@@ -60,7 +60,11 @@ struct Fp8MatmulArgs {
   void* out;            // [M, N]
   int out_type;
   int M, N, K;
+  bool weights_ready;   // `b` and `b_s` were written before the kernel in front of this one began
 };
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
+
+// Status word of the products (MOE_W4A16_STATUS_TIMEOUT when a wait gave up); clears it.
+cudaError_t fp8_status(int32_t* out, cudaStream_t stream);
 
 }  // namespace moe

@@ -129,8 +129,13 @@ int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, cons
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
-  Fp8MatmulArgs g{a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K};
+  Fp8MatmulArgs g{a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K, false};
   return done(launch_fp8_matmul(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4a16_fp8_status(int32_t* status, void* stream) {
+  if (!status) return bad("null pointer argument");
+  return done(fp8_status(status, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -184,10 +189,10 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
   float* gu = reinterpret_cast<float*>(ws + L.gu);
   e = launch_quantize(QuantArgs{hidden, kTypeBf16, K, M, K, q1, s1}, false, s);
   if (e == cudaSuccess)
-    e = launch_fp8_matmul(Fp8MatmulArgs{q1, K, s1, w1, K, w1_s, nullptr, gu, kTypeF32, M, 2 * N, K}, sms, s);
+    e = launch_fp8_matmul(Fp8MatmulArgs{q1, K, s1, w1, K, w1_s, nullptr, gu, kTypeF32, M, 2 * N, K, true}, sms, s);
   if (e == cudaSuccess) e = launch_quantize(QuantArgs{gu, kTypeF32, 2LL * N, M, N, q2, s2}, true, s);
   if (e == cudaSuccess)
-    e = launch_fp8_matmul(Fp8MatmulArgs{q2, N, s2, w2, N, w2_s, add, out, kTypeBf16, M, K, N}, sms, s);
+    e = launch_fp8_matmul(Fp8MatmulArgs{q2, N, s2, w2, N, w2_s, add, out, kTypeBf16, M, K, N, true}, sms, s);
   return done(e);
 }
 
