@@ -1,0 +1,366 @@
+// 8-bit block-scaled product of many rows: the batch as the MMA's rows.
+//
+// A pair of CTAs computes a tile of 256 rows x 256 features with cta_group::2 MMAs: each
+// CTA holds its 128 rows of `a` and half of `b`'s 256 in shared memory, and its rows'
+// fp32 sums in tensor memory. Scales differ from block to block of the reduction, so a
+// block of 128 elements (four MMAs) goes into a fresh accumulator; eight warps take it
+// out of tensor memory, scale it by a_s[row] b_s[feature block] and add it to the running
+// sums in registers (thread = one row, 128 features) while the MMAs of the next block
+// fill the other accumulator. Tensor memory holds exactly the two.
+//
+// What bounds it: the way out of tensor memory. A block's MMAs take 512 cycles, its sums
+// 450 of loads and additions plus about 550 from the last MMA to the first load and from
+// the release to the next MMA, with two accumulators in turn: 750 cycles a block. The
+// loads of 32 columns run one piece ahead of the sums (of 16 columns: +4%).
+// Measured and not kept: halves of an accumulator handed back one by one (up to +15%),
+// 16 summing warps (+12%), scales staged in shared memory by other warps (+10%), output
+// through shared memory and the copy engine (+5%), copies into L2 six blocks ahead (+2%).
+//
+// Warps: 0..7 sums and output, 8 copies (one lane of each CTA, both counting on the
+// leader's barriers), 9 the MMAs (the leader's), 10 and 11 idle. Persistent: a pair
+// takes every (number of pairs)-th tile. 8,192 x 4,096 x 7,168: 161 us, 2,990 TFLOP/s.
+#include <cuda_bf16.h>
+
+#include "fp8_tma.cuh"
+
+namespace moe {
+namespace {
+
+// 32 bytes at a time (32-byte aligned).
+struct Words8 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ void st_global_32b(void* p, const Words8& v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]), "r"(v.w[1]),
+               "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]), "r"(v.w[7])
+               : "memory");
+}
+__device__ __forceinline__ Words8 ld_global_32b(const void* p) {
+  Words8 v;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                 "=r"(v.w[7])
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+constexpr int kEpiWarps = 8, kWarpTma = 8, kWarpMma = 9;
+constexpr int kThreads = 12 * 32;  // (two warps idle: registers move between groups of four warps)
+constexpr int kEpiRegs = 232, kOtherRegs = 40;
+static_assert(256 * kEpiRegs + 128 * kOtherRegs <= kThreads * 168, "more registers than the launch's");
+constexpr int kTileM = 256, kTileN = 256;  // of a pair
+constexpr int kHalf = 128;                 // rows, and features, of a CTA
+constexpr int kSums = kTileN / 2;          // of a thread: one row, 128 features
+constexpr int kPiece = 32;                 // columns of a tensor-memory load
+constexpr int kOperand = 128 * 128;        // bytes of a box
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kStages = 5;
+constexpr int kBars = kStages * kStageBytes;
+constexpr int kSmem = kBars + 256 + 1024;
+static_assert(8 * (2 * kStages + 5) + 8 <= 256, "barriers");
+
+// acc (two sums) += v (two block sums) * s
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
+  asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(s2));
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+
+// Tile `t` of a grid of mt x nt: bands of 8 row tiles, features outer inside a band, so
+// that the pairs at work together share rows and features in L2.
+constexpr int kBand = 8;
+__device__ __forceinline__ void tile_at(int t, int mt, int nt, int* im, int* in) {
+  const int band = t / (kBand * nt);
+  const int rows = min(kBand, mt - band * kBand);
+  const int r = t - band * kBand * nt;
+  *im = band * kBand + r % rows;
+  *in = r / rows;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+
+// A thread's sums to the output. `vec`: rows are whole 32-byte pieces.
+__device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, int n, const uint64_t (&acc)[kSums / 2],
+                                          bool vec) {
+  const long long at = m * a.N + n;
+  if (a.out_type == kTypeBf16) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at;
+    if (vec) {
+#pragma unroll
+      for (int c = 0; c < kSums / 16; ++c) {
+        if (n + 16 * c >= a.N) break;
+        Words8 w, d;
+        if (a.add) d = ld_global_32b(a.add + at + 16 * c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float2 y = unpack2(acc[8 * c + i]);
+          if (a.add) y.x += __uint_as_float(d.w[i] << 16), y.y += __uint_as_float(d.w[i] & 0xFFFF0000u);
+          w.w[i] = bf16x2(y.x, y.y);
+        }
+        st_global_32b(out + 16 * c, w);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kSums / 2; ++i) {
+      const float2 y = unpack2(acc[i]);
+      const float v[2] = {y.x, y.y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = 2 * i + k;
+        if (n + j < a.N)
+          out[j] = __float2bfloat16_rn(v[k] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at + j]) << 16) : 0.f));
+      }
+    }
+  } else {
+    float* out = static_cast<float*>(a.out) + at;
+    if (vec && !a.add) {
+#pragma unroll
+      for (int c = 0; c < kSums / 8; ++c) {
+        if (n + 8 * c >= a.N) break;
+        Words8 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = unpack2(acc[4 * c + i]);
+          w.w[2 * i] = __float_as_uint(y.x), w.w[2 * i + 1] = __float_as_uint(y.y);
+        }
+        st_global_32b(out + 8 * c, w);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kSums / 2; ++i) {
+      const float2 y = unpack2(acc[i]);
+      const float v[2] = {y.x, y.y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int j = 2 * i + k;
+        if (n + j < a.N) out[j] = v[k] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at + j]) << 16) : 0.f);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_matmul_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                           const __grid_constant__ Fp8MatmulArgs a, int mt, int nt, bool vec, int32_t* status) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
+  auto full = [&](int i) { return base + kBars + 8 * i; };                    // leader's: both CTAs' copies
+  auto empty = [&](int i) { return base + kBars + 8 * (kStages + i); };       // each CTA's
+  auto tfull = [&](int i) { return base + kBars + 8 * (2 * kStages + i); };   // each CTA's
+  auto tempty = [&](int i) { return base + kBars + 8 * (2 * kStages + 2 + i); };  // leader's: both CTAs' warps
+  const uint32_t drain = base + kBars + 8 * (2 * kStages + 4);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kBars + 8 * (2 * kStages + 5));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
+  const int tiles = mt * nt;
+  const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const uint32_t limit = kWaitLimitKCyclesDefault;
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_map(&amap);
+    tma_prefetch_map(&bmap);
+    for (int i = 0; i < kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), 2 * kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp >= kEpiWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kWarpTma && lane == 0) {
+      const uint64_t keep = l2_policy_evict_last();
+      pdl_wait();
+      int st = 0;
+      uint32_t ph = 0;
+      int issued = 0;  // (only its last kStages and their phases matter: kept small)
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        int im, in;
+        tile_at(t, mt, nt, &im, &in);
+        const int m0 = im * kTileM + rank * kHalf, n0 = in * kTileN + rank * kHalf;
+        for (int kb = 0; kb < Kb; ++kb) {
+          if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, status, kStatusTimeout, limit)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * kStageBytes);
+          const uint32_t bar = map_rank(full(st), 0);
+          tma_load_2d_pair(base + st * kStageBytes, &amap, kb * 128, m0, bar, keep);
+          tma_load_2d_pair(base + st * kStageBytes + kOperand, &bmap, kb * 128, n0, bar, keep);
+          if (++issued == 4 * kStages) issued = 2 * kStages;
+          if (++st == kStages) st = 0, ph ^= 1u;
+        }
+      }
+      // shared memory is released only after the last copies have landed, whoever gave up
+      if (rank == 0)
+        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+          mbar_drain(full(i % kStages), (i / kStages) & 1);
+      if (*abort_flag) {  // (the other CTA's copies count on the leader's barriers: give them 2 ms)
+        const long long c0 = clock64();
+        while (clock64() - c0 < 4000000) {
+        }
+      }
+    }
+    if (warp == kWarpMma && rank == 0) {
+      const uint32_t idesc = idesc_e4m3_f32(kTileM, kTileN);
+      const bool leader = elect_one();
+      int st = 0, ac = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        for (int kb = 0; kb < Kb; ++kb) {
+          ok = __all_sync(0xffffffffu, mbar_wait(full(st), ph, abort_flag, status, kStatusTimeout, limit) &&
+                                           mbar_wait(tempty(ac), aph ^ 1u, abort_flag, status, kStatusTimeout, limit));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t ad = sw128_kmajor_desc(base + st * kStageBytes);
+            const uint64_t bd = sw128_kmajor_desc(base + st * kStageBytes + kOperand);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // (32 bytes on: 2 descriptor units)
+              tc_mma_e4m3_pair(tmem + ac * kTileN, ad + 2 * i, bd + 2 * i, idesc, i > 0);
+            tc_commit_pair(empty(st));
+            tc_commit_pair(tfull(ac));
+          }
+          __syncwarp();
+          if (++st == kStages) st = 0, ph ^= 1u;
+          if (++ac == 2) ac = 0, aph ^= 1u;
+        }
+      }
+      if (leader) {  // tensor memory is freed only after the last MMAs, whoever gave up
+        tc_commit_pair(drain);
+        mbar_drain(drain, 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    const int half = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t src0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kSums;
+    const uint32_t give0 = map_rank(tempty(0), 0);
+    const int nb = (a.N + kScaleBlock - 1) / kScaleBlock;
+    int ac = 0;
+    uint32_t aph = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      int im, in;
+      tile_at(t, mt, nt, &im, &in);
+      const int m = im * kTileM + rank * kHalf + row;  // (below 2^31: M is at most 2^30)
+      const int n = in * kTileN + half * kSums;
+      const bool live = m < a.M;
+      // (rows and features behind the end read the scales of the first row, the last block)
+      const float* as = a.a_s + static_cast<long long>(live ? m : 0) * Kb;
+      const float* bs = a.b_s + static_cast<long long>(min(n / kScaleBlock, nb - 1)) * Kb;
+      float sa = *as, sb = *bs;
+      uint64_t acc[kSums / 2];
+#pragma unroll
+      for (int i = 0; i < kSums / 2; ++i) acc[i] = 0;
+      for (int kb = 0; kb < Kb; ++kb) {
+        const uint64_t s2 = pack2(sa * sb, sa * sb);
+        if (kb + 1 < Kb) sa = *++as, sb = *++bs;
+        ok = __all_sync(0xffffffffu, mbar_wait(tfull(ac), aph, abort_flag, status, kStatusTimeout, limit));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = src0 + ac * kTileN;
+        // the loads of a piece overlap the sums of the one before it
+        uint32_t v[2][kPiece];
+        tmem_ld32(src, v[0]);
+#pragma unroll
+        for (int c = 0; c < kSums / kPiece; ++c) {
+          tmem_ld_wait();
+          if (c + 1 < kSums / kPiece) {
+            tmem_ld32(src + kPiece * (c + 1), v[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(give0 + 8 * ac);
+          }
+#pragma unroll
+          for (int i = 0; i < kPiece / 2; ++i)
+            fma2(acc[c * (kPiece / 2) + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], s2);
+        }
+        if (++ac == 2) ac = 0, aph ^= 1u;
+      }
+      if (ok && live) store_row(a, m, n, acc, vec);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == kWarpMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
+  // pairs that can run at once (SMs that have a partner), asked once
+  static int pairs = 0;
+  if (pairs == 0) {
+    cudaError_t e = cudaFuncSetAttribute(fp8_matmul_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms / 2));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_many_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    pairs = n < 1 ? 1 : (n > num_sms / 2 ? num_sms / 2 : n);
+  }
+  CUtensorMap amap, bmap;
+  if (!make_byte_map(&amap, a.a, a.M, a.K, a.lda, kHalf) || !make_byte_map(&bmap, a.b, a.N, a.K, a.ldb, kHalf))
+    return cudaErrorInvalidValue;
+  const int mt = (a.M + kTileM - 1) / kTileM, nt = (a.N + kTileN - 1) / kTileN;
+  const long long tiles = static_cast<long long>(mt) * nt;
+  if (tiles > (1 << 30)) return cudaErrorInvalidValue;  // (7e13 outputs)
+  const int elems = a.out_type == kTypeBf16 ? 16 : 8;  // of a 32-byte piece
+  const bool vec = a.N % elems == 0 && (reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add)) % 32 == 0;
+  const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? tiles : pairs);
+  return launch_cluster(fp8_matmul_many_kernel, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt, vec,
+                        status);
+}
+
+}  // namespace moe

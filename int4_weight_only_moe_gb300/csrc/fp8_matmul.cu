@@ -127,7 +127,7 @@ __host__ __device__ constexpr int few_accs() { return kChunks <= 4 ? 4 : 2; }
 template <int kChunks>
 __global__ void __launch_bounds__(kFewThreads)
     fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                          const __grid_constant__ Fp8MatmulArgs a, int bt, int split) {
+                          const __grid_constant__ Fp8MatmulArgs a, int bt, int split, int32_t* status) {
   constexpr FewLayout L = few_layout<kChunks>();
   constexpr int kAccs = few_accs<kChunks>();
   constexpr int kCols = kAccs * 16 * kChunks < 32 ? 32 : kAccs * 16 * kChunks;
@@ -155,7 +155,6 @@ __global__ void __launch_bounds__(kFewThreads)
   const int kb1 = static_cast<int>(static_cast<long long>(Kb) * (rank + 1) / split);
   const uint32_t bytes = kWTile + bt * 128;
   const uint32_t limit = kWaitLimitKCyclesDefault;
-  int32_t* status = &g_fp8_status;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&wmap);
@@ -323,29 +322,8 @@ __global__ void __launch_bounds__(kFewThreads)
 
 // ---------------------------------------------------------------- host
 
-// Cluster launch with programmatic dependence.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                           int cluster, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
 template <int kChunks>
-cudaError_t launch_few(const Fp8MatmulArgs& a, int bt, int split, cudaStream_t stream) {
+cudaError_t launch_few(const Fp8MatmulArgs& a, int bt, int split, int32_t* status, cudaStream_t stream) {
   constexpr FewLayout L = few_layout<kChunks>();
   static cudaError_t set = cudaFuncSetAttribute(fp8_matmul_few_kernel<kChunks>,
                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
@@ -355,7 +333,7 @@ cudaError_t launch_few(const Fp8MatmulArgs& a, int bt, int split, cudaStream_t s
     return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * split), static_cast<unsigned>((a.M + bt - 1) / bt));
   return launch_cluster(fp8_matmul_few_kernel<kChunks>, grid, dim3(kFewThreads), L.total, stream, split, wmap, xmap, a,
-                        bt, split);
+                        bt, split, status);
 }
 
 }  // namespace
@@ -388,10 +366,13 @@ bool tma_ok(const Fp8MatmulArgs& a) {
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream) {
-  if (!tma_ok(a) || a.M > (1 << 22)) {
+  if (!tma_ok(a)) {
     const dim3 grid((a.M + kT - 1) / kT, (a.N + kT - 1) / kT);
     return launch_k(fp8_matmul_plain_kernel, grid, dim3(256), 0, stream, true, a);
   }
+  int32_t* status = fp8_status_word();
+  if (!status) return cudaErrorInvalidSymbol;
+  if (a.M > 128) return launch_fp8_many(a, status, num_sms, stream);
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   // tokens a tile: the batch in equal parts of at most 128, in steps of 16
   const long long parts = (static_cast<long long>(a.M) + 127) / 128;
@@ -400,16 +381,29 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t 
   const long long slots = static_cast<long long>(num_sms) * (bt <= 32 ? 2 : 1);
   int split = 1;
   while (split < 8 && tiles * split * 2 <= slots && Kb >= 2 * split * 2) split *= 2;
-  if (bt <= 16) return launch_few<1>(a, bt, split, stream);
-  if (bt <= 32) return launch_few<2>(a, bt, split, stream);
-  if (bt <= 64) return launch_few<4>(a, bt, split, stream);
-  return launch_few<8>(a, bt, split, stream);
+  if (bt <= 16) return launch_few<1>(a, bt, split, status, stream);
+  if (bt <= 32) return launch_few<2>(a, bt, split, status, stream);
+  if (bt <= 64) return launch_few<4>(a, bt, split, status, stream);
+  return launch_few<8>(a, bt, split, status, stream);
+}
+
+int32_t* fp8_status_word() {
+  // (one context per device in a process; asked once per device)
+  static int32_t* cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  if (dev >= 0 && dev < 64 && cached[dev]) return cached[dev];
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_fp8_status) != cudaSuccess) return nullptr;
+  if (dev >= 0 && dev < 64) cached[dev] = static_cast<int32_t*>(p);
+  return static_cast<int32_t*>(p);
 }
 
 cudaError_t fp8_status(int32_t* out, cudaStream_t stream) {
-  const int32_t zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_fp8_status, sizeof(zero), 0, cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_fp8_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream);
+  int32_t* p = fp8_status_word();
+  if (!p) return cudaErrorInvalidSymbol;
+  cudaError_t e = cudaMemcpyAsync(out, p, sizeof(*p), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, sizeof(*p), stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   return e;
 }
