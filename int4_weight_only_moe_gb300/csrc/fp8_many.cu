@@ -94,13 +94,14 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 
-// A thread's sums to the output. `vec`: rows are whole 32-byte pieces.
+// A thread's sums to the output, in pieces of `piece` bytes that are whole and aligned:
+// 32, 8, or 0 for value by value.
 __device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, int n, const uint64_t (&acc)[kSums / 2],
-                                          bool vec) {
+                                          int piece) {
   const long long at = m * a.N + n;
   if (a.out_type == kTypeBf16) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at;
-    if (vec) {
+    if (piece == 32) {
 #pragma unroll
       for (int c = 0; c < kSums / 16; ++c) {
         if (n + 16 * c >= a.N) break;
@@ -116,49 +117,54 @@ __device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, i
       }
       return;
     }
+    if (piece == 8) {
 #pragma unroll
-    for (int i = 0; i < kSums / 2; ++i) {
-      const float2 y = unpack2(acc[i]);
-      const float v[2] = {y.x, y.y};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = 2 * i + k;
-        if (n + j < a.N)
-          out[j] = __float2bfloat16_rn(v[k] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at + j]) << 16) : 0.f));
-      }
-    }
-  } else {
-    float* out = static_cast<float*>(a.out) + at;
-    if (vec && !a.add) {
-#pragma unroll
-      for (int c = 0; c < kSums / 8; ++c) {
-        if (n + 8 * c >= a.N) break;
-        Words8 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 y = unpack2(acc[4 * c + i]);
-          w.w[2 * i] = __float_as_uint(y.x), w.w[2 * i + 1] = __float_as_uint(y.y);
-        }
-        st_global_32b(out + 8 * c, w);
+      for (int c = 0; c < kSums / 4; ++c) {
+        if (n + 4 * c >= a.N) break;
+        uint2 d = make_uint2(0u, 0u);  // the addend (0 adds nothing)
+        if (a.add) d = *reinterpret_cast<const uint2*>(a.add + at + 4 * c);
+        const float2 y = unpack2(acc[2 * c]), z = unpack2(acc[2 * c + 1]);
+        d.x = bf16x2(y.x + __uint_as_float(d.x << 16), y.y + __uint_as_float(d.x & 0xFFFF0000u));
+        d.y = bf16x2(z.x + __uint_as_float(d.y << 16), z.y + __uint_as_float(d.y & 0xFFFF0000u));
+        *reinterpret_cast<uint2*>(out + 4 * c) = d;
       }
       return;
     }
+  } else if (piece == 32 && !a.add) {
+    float* out = static_cast<float*>(a.out) + at;
 #pragma unroll
-    for (int i = 0; i < kSums / 2; ++i) {
-      const float2 y = unpack2(acc[i]);
-      const float v[2] = {y.x, y.y};
+    for (int c = 0; c < kSums / 8; ++c) {
+      if (n + 8 * c >= a.N) break;
+      Words8 w;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int j = 2 * i + k;
-        if (n + j < a.N) out[j] = v[k] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at + j]) << 16) : 0.f);
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = unpack2(acc[4 * c + i]);
+        w.w[2 * i] = __float_as_uint(y.x), w.w[2 * i + 1] = __float_as_uint(y.y);
       }
+      st_global_32b(out + 8 * c, w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kSums / 2; ++i) {
+    const float2 y = unpack2(acc[i]);
+    const float v[2] = {y.x, y.y};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int j = 2 * i + k;
+      if (n + j >= a.N) continue;
+      const float w = v[k] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at + j]) << 16) : 0.f);
+      if (a.out_type == kTypeBf16)
+        static_cast<__nv_bfloat16*>(a.out)[at + j] = __float2bfloat16_rn(w);
+      else
+        static_cast<float*>(a.out)[at + j] = w;
     }
   }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                           const __grid_constant__ Fp8MatmulArgs a, int mt, int nt, bool vec, int32_t* status) {
+                           const __grid_constant__ Fp8MatmulArgs a, int mt, int nt, int piece, int32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (++ac == 2) ac = 0, aph ^= 1u;
       }
-      if (ok && live) store_row(a, m, n, acc, vec);
+      if (ok && live) store_row(a, m, n, acc, piece);
     }
   }
   __syncwarp();
@@ -356,10 +362,12 @@ cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms
   const int mt = (a.M + kTileM - 1) / kTileM, nt = (a.N + kTileN - 1) / kTileN;
   const long long tiles = static_cast<long long>(mt) * nt;
   if (tiles > (1 << 30)) return cudaErrorInvalidValue;  // (7e13 outputs)
-  const int elems = a.out_type == kTypeBf16 ? 16 : 8;  // of a 32-byte piece
-  const bool vec = a.N % elems == 0 && (reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add)) % 32 == 0;
+  const uintptr_t where = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add);
+  const int piece = a.N % (a.out_type == kTypeBf16 ? 16 : 8) == 0 && where % 32 == 0 ? 32
+                    : a.N % 4 == 0 && where % 8 == 0                                ? 8
+                                                                                    : 0;
   const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? tiles : pairs);
-  return launch_cluster(fp8_matmul_many_kernel, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt, vec,
+  return launch_cluster(fp8_matmul_many_kernel, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt, piece,
                         status);
 }
 

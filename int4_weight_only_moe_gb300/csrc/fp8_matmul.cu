@@ -85,89 +85,132 @@ __global__ void __launch_bounds__(256) fp8_matmul_plain_kernel(Fp8MatmulArgs a) 
 
 // ---------------------------------------------------------------- few rows
 //
-// A batch of few rows reads every weight once and does little with it: the weights are
-// the MMA's 128 rows (M) and the batch its columns (N = 16 .. 128), so one token costs
-// 16 columns, not 128 rows. A tile's reduction is split over the CTAs of a cluster, so
-// that every SM streams weights; the fp32 partial sums meet in distributed shared memory
-// and are added in the order of the ranks (the same result every time).
+// A batch of few rows reads every weight once and does little with it. Up to 32 rows the
+// weights are the MMA's 128 rows (M) and the batch its columns (N = 16 or 32), so one
+// token costs 16 columns, not 128 rows, and a thread sums one weight row over the batch.
+// From 33 rows on the batch is the MMA's 128 rows and 128 weights its columns: a thread
+// sums one batch row, whose scale is one number a block (with the weights as rows it has
+// one for each column, and 128 columns took 850 cycles a block). A tile's reduction is
+// split over the CTAs of a cluster, so that every SM streams weights; the fp32 partial
+// sums meet in distributed shared memory and are added in the order of the ranks (the
+// same result every time).
 //
-// Warps of a CTA: 0 copies (one lane; a stage is 128 x 128 weight bytes and the batch's
-// 128 bytes per row), 1 issues the MMAs (four of 32 reduction elements for a block) into
-// one of kAccs accumulators, 2..5 take the block sum out of tensor memory, scale it and
-// add it to the running sum in registers (thread = weight row).
-constexpr int kFewThreads = 6 * 32;
-constexpr int kFewEpi = 128;
+// Warps of a CTA: the first four (eight for 128 columns, half of the columns each) take
+// the block sums out of tensor memory, scale them and add them to the running sums in
+// registers; then one that copies (one lane; a stage is 128 x 128 weight bytes and the
+// batch's 128 bytes per row) and one that issues the MMAs (four of 32 reduction elements
+// for a block) into four accumulators in turn.
 constexpr int kWTile = 128 * 128;  // bytes of a weight box
 constexpr int kScaleRun = 32;      // blocks whose scales are staged at a time
+constexpr int kMaxStages = 10;
 
 __device__ int32_t g_fp8_status;
 
-struct FewLayout {  // shared memory
-  int stages, stage_bytes, scales, bars, total;
+template <int kRows>  // batch rows of a tile: 16, 32 or 128
+struct Few {
+  static constexpr bool kBatchIsM = kRows == 128;
+  static constexpr int kCols = kRows;  // of the MMA: the batch, or 128 weights
+  static constexpr int kEpiWarps = kBatchIsM ? 8 : 4;
+  static constexpr int kEpiThreads = kEpiWarps * 32;
+  static constexpr int kThreads = kEpiThreads + 64;
+  static constexpr int kMine = kCols / (kEpiWarps / 4);  // columns of a thread
+  static constexpr int kPiece = kMine < 32 ? kMine : 32;
+  static constexpr int kAccs = 4;
+  static constexpr int kTmem = kAccs * kCols;
+  static constexpr int kStageBytes = kWTile + kRows * 128;
+  // two CTAs to an SM up to 32 columns
+  static constexpr int kRoom = (kBatchIsM ? 226 : 113) * 1024;
+  static constexpr int kScaleRow = kRows + 4;  // (padded: the staging's stores spread over the banks)
+  static constexpr int kFixed = kScaleRun * kScaleRow * 4 + 512 + 1024;  // (1,024: up to the swizzle atom)
+  static constexpr int kFit = (kRoom - kFixed) / kStageBytes;
+  static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
+  static constexpr int kScales = kStages * kStageBytes;
+  static constexpr int kBars = kScales + kScaleRun * kScaleRow * 4;
+  static constexpr int kSmem = kBars + 512 + 1024;
+  static_assert(kStages >= 2 && 8 * (2 * kStages + 2 * kAccs + 1) + 8 <= 512, "barriers");
+  static_assert(kStages * kStageBytes >= kRows * 128 * 4, "the partial sums fit the stages");
 };
-constexpr int kMaxStages = 10;
-template <int kChunks>
-__host__ __device__ constexpr FewLayout few_layout() {
-  FewLayout L{};
-  const int bt = 16 * kChunks;
-  L.stage_bytes = kWTile + bt * 128;
-  // two CTAs to an SM while the registers allow it
-  const int room = (kChunks <= 2 ? 113 : 226) * 1024 - 1024;
-  const int fixed = kScaleRun * bt * 4 + 512;
-  L.stages = (room - fixed) / L.stage_bytes;
-  if (L.stages > kMaxStages) L.stages = kMaxStages;
-  L.scales = L.stages * L.stage_bytes;
-  L.bars = L.scales + kScaleRun * bt * 4;
-  L.total = L.bars + 512 + 1024;  // (1,024: the base is rounded up to the swizzle atom)
-  return L;
-}
-template <int kChunks>
-__host__ __device__ constexpr int few_accs() { return kChunks <= 4 ? 4 : 2; }
 
-template <int kChunks>
-__global__ void __launch_bounds__(kFewThreads)
+__device__ __forceinline__ void tmem_piece(uint32_t src, uint32_t (&v)[16]) { tmem_ld16(src, v); }
+__device__ __forceinline__ void tmem_piece(uint32_t src, uint32_t (&v)[32]) { tmem_ld32(src, v); }
+
+// Byte offset of weights 4 c .. 4 c + 3 in row j of the partial sums.
+__device__ __forceinline__ uint32_t part_at(int j, int c) { return j * 512 + ((c ^ (j & 7)) << 4); }
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Four consecutive outputs; `vec`: whole and aligned for one access.
+__device__ __forceinline__ void store_out4(const Fp8MatmulArgs& a, long long m, int n, float4 y, bool vec) {
+  const long long at = m * a.N + n;
+  if (!vec) {
+    const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < a.N) store_out(a, at + i, v[i]);
+    return;
+  }
+  if (n >= a.N) return;
+  if (a.add) {
+    const uint2 d = *reinterpret_cast<const uint2*>(a.add + at);
+    y.x += __uint_as_float(d.x << 16), y.y += __uint_as_float(d.x & 0xFFFF0000u);
+    y.z += __uint_as_float(d.y << 16), y.w += __uint_as_float(d.y & 0xFFFF0000u);
+  }
+  if (a.out_type == kTypeF32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+template <int kRows>
+__global__ void __launch_bounds__(Few<kRows>::kThreads)
     fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                          const __grid_constant__ Fp8MatmulArgs a, int bt, int split, int32_t* status) {
-  constexpr FewLayout L = few_layout<kChunks>();
-  constexpr int kAccs = few_accs<kChunks>();
-  constexpr int kCols = kAccs * 16 * kChunks < 32 ? 32 : kAccs * 16 * kChunks;
-  static_assert(L.stages >= 2 && 8 * (2 * L.stages + 2 * kAccs + 1) + 8 <= 512, "shared memory layout");
-  // the reduction reuses the stages
-  static_assert(L.stages * L.stage_bytes >= 16 * kChunks * 128 * 4, "partial sums fit the stages");
+                          const __grid_constant__ Fp8MatmulArgs a, int split, bool vec, int32_t* status) {
+  using L = Few<kRows>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
-  float* scales = reinterpret_cast<float*>(gbase + L.scales);  // [kScaleRun][bt max]
-  auto full = [&](int i) { return base + L.bars + 8 * i; };
-  auto empty = [&](int i) { return base + L.bars + 8 * (L.stages + i); };
-  auto tfull = [&](int i) { return base + L.bars + 8 * (2 * L.stages + i); };
-  auto tempty = [&](int i) { return base + L.bars + 8 * (2 * L.stages + kAccs + i); };
-  const uint32_t drain = base + L.bars + 8 * (2 * L.stages + 2 * kAccs);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L.bars + 8 * (2 * L.stages + 2 * kAccs + 1));
+  float* scales = reinterpret_cast<float*>(gbase + L::kScales);  // [kScaleRun][kScaleRow]
+  auto full = [&](int i) { return base + L::kBars + 8 * i; };
+  auto empty = [&](int i) { return base + L::kBars + 8 * (L::kStages + i); };
+  auto tfull = [&](int i) { return base + L::kBars + 8 * (2 * L::kStages + i); };
+  auto tempty = [&](int i) { return base + L::kBars + 8 * (2 * L::kStages + L::kAccs + i); };
+  const uint32_t drain = base + L::kBars + 8 * (2 * L::kStages + 2 * L::kAccs);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kBars + 8 * (2 * L::kStages + 2 * L::kAccs + 1));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  constexpr int kWarpTma = L::kEpiWarps, kWarpMma = L::kEpiWarps + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int n0 = static_cast<int>(blockIdx.x / split) * 128;
-  const long long m0 = static_cast<long long>(blockIdx.y) * bt;
+  const long long m0 = static_cast<long long>(blockIdx.y) * kRows;
+  const int rows = static_cast<int>(a.M - m0 < kRows ? a.M - m0 : kRows);
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   const int kb0 = static_cast<int>(static_cast<long long>(Kb) * rank / split);
   const int kb1 = static_cast<int>(static_cast<long long>(Kb) * (rank + 1) / split);
-  const uint32_t bytes = kWTile + bt * 128;
+  constexpr uint32_t bytes = L::kStageBytes;
   const uint32_t limit = kWaitLimitKCyclesDefault;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&wmap);
     tma_prefetch_map(&xmap);
-    for (int i = 0; i < L.stages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
-    for (int i = 0; i < kAccs; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), 4);
+    for (int i = 0; i < L::kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
+    for (int i = 0; i < L::kAccs; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), L::kEpiWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == kWarpMma) {
     __syncwarp();
-    tmem_alloc(smem_u32(tmem_slot), kCols);
+    tmem_alloc(smem_u32(tmem_slot), L::kTmem);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -175,15 +218,15 @@ __global__ void __launch_bounds__(kFewThreads)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
+  if (warp == kWarpTma) {
     if (lane == 0) {
       const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
       // weights that no preceding kernel of this call writes may stream ahead of the wait
       int ahead = 0;
       if (a.weights_ready)
-        for (; ahead < L.stages && kb0 + ahead < kb1; ++ahead) {
+        for (; ahead < L::kStages && kb0 + ahead < kb1; ++ahead) {
           mbar_arrive_expect_tx(full(ahead), bytes);
-          tma_load_2d(base + ahead * L.stage_bytes, &wmap, (kb0 + ahead) * 128, n0, full(ahead), once);
+          tma_load_2d(base + ahead * L::kStageBytes, &wmap, (kb0 + ahead) * 128, n0, full(ahead), once);
         }
       pdl_wait();
       int st = 0, it = 0;
@@ -192,16 +235,17 @@ __global__ void __launch_bounds__(kFewThreads)
         if (it >= ahead) {
           if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, status, kStatusTimeout, limit)) break;
           mbar_arrive_expect_tx(full(st), bytes);
-          tma_load_2d(base + st * L.stage_bytes, &wmap, kb * 128, n0, full(st), once);
+          tma_load_2d(base + st * L::kStageBytes, &wmap, kb * 128, n0, full(st), once);
         }
-        tma_load_2d(base + st * L.stage_bytes + kWTile, &xmap, kb * 128, static_cast<int>(m0), full(st), keep);
-        if (++st == L.stages) st = 0, ph ^= 1u;
+        tma_load_2d(base + st * L::kStageBytes + kWTile, &xmap, kb * 128, static_cast<int>(m0), full(st), keep);
+        if (++st == L::kStages) st = 0, ph ^= 1u;
       }
       // shared memory is released only after the last copies have landed, whoever gave up
-      for (int i = it > L.stages ? it - L.stages : 0; i < it; ++i) mbar_drain(full(i % L.stages), (i / L.stages) & 1);
+      for (int i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
+        mbar_drain(full(i % L::kStages), (i / L::kStages) & 1);
     }
-  } else if (warp == 1) {
-    const uint32_t idesc = idesc_e4m3_f32(128, bt);
+  } else if (warp == kWarpMma) {
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, L::kCols);
     const bool leader = elect_one();
     int st = 0, ac = 0;
     uint32_t ph = 0, aph = 0;
@@ -212,18 +256,18 @@ __global__ void __launch_bounds__(kFewThreads)
         break;
       tc_fence_after();
       if (leader) {
-        const uint64_t wd = sw128_kmajor_desc(base + st * L.stage_bytes);
-        const uint64_t xd = sw128_kmajor_desc(base + st * L.stage_bytes + kWTile);
-        const uint32_t d = tmem + ac * 16 * kChunks;
+        const uint64_t wd = sw128_kmajor_desc(base + st * L::kStageBytes);
+        const uint64_t xd = sw128_kmajor_desc(base + st * L::kStageBytes + kWTile);
+        const uint32_t d = tmem + ac * L::kCols;
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // (32 bytes on: 2 descriptor units)
-          tc_mma_e4m3(d, wd + 2 * i, xd + 2 * i, idesc, i > 0);
+          tc_mma_e4m3(d, (L::kBatchIsM ? xd : wd) + 2 * i, (L::kBatchIsM ? wd : xd) + 2 * i, idesc, i > 0);
         tc_commit(empty(st));
         tc_commit(tfull(ac));
       }
       __syncwarp();
-      if (++st == L.stages) st = 0, ph ^= 1u;
-      if (++ac == kAccs) ac = 0, aph ^= 1u;
+      if (++st == L::kStages) st = 0, ph ^= 1u;
+      if (++ac == L::kAccs) ac = 0, aph ^= 1u;
     }
     if (leader) {  // tensor memory is freed only after the last MMAs, whoever gave up
       tc_commit(drain);
@@ -232,16 +276,13 @@ __global__ void __launch_bounds__(kFewThreads)
     __syncwarp();
   } else {
     pdl_wait();
-    if (warp == 2 && lane == 0) pdl_launch_dependents();
-    const int tid = threadIdx.x - 64;
+    if (threadIdx.x == 0) pdl_launch_dependents();
     const int row = (warp & 3) * 32 + lane;
-    const int n = n0 + row;
-    const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int rows = static_cast<int>(a.M - m0 < bt ? a.M - m0 : bt);
-    const int chunks = bt / 16;
-    float acc[16 * kChunks];
+    const int c0 = (warp >> 2) * L::kMine;  // first column
+    const uint32_t src0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
+    float acc[L::kMine];
 #pragma unroll
-    for (int j = 0; j < 16 * kChunks; ++j) acc[j] = 0.f;
+    for (int j = 0; j < L::kMine; ++j) acc[j] = 0.f;
     int ac = 0;
     uint32_t aph = 0;
     bool ok = true;  // (a warp that gave up goes on without sums: the others meet it at the barrier)
@@ -249,91 +290,103 @@ __global__ void __launch_bounds__(kFewThreads)
       const int at = (kb - kb0) % kScaleRun;
       if (at == 0) {  // both scales of the next blocks, multiplied
         const int run = min(kScaleRun, kb1 - kb);
-        named_bar_sync(1, kFewEpi);
-        for (int i = tid; i < run * bt; i += kFewEpi) {
-          const int j = i / run, k = i % run;
-          scales[k * bt + j] = j < rows ? a.a_s[(m0 + j) * Kb + kb + k] *
-                                              a.b_s[static_cast<long long>(n0 / kScaleBlock) * Kb + kb + k]
-                                        : 0.f;
+        named_bar_sync(1, L::kEpiThreads);
+        if (lane < run) {  // (lanes along the blocks: whole lines of a_s)
+          const float sb = a.b_s[static_cast<long long>(n0 / kScaleBlock) * Kb + kb + lane];
+#pragma unroll 4
+          for (int j = warp; j < kRows; j += L::kEpiWarps)
+            scales[lane * L::kScaleRow + j] = j < rows ? a.a_s[(m0 + j) * Kb + kb + lane] * sb : 0.f;
         }
-        named_bar_sync(1, kFewEpi);
+        named_bar_sync(1, L::kEpiThreads);
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(ac), aph, abort_flag, status, kStatusTimeout, limit));
       if (!ok) continue;
       tc_fence_after();
+      const float mine = scales[at * L::kScaleRow + (L::kBatchIsM ? row : 0)];
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        if (c >= chunks) break;
-        uint32_t v[16];
-        tmem_ld16(tmem + t_lane + ac * 16 * kChunks + 16 * c, v);
+      for (int c = 0; c < L::kMine / L::kPiece; ++c) {
+        uint32_t v[L::kPiece];
+        tmem_piece(src0 + ac * L::kCols + c * L::kPiece, v);
+        const float4* sc = reinterpret_cast<const float4*>(scales + at * L::kScaleRow + c * L::kPiece);
         tmem_ld_wait();
-        const float4* sc = reinterpret_cast<const float4*>(scales + at * bt + 16 * c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 s4 = sc[q];
-          acc[16 * c + 4 * q + 0] = fmaf(__uint_as_float(v[4 * q + 0]), s4.x, acc[16 * c + 4 * q + 0]);
-          acc[16 * c + 4 * q + 1] = fmaf(__uint_as_float(v[4 * q + 1]), s4.y, acc[16 * c + 4 * q + 1]);
-          acc[16 * c + 4 * q + 2] = fmaf(__uint_as_float(v[4 * q + 2]), s4.z, acc[16 * c + 4 * q + 2]);
-          acc[16 * c + 4 * q + 3] = fmaf(__uint_as_float(v[4 * q + 3]), s4.w, acc[16 * c + 4 * q + 3]);
+        for (int q = 0; q < L::kPiece / 4; ++q) {
+          const float4 s4 = L::kBatchIsM ? make_float4(mine, mine, mine, mine) : sc[q];
+          float* x = acc + c * L::kPiece + 4 * q;
+          x[0] = fmaf(__uint_as_float(v[4 * q + 0]), s4.x, x[0]);
+          x[1] = fmaf(__uint_as_float(v[4 * q + 1]), s4.y, x[1]);
+          x[2] = fmaf(__uint_as_float(v[4 * q + 2]), s4.z, x[2]);
+          x[3] = fmaf(__uint_as_float(v[4 * q + 3]), s4.w, x[3]);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty(ac));
-      if (++ac == kAccs) ac = 0, aph ^= 1u;
+      if (++ac == L::kAccs) ac = 0, aph ^= 1u;
     }
-    if (split == 1) {
-      if (n < a.N)
+    // sums [batch row][128 weights], 16-byte pieces swizzled by the row (every MMA is done --
+    // the last accumulator was waited for -- so the stages are free)
+    if (L::kBatchIsM) {
 #pragma unroll
-        for (int j = 0; j < 16 * kChunks; ++j)
-          if (j < rows) store_out(a, (m0 + j) * a.N + n, acc[j]);
+      for (int i = 0; i < L::kMine; i += 4)
+        *reinterpret_cast<float4*>(gbase + part_at(row, (c0 + i) / 4)) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
     } else {
-      // (every MMA is done -- the last accumulator was waited for -- so the stages are free)
-      float* part = reinterpret_cast<float*>(gbase);
 #pragma unroll
-      for (int j = 0; j < 16 * kChunks; ++j)
-        if (j < rows) part[j * 128 + row] = acc[j];
+      for (int j = 0; j < L::kMine; ++j)
+        if (j < rows) *reinterpret_cast<float*>(gbase + part_at(j, row / 4) + (row & 3) * 4) = acc[j];
     }
   }
   __syncwarp();
   tc_fence_before();
-  if (split > 1) {
+  if (split > 1)
     cluster_sync();
-    if (warp >= 2) {
-      const int row = (warp & 3) * 32 + lane;
-      const int rows = static_cast<int>(a.M - m0 < bt ? a.M - m0 : bt);
-      for (int j = rank; j < rows; j += split) {
-        float y = 0.f;
-        for (int r = 0; r < split; ++r) y += ld_cluster_f32(map_rank(base + (j * 128 + row) * 4, r));
-        if (n0 + row < a.N) store_out(a, (m0 + j) * a.N + n0 + row, y);
-      }
-    }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while another reads its sums
-  } else {
+  else
     __syncthreads();
+  if (warp < L::kEpiWarps) {
+    // a warp takes whole columns, four weight rows a lane, two columns at a time
+    const int step = split * L::kEpiWarps;
+    const int n = n0 + 4 * lane;
+    for (int j = rank * L::kEpiWarps + warp; j < rows; j += 2 * step) {
+      const bool two = j + step < rows;
+      const uint32_t at0 = base + part_at(j, lane), at1 = base + part_at(two ? j + step : j, lane);
+      float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f), y1 = y0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r >= split) break;
+        const float4 u = ld_cluster_v4(split > 1 ? map_rank(at0, r) : at0);
+        const float4 v = two ? ld_cluster_v4(split > 1 ? map_rank(at1, r) : at1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        y0.x += u.x, y0.y += u.y, y0.z += u.z, y0.w += u.w;
+        y1.x += v.x, y1.y += v.y, y1.z += v.z, y1.w += v.w;
+      }
+      store_out4(a, m0 + j, n, y0, vec);
+      if (two) store_out4(a, m0 + j + step, n, y1, vec);
+    }
   }
-  if (warp == 1) {
+  __syncwarp();
+  if (split > 1) cluster_sync();  // no CTA leaves while another reads its sums
+  if (warp == kWarpMma) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, kCols);
+    tmem_dealloc(tmem, L::kTmem);
   }
 }
 
 // ---------------------------------------------------------------- host
 
-template <int kChunks>
-cudaError_t launch_few(const Fp8MatmulArgs& a, int bt, int split, int32_t* status, cudaStream_t stream) {
-  constexpr FewLayout L = few_layout<kChunks>();
-  static cudaError_t set = cudaFuncSetAttribute(fp8_matmul_few_kernel<kChunks>,
-                                                cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+template <int kRows>
+cudaError_t launch_few(const Fp8MatmulArgs& a, int split, int32_t* status, cudaStream_t stream) {
+  using L = Few<kRows>;
+  static const cudaError_t set =
+      cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (set != cudaSuccess) return set;
   CUtensorMap wmap, xmap;
-  if (!make_byte_map(&wmap, a.b, a.N, a.K, a.ldb, 128) || !make_byte_map(&xmap, a.a, a.M, a.K, a.lda, bt))
+  if (!make_byte_map(&wmap, a.b, a.N, a.K, a.ldb, 128) || !make_byte_map(&xmap, a.a, a.M, a.K, a.lda, kRows))
     return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * split), static_cast<unsigned>((a.M + bt - 1) / bt));
-  return launch_cluster(fp8_matmul_few_kernel<kChunks>, grid, dim3(kFewThreads), L.total, stream, split, wmap, xmap, a,
-                        bt, split, status);
+  const bool vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.out_type == kTypeF32 ? 16 : 8) == 0 &&
+                   reinterpret_cast<uintptr_t>(a.add) % 8 == 0;
+  const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * split), static_cast<unsigned>((a.M + kRows - 1) / kRows));
+  return launch_cluster(fp8_matmul_few_kernel<kRows>, grid, dim3(L::kThreads), L::kSmem, stream, split, wmap, xmap, a,
+                        split, vec, status);
 }
 
 }  // namespace
@@ -372,19 +425,28 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t 
   }
   int32_t* status = fp8_status_word();
   if (!status) return cudaErrorInvalidSymbol;
-  if (a.M > 128) return launch_fp8_many(a, status, num_sms, stream);
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
-  // tokens a tile: the batch in equal parts of at most 128, in steps of 16
-  const long long parts = (static_cast<long long>(a.M) + 127) / 128;
-  const int bt = static_cast<int>(((a.M + parts - 1) / parts + 15) / 16 * 16);
-  const long long tiles = (a.N + 127) / 128 * ((static_cast<long long>(a.M) + bt - 1) / bt);
-  const long long slots = static_cast<long long>(num_sms) * (bt <= 32 ? 2 : 1);
+  const int rows = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 128;
+  const long long tiles = (a.N + 127) / 128 * ((static_cast<long long>(a.M) + rows - 1) / rows);
+  const long long slots = static_cast<long long>(num_sms) * (rows <= 32 ? 2 : 1);
+  // CTAs to a tile: more while all run at once and each still has eight blocks (4,096 x
+  // 7,168, one row: 18.2, 10.9, 6.4, 6.7 us with 1, 2, 4, 8; 7,168 x 2,048: 6.4, 4.7, 4.9)
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= slots && Kb >= 2 * split * 2) split *= 2;
-  if (bt <= 16) return launch_few<1>(a, bt, split, status, stream);
-  if (bt <= 32) return launch_few<2>(a, bt, split, status, stream);
-  if (bt <= 64) return launch_few<4>(a, bt, split, status, stream);
-  return launch_few<8>(a, bt, split, status, stream);
+  while (split < 8 && tiles * split * 2 <= slots && Kb >= 16 * split) split *= 2;
+  if (rows == 128) {
+    // Both kernels' times by what they were measured to take, in hundredths of a us: here
+    // 30 a block and 500 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
+    // all. (256 x 4,096 x 7,168: 15.4 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
+    // 7,168 x 2,048: 20.7 and 18.1; 8,192 x 4,096 x 7,168: 630 estimated and 160.)
+    const long long pairs = num_sms / 2;
+    const long long big = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + 255) / 256);
+    const long long here = (tiles * split + slots - 1) / slots * (30LL * ((Kb + split - 1) / split) + 500) + 100;
+    const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120) + 300;
+    if (there < here) return launch_fp8_many(a, status, num_sms, stream);
+  }
+  if (rows == 16) return launch_few<16>(a, split, status, stream);
+  if (rows == 32) return launch_few<32>(a, split, status, stream);
+  return launch_few<128>(a, split, status, stream);
 }
 
 int32_t* fp8_status_word() {
