@@ -22,27 +22,58 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 
-// Eight consecutive values: 16 (bf16) or 32 (fp32) bytes.
-__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
-  const uint4 t = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf16_lo(t.x), v[1] = bf16_hi(t.x), v[2] = bf16_lo(t.y), v[3] = bf16_hi(t.y);
-  v[4] = bf16_lo(t.z), v[5] = bf16_hi(t.z), v[6] = bf16_lo(t.w), v[7] = bf16_hi(t.w);
+constexpr int kLane = 16;                       // values of a thread
+constexpr int kLanes = kScaleBlock / kLane;     // threads to a block of 128 columns
+
+// kLane consecutive values: 32 (bf16) or 64 (fp32) bytes.
+__device__ __forceinline__ void load_lane(const uint16_t* p, float (&v)[kLane]) {
+  const uint4* q = reinterpret_cast<const uint4*>(p);
+  const uint4 t[2] = {q[0], q[1]};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[8 * i + 0] = bf16_lo(t[i].x), v[8 * i + 1] = bf16_hi(t[i].x), v[8 * i + 2] = bf16_lo(t[i].y);
+    v[8 * i + 3] = bf16_hi(t[i].y), v[8 * i + 4] = bf16_lo(t[i].z), v[8 * i + 5] = bf16_hi(t[i].z);
+    v[8 * i + 6] = bf16_lo(t[i].w), v[8 * i + 7] = bf16_hi(t[i].w);
+  }
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void load_lane(const float* p, float (&v)[kLane]) {
+#pragma unroll
+  for (int i = 0; i < kLane / 4; ++i) {
+    const float4 t = reinterpret_cast<const float4*>(p)[i];
+    v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
+  }
 }
 
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// SiLU(g) * u with the hardware's exponential and reciprocal: a few 2^-22 of the result,
+// of which e4m3 keeps 2^-4. Below -88, where the exponential overflows, the result is 0
+// (it is at most 1e-36 of u there).
+__device__ __forceinline__ float swiglu(float g, float u) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r * u;
+}
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// max(m, |v|) that keeps a NaN.
+__device__ __forceinline__ float max_nan(float m, float v) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(m), "f"(fabsf(v)));
+  return d;
+}
 
-// Scale of a block from the largest magnitude's bits (as integers NaN is above
-// infinity is above every number, so neither is lost in the maximum).
-__device__ __forceinline__ float block_scale(uint32_t amax) {
-  const float m = __uint_as_float(amax);
-  const float s = __fdiv_rn(m, kE4m3Max);
+// Scale of a block from its largest magnitude.
+__device__ __forceinline__ float block_scale(float amax) {
+  const float s = __fdiv_rn(amax, kE4m3Max);
   return s != s ? s : fmaxf(s, kScaleFloor);
+}
+
+// x / s, correctly rounded, from r = 1 / s correctly rounded: q = x r, then one step with
+// the exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990). Only for scales in [2^-90, 2^90], where the remainder
+// stays in fp32's range.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, s, x), r, q);
 }
 
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
@@ -50,23 +81,23 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
 }
 
 template <bool kSwiglu, bool kVec, typename T>
-__device__ __forceinline__ void load_chunk(const T* row, int col, int N, float (&v)[8]) {
+__device__ __forceinline__ void load_chunk(const T* row, int col, int N, float (&v)[kLane]) {
   if (kVec) {
     if (col < N) {
-      load8(row + col, v);
+      load_lane(row + col, v);
       if (kSwiglu) {
-        float u[8];
-        load8(row + N + col, u);
+        float u[kLane];
+        load_lane(row + N + col, u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = swiglu(v[i], u[i]);
+        for (int i = 0; i < kLane; ++i) v[i] = swiglu(v[i], u[i]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < kLane; ++i) v[i] = 0.f;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kLane; ++i) {
       v[i] = col + i < N ? to_f32(row[col + i]) : 0.f;
       if (kSwiglu) v[i] = swiglu(v[i], col + i < N ? to_f32(row[N + col + i]) : 0.f);
     }
@@ -74,88 +105,116 @@ __device__ __forceinline__ void load_chunk(const T* row, int col, int N, float (
 }
 
 template <bool kVec>
-__device__ __forceinline__ void store_chunk(uint8_t* q, long long row_at, int col, int N, const float (&v)[8],
+__device__ __forceinline__ void store_chunk(uint8_t* q, long long row_at, int col, int N, const float (&v)[kLane],
                                             float s) {
-  uint32_t w[4];
+  uint32_t w[kLane / 2];
+  if (s >= 0x1p-90f && s <= 0x1p90f) {
+    const float r = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = e4m3_pair(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
-  if (kVec) {
-    if (col < N) *reinterpret_cast<uint2*>(q + row_at + col) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    for (int i = 0; i < kLane / 2; ++i) w[i] = e4m3_pair(quotient(v[2 * i], s, r), quotient(v[2 * i + 1], s, r));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kLane / 2; ++i) w[i] = e4m3_pair(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
+  }
+  if (kVec) {
+    if (col < N)
+      *reinterpret_cast<uint4*>(q + row_at + col) =
+          make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLane; ++i)
       if (col + i < N) q[row_at + col + i] = static_cast<uint8_t>(w[i >> 1] >> (8 * (i & 1)));
   }
 }
 
-// 16 lanes to a block of 128 columns, 8 values each.
+constexpr int kThreads = 256;
+constexpr int kPerCta = kThreads / kLanes;  // blocks, or rows of a weight block
+
+// kLanes threads to a block of 128 columns, kLane values each. Bound by memory: 8,191 x
+// 2,048 SwiGLU pairs (84 MB) in 15.0 us, 5.6 TB/s; with
+// full-precision exponentials and divisions, eight values a thread, 28 us, by its instructions.
 template <bool kSwiglu, bool kVec, typename T>
-__global__ void __launch_bounds__(256) quantize_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(kThreads) quantize_kernel(QuantArgs a, uint32_t blocks) {
   pdl_wait();
   pdl_launch_dependents();
-  const int nb = (a.N + kScaleBlock - 1) / kScaleBlock;
-  const long long blk = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 4);
-  // (lanes of a warp's idle half stay for the shuffles)
-  const bool live = blk < static_cast<long long>(a.M) * nb;
-  const long long m = live ? blk / nb : 0;
-  const int kb = live ? static_cast<int>(blk % nb) : 0;
-  const int col = kb * kScaleBlock + (threadIdx.x & 15) * 8;
+  const uint32_t nb = (a.N + kScaleBlock - 1) / kScaleBlock;
+  const uint32_t blk = blockIdx.x * kPerCta + threadIdx.x / kLanes;
+  // (lanes without a block stay for the shuffles)
+  const bool live = blk < blocks;
+  const uint32_t m = live ? blk / nb : 0;
+  const int col = static_cast<int>(live ? blk - m * nb : 0) * kScaleBlock + (threadIdx.x % kLanes) * kLane;
   const T* row = static_cast<const T*>(a.x) + m * a.row_stride;
-  float v[8];
+  float v[kLane];
   load_chunk<kSwiglu, kVec>(row, live ? col : a.N, a.N, v);
-  uint32_t amax = 0;
+  float amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(v[i]));
+  for (int i = 0; i < kLane; ++i) amax = max_nan(amax, v[i]);
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  for (int off = kLanes / 2; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   if (!live) return;
   const float s = block_scale(amax);
-  store_chunk<kVec>(a.q, m * a.N, col, a.N, v, s);
-  if ((threadIdx.x & 15) == 0) a.s[blk] = s;
+  store_chunk<kVec>(a.q, static_cast<long long>(m) * a.N, col, a.N, v, s);
+  if (threadIdx.x % kLanes == 0) a.s[blk] = s;
 }
 
-// One CTA per 128 x 128 block: 16 lanes to a row, 16 rows at a time.
+// One CTA per 128 x 128 block: kLanes threads to a row.
 template <bool kVec, typename T>
-__global__ void __launch_bounds__(256) quantize_weight_kernel(QuantArgs a) {
+__global__ void __launch_bounds__(kThreads) quantize_weight_kernel(QuantArgs a) {
   // (waits for the producer of x, and lets nothing start early: a later kernel may
   // read these weights ahead of its own wait)
   pdl_wait();
-  __shared__ uint32_t warp_max[8];
+  __shared__ float warp_max[kThreads / 32];
   const int kb = blockIdx.x, m0 = blockIdx.y * kScaleBlock;
-  const int col = kb * kScaleBlock + (threadIdx.x & 15) * 8;
-  const int r0 = threadIdx.x >> 4;
-  uint32_t amax = 0;
-  float v[8];
-  for (int r = r0; r < kScaleBlock && m0 + r < a.M; r += 16) {
+  const int col = kb * kScaleBlock + (threadIdx.x % kLanes) * kLane;
+  const int r0 = threadIdx.x / kLanes;
+  float amax = 0.f;
+  float v[kLane];
+  for (int r = r0; r < kScaleBlock && m0 + r < a.M; r += kPerCta) {
     load_chunk<false, kVec>(static_cast<const T*>(a.x) + (m0 + r) * a.row_stride, col, a.N, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, magnitude(v[i]));
+    for (int i = 0; i < kLane; ++i) amax = max_nan(amax, v[i]);
   }
-  amax = __reduce_max_sync(0xffffffffu, amax);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, warp_max[i]);
+  for (int i = 0; i < kThreads / 32; ++i) amax = max_nan(amax, warp_max[i]);
   const float s = block_scale(amax);
-  for (int r = r0; r < kScaleBlock && m0 + r < a.M; r += 16) {
+  for (int r = r0; r < kScaleBlock && m0 + r < a.M; r += kPerCta) {
     load_chunk<false, kVec>(static_cast<const T*>(a.x) + (m0 + r) * a.row_stride, col, a.N, v);
     store_chunk<kVec>(a.q, static_cast<long long>(m0 + r) * a.N, col, a.N, v, s);
   }
   if (threadIdx.x == 0) a.s[static_cast<long long>(blockIdx.y) * gridDim.x + kb] = s;
 }
 
-// Whether every chunk of eight values is whole and its loads and stores aligned.
+// Whether every thread's values are whole and its loads and stores aligned.
 bool vector_ok(const QuantArgs& a) {
-  return a.N % 8 == 0 && a.row_stride % 8 == 0 && reinterpret_cast<uintptr_t>(a.x) % 16 == 0 &&
-         reinterpret_cast<uintptr_t>(a.q) % 8 == 0;
+  return a.N % kLane == 0 && a.row_stride % (a.x_type == kTypeF32 ? 4 : 8) == 0 &&
+         (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.q)) % 16 == 0;
 }
 
+// (blocks are counted in 32 bits: rows beyond that go in launches of their own)
 template <bool kSwiglu, typename T>
-cudaError_t launch_rows(const QuantArgs& a, cudaStream_t stream) {
-  const long long blocks = static_cast<long long>(a.M) * ((a.N + kScaleBlock - 1) / kScaleBlock);
-  const dim3 grid(static_cast<unsigned>((blocks + 15) / 16));
-  return vector_ok(a) ? launch_k(quantize_kernel<kSwiglu, true, T>, grid, dim3(256), 0, stream, true, a)
-                      : launch_k(quantize_kernel<kSwiglu, false, T>, grid, dim3(256), 0, stream, true, a);
+cudaError_t launch_rows(QuantArgs a, cudaStream_t stream) {
+  const long long nb = (a.N + kScaleBlock - 1) / kScaleBlock;
+  const bool vec = vector_ok(a);
+  const int rows = a.M;
+  const long long most = (1LL << 30) / nb;
+  for (long long m = 0; m < rows; m += most) {
+    QuantArgs b = a;
+    b.M = static_cast<int>(rows - m < most ? rows - m : most);
+    b.x = static_cast<const T*>(a.x) + m * a.row_stride;
+    b.q += m * a.N;
+    b.s += m * nb;
+    const uint32_t blocks = static_cast<uint32_t>(b.M * nb);
+    const dim3 grid((blocks + kPerCta - 1) / kPerCta);
+    const cudaError_t e =
+        vec ? launch_k(quantize_kernel<kSwiglu, true, T>, grid, dim3(kThreads), 0, stream, true, b, blocks)
+            : launch_k(quantize_kernel<kSwiglu, false, T>, grid, dim3(kThreads), 0, stream, true, b, blocks);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -168,7 +227,7 @@ cudaError_t launch_quantize(const QuantArgs& a, bool swiglu, cudaStream_t stream
 cudaError_t launch_quantize_weight(const QuantArgs& a, cudaStream_t stream) {
   const dim3 grid((a.N + kScaleBlock - 1) / kScaleBlock, (a.M + kScaleBlock - 1) / kScaleBlock);
   const bool vec = vector_ok(a);
-  auto go = [&](auto kernel) { return launch_k(kernel, grid, dim3(256), 0, stream, true, a); };
+  auto go = [&](auto kernel) { return launch_k(kernel, grid, dim3(kThreads), 0, stream, true, a); };
   if (a.x_type == kTypeF32)
     return vec ? go(quantize_weight_kernel<true, float>) : go(quantize_weight_kernel<false, float>);
   return vec ? go(quantize_weight_kernel<true, uint16_t>) : go(quantize_weight_kernel<false, uint16_t>);
