@@ -32,7 +32,7 @@ struct RouteScoredArgs {
   int32_t* ids;        // [M, topk]
   float* weights;      // [M, topk]
 };
-cudaError_t launch_route_scored(const RouteScoredArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t stream);
 
 // Block quantiser: x [M, N] (or, for the SwiGLU form, rows [g | u] of 2N) -> q e4m3
 // [M, N], s fp32 [M, ceil(N / 128)].

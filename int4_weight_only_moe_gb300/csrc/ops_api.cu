@@ -70,9 +70,6 @@ int moe_w4a16_route_scored(const void* logits, int logits_type, long long row_st
   if (misaligned(logits, logits_type == MOE_W4A16_F32 ? 4 : 2) || misaligned(bias, 4) || misaligned(topk_ids, 4) ||
       misaligned(topk_weights, 4))
     return bad("a pointer is not aligned to its type");
-  cudaError_t e;
-  const int sms = num_sms(&e);
-  if (e != cudaSuccess) return done(e);
   RouteScoredArgs a{};
   a.logits = logits;
   a.logits_type = logits_type;
@@ -89,7 +86,7 @@ int moe_w4a16_route_scored(const void* logits, int logits_type, long long row_st
   a.scale = scale;
   a.ids = topk_ids;
   a.weights = topk_weights;
-  return done(launch_route_scored(a, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_route_scored(a, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_w4a16_fp8_quantize(const void* x, int x_type, long long row_stride, int M, int K, uint8_t* q, float* s,
