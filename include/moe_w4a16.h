@@ -298,11 +298,12 @@ int moe_w4a16_fp8_status(int32_t* status, void* stream);
  *   q2, s2 = quantize(SiLU(g) * u)         out = bf16(q2 s2 . (w2 w2_s)^T + add)
  *   hidden bf16 [M, K];  w1 [2N, K] (gate rows, then up rows), w1_s [2N/128, K/128];
  *   w2 [K, N], w2_s [K/128, N/128];  add bf16 [M, K] (the routed experts' output) or
- *   NULL, may be `out`;  out bf16 [M, K];  all contiguous
+ *   NULL, may be `out`;  out bf16 [M, K];  all contiguous, w1 and w2 16-byte aligned
  *   workspace  >= moe_w4a16_shared_expert_workspace_size(M, K, N) bytes (0 for a shape
  *   that is not supported), 256-byte aligned; holds nothing between calls
- * K % 128 == 0, N % 128 == 0. M == 0 is a no-op. Launches on `stream`, allocates
- * nothing, no host synchronisation. */
+ * K % 128 == 0, N % 128 == 0. M == 0 is a no-op. Three launches on `stream` (quantise;
+ * gate/up product, SwiGLU and quantise; down product), allocates nothing, no host
+ * synchronisation. */
 size_t moe_w4a16_shared_expert_workspace_size(int M, int K, int N);
 int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const float* w1_s, const uint8_t* w2,
                             const float* w2_s, const uint16_t* add, uint16_t* out, int M, int K, int N,

@@ -16,11 +16,16 @@
 // 16 summing warps (+12%), scales staged in shared memory by other warps (+10%), output
 // through shared memory and the copy engine (+5%), copies into L2 six blocks ahead (+2%).
 //
+// The SwiGLU form takes 128 gate features and the same 128 up features as its 256, and a
+// thread sums 64 of each: it holds both for its features, agrees with the warp that has
+// the row's other 64 on the scale, and writes e4m3.
+//
 // Warps: 0..7 sums and output, 8 copies (one lane of each CTA, both counting on the
 // leader's barriers), 9 the MMAs (the leader's), 10 and 11 idle. Persistent: a pair
 // takes every (number of pairs)-th tile. 8,192 x 4,096 x 7,168: 161 us, 2,990 TFLOP/s.
 #include <cuda_bf16.h>
 
+#include "fp8_quant.cuh"
 #include "fp8_tma.cuh"
 
 namespace moe {
@@ -52,13 +57,13 @@ static_assert(256 * kEpiRegs + 128 * kOtherRegs <= kThreads * 168, "more registe
 constexpr int kTileM = 256, kTileN = 256;  // of a pair
 constexpr int kHalf = 128;                 // rows, and features, of a CTA
 constexpr int kSums = kTileN / 2;          // of a thread: one row, 128 features
-constexpr int kPiece = 32;                 // columns of a tensor-memory load
 constexpr int kOperand = 128 * 128;        // bytes of a box
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kStages = 5;
-constexpr int kBars = kStages * kStageBytes;
+constexpr int kMax = kStages * kStageBytes;  // SwiGLU: the rows' maxima [tile parity][quarter][half][32]
+constexpr int kBars = kMax + 2 * 1024;
 constexpr int kSmem = kBars + 256 + 1024;
-static_assert(8 * (2 * kStages + 5) + 8 <= 256, "barriers");
+static_assert(8 * (2 * kStages + 4 + 1 + 4) + 8 <= 256, "barriers");
 
 // acc (two sums) += v (two block sums) * s
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
@@ -76,6 +81,9 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
   return v;
 }
+
+__device__ __forceinline__ void tmem_piece(uint32_t src, uint32_t (&v)[16]) { tmem_ld16(src, v); }
+__device__ __forceinline__ void tmem_piece(uint32_t src, uint32_t (&v)[32]) { tmem_ld32(src, v); }
 
 // Tile `t` of a grid of mt x nt: bands of 8 row tiles, features outer inside a band, so
 // that the pairs at work together share rows and features in L2.
@@ -162,6 +170,40 @@ __device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, i
   }
 }
 
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+
+// SiLU(gate) * up of a thread's 64 features (the first half of its sums are the gate's, the
+// other the up projection's), into the first half; the largest magnitude.
+__device__ __forceinline__ float join_row(uint64_t (&acc)[kSums / 2]) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSums / 4; ++i) {
+    const float2 g = unpack2(acc[i]), u = unpack2(acc[kSums / 4 + i]);
+    const float h0 = swiglu(g.x, u.x), h1 = swiglu(g.y, u.y);
+    amax = max_nan(max_nan(amax, h0), h1);
+    acc[i] = pack2(h0, h1);
+  }
+  return amax;
+}
+__device__ __forceinline__ void store_quantized(const uint64_t (&acc)[kSums / 2], float s, uint8_t* to) {
+  const float r = __frcp_rn(s);
+  const bool exact = quotient_ok(s);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    Words8 w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 y = unpack2(acc[16 * c + 2 * i]), z = unpack2(acc[16 * c + 2 * i + 1]);
+      w.w[i] = e4m3_quad(y.x, y.y, z.x, z.y, s, r, exact);
+    }
+    st_global_32b(to + 32 * c, w);
+  }
+}
+
+template <bool kSwiglu>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                            const __grid_constant__ Fp8MatmulArgs a, int mt, int nt, int piece, int32_t* status) {
@@ -173,7 +215,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull = [&](int i) { return base + kBars + 8 * (2 * kStages + i); };   // each CTA's
   auto tempty = [&](int i) { return base + kBars + 8 * (2 * kStages + 2 + i); };  // leader's: both CTAs' warps
   const uint32_t drain = base + kBars + 8 * (2 * kStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kBars + 8 * (2 * kStages + 5));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kBars + 8 * (2 * kStages + 9));
+  auto met = [&](int i) { return drain + 8 + 8 * i; };  // a row quarter's two warps have their maxima
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), 2 * kEpiWarps);
     mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(met(i), 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -214,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = pair; t < tiles && ok; t += pairs) {
         int im, in;
         tile_at(t, mt, nt, &im, &in);
-        const int m0 = im * kTileM + rank * kHalf, n0 = in * kTileN + rank * kHalf;
+        const int m0 = im * kTileM + rank * kHalf;
+        const int n0 = kSwiglu ? in * kHalf + rank * a.N : in * kTileN + rank * kHalf;
         for (int kb = 0; kb < Kb; ++kb) {
           if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, status, kStatusTimeout, limit)) {
             ok = false;
@@ -276,11 +321,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) pdl_launch_dependents();
     const int half = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
-    const uint32_t src0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * kSums;
+    // (columns: 128 of the tile's 256; of the SwiGLU form 64 gate and, 128 on, 64 up)
+    const uint32_t src0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * (kSwiglu ? kSums / 2 : kSums);
     const uint32_t give0 = map_rank(tempty(0), 0);
     const int nb = (a.N + kScaleBlock - 1) / kScaleBlock;
     int ac = 0;
-    uint32_t aph = 0;
+    uint32_t aph = 0, met_ph = 0;
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += pairs) {
       int im, in;
@@ -290,38 +336,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = m < a.M;
       // (rows and features behind the end read the scales of the first row, the last block)
       const float* as = a.a_s + static_cast<long long>(live ? m : 0) * Kb;
-      const float* bs = a.b_s + static_cast<long long>(min(n / kScaleBlock, nb - 1)) * Kb;
-      float sa = *as, sb = *bs;
+      const float* bs = a.b_s + static_cast<long long>(kSwiglu ? in : min(n / kScaleBlock, nb - 1)) * Kb;
+      const long long up = kSwiglu ? static_cast<long long>(nb) * Kb : 0;  // from a gate block's scales to its up block's
+      float sa = *as, sb = *bs, sb2 = bs[up];
       uint64_t acc[kSums / 2];
 #pragma unroll
       for (int i = 0; i < kSums / 2; ++i) acc[i] = 0;
       for (int kb = 0; kb < Kb; ++kb) {
-        const uint64_t s2 = pack2(sa * sb, sa * sb);
-        if (kb + 1 < Kb) sa = *++as, sb = *++bs;
+        const uint64_t s2 = pack2(sa * sb, sa * sb), s2up = pack2(sa * sb2, sa * sb2);
+        if (kb + 1 < Kb) {
+          sa = *++as, sb = *++bs;
+          if (kSwiglu) sb2 = bs[up];
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(tfull(ac), aph, abort_flag, status, kStatusTimeout, limit));
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = src0 + ac * kTileN;
         // the loads of a piece overlap the sums of the one before it
+        constexpr int kPiece = kSwiglu ? 16 : 32;  // (the SwiGLU form has no registers for 32)
+        constexpr int kPieces = kSums / kPiece;
+        auto column = [](int c) { return c * kPiece + (kSwiglu && c >= kPieces / 2 ? kSums / 2 : 0); };
         uint32_t v[2][kPiece];
-        tmem_ld32(src, v[0]);
+        tmem_piece(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < kSums / kPiece; ++c) {
+        for (int c = 0; c < kPieces; ++c) {
           tmem_ld_wait();
-          if (c + 1 < kSums / kPiece) {
-            tmem_ld32(src + kPiece * (c + 1), v[(c + 1) & 1]);
+          if (c + 1 < kPieces) {
+            tmem_piece(src + column(c + 1), v[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(give0 + 8 * ac);
           }
+          const uint64_t by = kSwiglu && c >= kPieces / 2 ? s2up : s2;
 #pragma unroll
           for (int i = 0; i < kPiece / 2; ++i)
-            fma2(acc[c * (kPiece / 2) + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], s2);
+            fma2(acc[c * (kPiece / 2) + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], by);
         }
         if (++ac == 2) ac = 0, aph ^= 1u;
       }
-      if (ok && live) store_row(a, m, n, acc, piece);
+      if (!kSwiglu) {
+        if (ok && live) store_row(a, m, n, acc, piece);
+        continue;
+      }
+      // (bounded waits: a warp that gave up sends nothing, and its partner gives up too)
+      if (!ok) break;
+      const int quad = warp & 3;
+      const float amax = join_row(acc);
+      const uint32_t maxima = base + kMax + met_ph * 1024 + (quad * 64 + lane) * 4;
+      st_shared_f32(maxima + half * 128, amax);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(met(quad));
+      ok = __all_sync(0xffffffffu, mbar_wait(met(quad), met_ph, abort_flag, status, kStatusTimeout, limit));
+      if (!ok) break;
+      met_ph ^= 1u;
+      const float s = block_scale(max_nan(amax, ld_shared_f32(maxima + (half ^ 1) * 128)));
+      // (the other warp writes here again two tiles on, after this one's next arrival)
+      if (live) {
+        store_quantized(acc, s, static_cast<uint8_t*>(a.out) + static_cast<long long>(m) * a.N + in * kHalf + half * 64);
+        if (half == 0) a.out_s[static_cast<long long>(m) * nb + in] = s;
+      }
     }
   }
   __syncwarp();
@@ -336,11 +410,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
+namespace {
+template <bool kSwiglu>
+cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
   // pairs that can run at once (SMs that have a partner), asked once
   static int pairs = 0;
   if (pairs == 0) {
-    cudaError_t e = cudaFuncSetAttribute(fp8_matmul_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(fp8_matmul_many_kernel<kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2));
@@ -352,14 +429,14 @@ cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_many_kernel, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_many_kernel<kSwiglu>, &cfg);
     if (e != cudaSuccess) return e;
     pairs = n < 1 ? 1 : (n > num_sms / 2 ? num_sms / 2 : n);
   }
   CUtensorMap amap, bmap;
-  if (!make_byte_map(&amap, a.a, a.M, a.K, a.lda, kHalf) || !make_byte_map(&bmap, a.b, a.N, a.K, a.ldb, kHalf))
+  if (!make_byte_map(&amap, a.a, a.M, a.K, a.lda, kHalf) || !make_byte_map(&bmap, a.b, (kSwiglu ? 2LL : 1LL) * a.N, a.K, a.ldb, kHalf))
     return cudaErrorInvalidValue;
-  const int mt = (a.M + kTileM - 1) / kTileM, nt = (a.N + kTileN - 1) / kTileN;
+  const int mt = (a.M + kTileM - 1) / kTileM, nt = kSwiglu ? a.N / kHalf : (a.N + kTileN - 1) / kTileN;
   const long long tiles = static_cast<long long>(mt) * nt;
   if (tiles > (1 << 30)) return cudaErrorInvalidValue;  // (7e13 outputs)
   const uintptr_t where = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add);
@@ -367,8 +444,14 @@ cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms
                     : a.N % 4 == 0 && where % 8 == 0                                ? 8
                                                                                     : 0;
   const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? tiles : pairs);
-  return launch_cluster(fp8_matmul_many_kernel, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt, piece,
+  return launch_cluster(fp8_matmul_many_kernel<kSwiglu>, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt, piece,
                         status);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream) {
+  return swiglu ? launch_many<true>(a, status, num_sms, stream) : launch_many<false>(a, status, num_sms, stream);
 }
 
 }  // namespace moe

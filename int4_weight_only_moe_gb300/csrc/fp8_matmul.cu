@@ -7,8 +7,7 @@
 // block of `b`. A block's products are summed in fp32 unscaled; the scaled block sums
 // are added in fp32 and rounded once to the output type.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
+#include "fp8_quant.cuh"
 #include "fp8_tma.cuh"
 
 namespace moe {
@@ -100,35 +99,43 @@ __global__ void __launch_bounds__(256) fp8_matmul_plain_kernel(Fp8MatmulArgs a) 
 // registers; then one that copies (one lane; a stage is 128 x 128 weight bytes and the
 // batch's 128 bytes per row) and one that issues the MMAs (four of 32 reduction elements
 // for a block) into four accumulators in turn.
+//
+// The SwiGLU form carries two weight boxes, 128 gate rows and the 128 up rows of the same
+// features: where the partial sums meet, a warp holds both for a whole scale block of 128
+// features of a batch row, and writes SiLU(gate) * up as e4m3 with its scale.
 constexpr int kWTile = 128 * 128;  // bytes of a weight box
-constexpr int kScaleRun = 32;      // blocks whose scales are staged at a time
 constexpr int kMaxStages = 10;
 
 __device__ int32_t g_fp8_status;
 
-template <int kRows>  // batch rows of a tile: 16, 32 or 128
+template <int kRows, bool kSwiglu>  // batch rows of a tile: 16, 32 or 128
 struct Few {
   static constexpr bool kBatchIsM = kRows == 128;
-  static constexpr int kCols = kRows;  // of the MMA: the batch, or 128 weights
+  static constexpr int kW = kSwiglu ? 2 : 1;               // weight boxes
+  static constexpr int kBoxCols = kBatchIsM ? 128 : kRows;  // accumulator columns of a box
+  static constexpr int kAccCols = kW * kBoxCols;
+  static constexpr int kAccs = 4 * kAccCols <= 512 ? 4 : 512 / kAccCols;
+  static constexpr int kTmem = kAccs * kAccCols;
   static constexpr int kEpiWarps = kBatchIsM ? 8 : 4;
   static constexpr int kEpiThreads = kEpiWarps * 32;
   static constexpr int kThreads = kEpiThreads + 64;
-  static constexpr int kMine = kCols / (kEpiWarps / 4);  // columns of a thread
+  static constexpr int kMine = kBoxCols / (kEpiWarps / 4);  // columns of a box for a thread
   static constexpr int kPiece = kMine < 32 ? kMine : 32;
-  static constexpr int kAccs = 4;
-  static constexpr int kTmem = kAccs * kCols;
-  static constexpr int kStageBytes = kWTile + kRows * 128;
-  // two CTAs to an SM up to 32 columns
+  static constexpr int kStageBytes = kW * kWTile + kRows * 128;
+  // two CTAs to an SM up to 32 rows
   static constexpr int kRoom = (kBatchIsM ? 226 : 113) * 1024;
+  static constexpr int kScaleRun = kBatchIsM && kSwiglu ? 16 : 32;  // blocks whose scales are staged at a time
   static constexpr int kScaleRow = kRows + 4;  // (padded: the staging's stores spread over the banks)
-  static constexpr int kFixed = kScaleRun * kScaleRow * 4 + 512 + 1024;  // (1,024: up to the swizzle atom)
+  static constexpr int kScaleBox = kScaleRun * kScaleRow;
+  static constexpr int kFixed = kW * kScaleBox * 4 + 512 + 1024;  // (1,024: up to the swizzle atom)
   static constexpr int kFit = (kRoom - kFixed) / kStageBytes;
   static constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   static constexpr int kScales = kStages * kStageBytes;
-  static constexpr int kBars = kScales + kScaleRun * kScaleRow * 4;
+  static constexpr int kBars = kScales + kW * kScaleBox * 4;
   static constexpr int kSmem = kBars + 512 + 1024;
+  static constexpr int kPart = kRows * 512;  // partial sums of a box
   static_assert(kStages >= 2 && 8 * (2 * kStages + 2 * kAccs + 1) + 8 <= 512, "barriers");
-  static_assert(kStages * kStageBytes >= kRows * 128 * 4, "the partial sums fit the stages");
+  static_assert(kStages * kStageBytes >= kW * kPart, "the partial sums fit the stages");
 };
 
 __device__ __forceinline__ void tmem_piece(uint32_t src, uint32_t (&v)[16]) { tmem_ld16(src, v); }
@@ -170,15 +177,15 @@ __device__ __forceinline__ void store_out4(const Fp8MatmulArgs& a, long long m, 
   }
 }
 
-template <int kRows>
-__global__ void __launch_bounds__(Few<kRows>::kThreads)
+template <int kRows, bool kSwiglu>
+__global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
     fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                           const __grid_constant__ Fp8MatmulArgs a, int split, bool vec, int32_t* status) {
-  using L = Few<kRows>;
+  using L = Few<kRows, kSwiglu>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
-  float* scales = reinterpret_cast<float*>(gbase + L::kScales);  // [kScaleRun][kScaleRow]
+  float* scales = reinterpret_cast<float*>(gbase + L::kScales);  // [kW][kScaleRun][kScaleRow]
   auto full = [&](int i) { return base + L::kBars + 8 * i; };
   auto empty = [&](int i) { return base + L::kBars + 8 * (L::kStages + i); };
   auto tfull = [&](int i) { return base + L::kBars + 8 * (2 * L::kStages + i); };
@@ -226,7 +233,10 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
       if (a.weights_ready)
         for (; ahead < L::kStages && kb0 + ahead < kb1; ++ahead) {
           mbar_arrive_expect_tx(full(ahead), bytes);
-          tma_load_2d(base + ahead * L::kStageBytes, &wmap, (kb0 + ahead) * 128, n0, full(ahead), once);
+#pragma unroll
+          for (int w = 0; w < L::kW; ++w)
+            tma_load_2d(base + ahead * L::kStageBytes + w * kWTile, &wmap, (kb0 + ahead) * 128, n0 + w * a.N, full(ahead),
+                        once);
         }
       pdl_wait();
       int st = 0, it = 0;
@@ -235,9 +245,11 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
         if (it >= ahead) {
           if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, status, kStatusTimeout, limit)) break;
           mbar_arrive_expect_tx(full(st), bytes);
-          tma_load_2d(base + st * L::kStageBytes, &wmap, kb * 128, n0, full(st), once);
+#pragma unroll
+          for (int w = 0; w < L::kW; ++w)
+            tma_load_2d(base + st * L::kStageBytes + w * kWTile, &wmap, kb * 128, n0 + w * a.N, full(st), once);
         }
-        tma_load_2d(base + st * L::kStageBytes + kWTile, &xmap, kb * 128, static_cast<int>(m0), full(st), keep);
+        tma_load_2d(base + st * L::kStageBytes + L::kW * kWTile, &xmap, kb * 128, static_cast<int>(m0), full(st), keep);
         if (++st == L::kStages) st = 0, ph ^= 1u;
       }
       // shared memory is released only after the last copies have landed, whoever gave up
@@ -245,7 +257,7 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
         mbar_drain(full(i % L::kStages), (i / L::kStages) & 1);
     }
   } else if (warp == kWarpMma) {
-    constexpr uint32_t idesc = idesc_e4m3_f32(128, L::kCols);
+    constexpr uint32_t idesc = idesc_e4m3_f32(128, L::kBatchIsM ? L::kAccCols : L::kBoxCols);
     const bool leader = elect_one();
     int st = 0, ac = 0;
     uint32_t ph = 0, aph = 0;
@@ -257,11 +269,16 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
       tc_fence_after();
       if (leader) {
         const uint64_t wd = sw128_kmajor_desc(base + st * L::kStageBytes);
-        const uint64_t xd = sw128_kmajor_desc(base + st * L::kStageBytes + kWTile);
-        const uint32_t d = tmem + ac * L::kCols;
+        const uint64_t xd = sw128_kmajor_desc(base + st * L::kStageBytes + L::kW * kWTile);
+        const uint32_t d = tmem + ac * L::kAccCols;
+        // (32 bytes on: 2 descriptor units; with the batch as rows both boxes are one operand)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)  // (32 bytes on: 2 descriptor units)
-          tc_mma_e4m3(d, (L::kBatchIsM ? xd : wd) + 2 * i, (L::kBatchIsM ? wd : xd) + 2 * i, idesc, i > 0);
+        for (int w = 0; w < (L::kBatchIsM ? 1 : L::kW); ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t wi = wd + w * (kWTile / 16) + 2 * i, xi = xd + 2 * i;
+            tc_mma_e4m3(d + w * L::kBoxCols, L::kBatchIsM ? xi : wi, L::kBatchIsM ? wi : xi, idesc, i > 0);
+          }
         tc_commit(empty(st));
         tc_commit(tfull(ac));
       }
@@ -280,43 +297,54 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
     const int row = (warp & 3) * 32 + lane;
     const int c0 = (warp >> 2) * L::kMine;  // first column
     const uint32_t src0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
-    float acc[L::kMine];
+    float acc[L::kW][L::kMine];
 #pragma unroll
-    for (int j = 0; j < L::kMine; ++j) acc[j] = 0.f;
+    for (int j = 0; j < L::kMine; ++j)
+#pragma unroll
+      for (int w = 0; w < L::kW; ++w) acc[w][j] = 0.f;
     int ac = 0;
     uint32_t aph = 0;
     bool ok = true;  // (a warp that gave up goes on without sums: the others meet it at the barrier)
     for (int kb = kb0; kb < kb1; ++kb) {
-      const int at = (kb - kb0) % kScaleRun;
+      const int at = (kb - kb0) % L::kScaleRun;
       if (at == 0) {  // both scales of the next blocks, multiplied
-        const int run = min(kScaleRun, kb1 - kb);
+        const int run = min(L::kScaleRun, kb1 - kb);
         named_bar_sync(1, L::kEpiThreads);
         if (lane < run) {  // (lanes along the blocks: whole lines of a_s)
-          const float sb = a.b_s[static_cast<long long>(n0 / kScaleBlock) * Kb + kb + lane];
+          float sb[L::kW];
+#pragma unroll
+          for (int w = 0; w < L::kW; ++w) sb[w] = a.b_s[static_cast<long long>((n0 + w * a.N) / kScaleBlock) * Kb + kb + lane];
 #pragma unroll 4
-          for (int j = warp; j < kRows; j += L::kEpiWarps)
-            scales[lane * L::kScaleRow + j] = j < rows ? a.a_s[(m0 + j) * Kb + kb + lane] * sb : 0.f;
+          for (int j = warp; j < kRows; j += L::kEpiWarps) {
+            const float sa = j < rows ? a.a_s[(m0 + j) * Kb + kb + lane] : 0.f;
+#pragma unroll
+            for (int w = 0; w < L::kW; ++w) scales[w * L::kScaleBox + lane * L::kScaleRow + j] = sa * sb[w];
+          }
         }
         named_bar_sync(1, L::kEpiThreads);
       }
       ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(ac), aph, abort_flag, status, kStatusTimeout, limit));
       if (!ok) continue;
       tc_fence_after();
-      const float mine = scales[at * L::kScaleRow + (L::kBatchIsM ? row : 0)];
 #pragma unroll
-      for (int c = 0; c < L::kMine / L::kPiece; ++c) {
-        uint32_t v[L::kPiece];
-        tmem_piece(src0 + ac * L::kCols + c * L::kPiece, v);
-        const float4* sc = reinterpret_cast<const float4*>(scales + at * L::kScaleRow + c * L::kPiece);
-        tmem_ld_wait();
+      for (int w = 0; w < L::kW; ++w) {
+        const float* table = scales + w * L::kScaleBox + at * L::kScaleRow;
+        const float mine = table[L::kBatchIsM ? row : 0];
 #pragma unroll
-        for (int q = 0; q < L::kPiece / 4; ++q) {
-          const float4 s4 = L::kBatchIsM ? make_float4(mine, mine, mine, mine) : sc[q];
-          float* x = acc + c * L::kPiece + 4 * q;
-          x[0] = fmaf(__uint_as_float(v[4 * q + 0]), s4.x, x[0]);
-          x[1] = fmaf(__uint_as_float(v[4 * q + 1]), s4.y, x[1]);
-          x[2] = fmaf(__uint_as_float(v[4 * q + 2]), s4.z, x[2]);
-          x[3] = fmaf(__uint_as_float(v[4 * q + 3]), s4.w, x[3]);
+        for (int c = 0; c < L::kMine / L::kPiece; ++c) {
+          uint32_t v[L::kPiece];
+          tmem_piece(src0 + ac * L::kAccCols + w * L::kBoxCols + c * L::kPiece, v);
+          const float4* sc = reinterpret_cast<const float4*>(table + c * L::kPiece);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < L::kPiece / 4; ++q) {
+            const float4 s4 = L::kBatchIsM ? make_float4(mine, mine, mine, mine) : sc[q];
+            float* x = acc[w] + c * L::kPiece + 4 * q;
+            x[0] = fmaf(__uint_as_float(v[4 * q + 0]), s4.x, x[0]);
+            x[1] = fmaf(__uint_as_float(v[4 * q + 1]), s4.y, x[1]);
+            x[2] = fmaf(__uint_as_float(v[4 * q + 2]), s4.z, x[2]);
+            x[3] = fmaf(__uint_as_float(v[4 * q + 3]), s4.w, x[3]);
+          }
         }
       }
       tc_fence_before();
@@ -326,14 +354,19 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
     }
     // sums [batch row][128 weights], 16-byte pieces swizzled by the row (every MMA is done --
     // the last accumulator was waited for -- so the stages are free)
-    if (L::kBatchIsM) {
 #pragma unroll
-      for (int i = 0; i < L::kMine; i += 4)
-        *reinterpret_cast<float4*>(gbase + part_at(row, (c0 + i) / 4)) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-    } else {
+    for (int w = 0; w < L::kW; ++w) {
+      uint8_t* part = gbase + w * L::kPart;
+      if (L::kBatchIsM) {
 #pragma unroll
-      for (int j = 0; j < L::kMine; ++j)
-        if (j < rows) *reinterpret_cast<float*>(gbase + part_at(j, row / 4) + (row & 3) * 4) = acc[j];
+        for (int i = 0; i < L::kMine; i += 4)
+          *reinterpret_cast<float4*>(part + part_at(row, (c0 + i) / 4)) =
+              make_float4(acc[w][i], acc[w][i + 1], acc[w][i + 2], acc[w][i + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < L::kMine; ++j)
+          if (j < rows) *reinterpret_cast<float*>(part + part_at(j, row / 4) + (row & 3) * 4) = acc[w][j];
+      }
     }
   }
   __syncwarp();
@@ -343,12 +376,14 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
   else
     __syncthreads();
   if (warp < L::kEpiWarps) {
-    // a warp takes whole columns, four weight rows a lane, two columns at a time
+    // a warp takes whole batch rows, four weights a lane: two rows at a time, or a row's
+    // gate and up
     const int step = split * L::kEpiWarps;
     const int n = n0 + 4 * lane;
-    for (int j = rank * L::kEpiWarps + warp; j < rows; j += 2 * step) {
-      const bool two = j + step < rows;
-      const uint32_t at0 = base + part_at(j, lane), at1 = base + part_at(two ? j + step : j, lane);
+    for (int j = rank * L::kEpiWarps + warp; j < rows; j += (kSwiglu ? 1 : 2) * step) {
+      const bool two = kSwiglu || j + step < rows;
+      const uint32_t at0 = base + part_at(j, lane);
+      const uint32_t at1 = kSwiglu ? at0 + L::kPart : base + part_at(two ? j + step : j, lane);
       float4 y0 = make_float4(0.f, 0.f, 0.f, 0.f), y1 = y0;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
@@ -358,8 +393,19 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
         y0.x += u.x, y0.y += u.y, y0.z += u.z, y0.w += u.w;
         y1.x += v.x, y1.y += v.y, y1.z += v.z, y1.w += v.w;
       }
-      store_out4(a, m0 + j, n, y0, vec);
-      if (two) store_out4(a, m0 + j + step, n, y1, vec);
+      if (kSwiglu) {
+        const float4 h = make_float4(swiglu(y0.x, y1.x), swiglu(y0.y, y1.y), swiglu(y0.z, y1.z), swiglu(y0.w, y1.w));
+        float amax = max_nan(max_nan(max_nan(max_nan(0.f, h.x), h.y), h.z), h.w);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        const float s = block_scale(amax);
+        const uint32_t q = e4m3_quad(h.x, h.y, h.z, h.w, s, __frcp_rn(s), quotient_ok(s));
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + (m0 + j) * a.N + n) = q;
+        if (lane == 0) a.out_s[(m0 + j) * (a.N / kScaleBlock) + n0 / kScaleBlock] = s;
+      } else {
+        store_out4(a, m0 + j, n, y0, vec);
+        if (two) store_out4(a, m0 + j + step, n, y1, vec);
+      }
     }
   }
   __syncwarp();
@@ -373,19 +419,19 @@ __global__ void __launch_bounds__(Few<kRows>::kThreads)
 
 // ---------------------------------------------------------------- host
 
-template <int kRows>
+template <int kRows, bool kSwiglu>
 cudaError_t launch_few(const Fp8MatmulArgs& a, int split, int32_t* status, cudaStream_t stream) {
-  using L = Few<kRows>;
+  using L = Few<kRows, kSwiglu>;
   static const cudaError_t set =
-      cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+      cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (set != cudaSuccess) return set;
   CUtensorMap wmap, xmap;
-  if (!make_byte_map(&wmap, a.b, a.N, a.K, a.ldb, 128) || !make_byte_map(&xmap, a.a, a.M, a.K, a.lda, kRows))
+  if (!make_byte_map(&wmap, a.b, L::kW * static_cast<long long>(a.N), a.K, a.ldb, 128) || !make_byte_map(&xmap, a.a, a.M, a.K, a.lda, kRows))
     return cudaErrorInvalidValue;
   const bool vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.out_type == kTypeF32 ? 16 : 8) == 0 &&
                    reinterpret_cast<uintptr_t>(a.add) % 8 == 0;
   const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * split), static_cast<unsigned>((a.M + kRows - 1) / kRows));
-  return launch_cluster(fp8_matmul_few_kernel<kRows>, grid, dim3(L::kThreads), L::kSmem, stream, split, wmap, xmap, a,
+  return launch_cluster(fp8_matmul_few_kernel<kRows, kSwiglu>, grid, dim3(L::kThreads), L::kSmem, stream, split, wmap, xmap, a,
                         split, vec, status);
 }
 
@@ -418,6 +464,39 @@ bool tma_ok(const Fp8MatmulArgs& a) {
 }
 }  // namespace
 
+namespace {
+// Kernel and split by size.
+template <bool kSwiglu>
+cudaError_t launch_tiles(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
+  const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
+  const int rows = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 128;
+  const long long tiles = (a.N + 127) / 128 * ((static_cast<long long>(a.M) + rows - 1) / rows);
+  const long long slots = static_cast<long long>(num_sms) * (rows <= 32 ? 2 : 1);
+  // CTAs to a tile: more while all run at once and each still has eight blocks (4,096 x
+  // 7,168, one row: 18.2, 10.9, 6.4, 6.7 us with 1, 2, 4, 8; 7,168 x 2,048: 6.4, 4.7, 4.9),
+  // or four where the weights stream in ahead of the rows. At one CTA to an SM at most
+  // four: not every cluster of eight finds room (the shared expert of 64 rows: 32.1 us
+  // with gate/up tiles over 8, 23.5 over 4).
+  const int most = rows == 128 ? 4 : 8, least = a.weights_ready ? 4 : 8;
+  int split = 1;
+  while (split < most && tiles * split * 2 <= slots && Kb >= 2 * least * split) split *= 2;
+  if (rows == 128) {
+    // Both kernels' times by what they were measured to take, in hundredths of a us: here
+    // 30 a block and 500 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
+    // all. (256 x 4,096 x 7,168: 15.4 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
+    // 7,168 x 2,048: 20.7 and 18.1; 8,192 x 4,096 x 7,168: 630 estimated and 160.)
+    const long long pairs = num_sms / 2;
+    const long long big = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + 255) / 256) * (kSwiglu ? 2 : 1);
+    const long long here = (tiles * split + slots - 1) / slots * ((kSwiglu ? 45LL : 30LL) * ((Kb + split - 1) / split) + 500) + 100;
+    const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120) + 300;
+    if (there < here) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
+  }
+  if (rows == 16) return launch_few<16, kSwiglu>(a, split, status, stream);
+  if (rows == 32) return launch_few<32, kSwiglu>(a, split, status, stream);
+  return launch_few<128, kSwiglu>(a, split, status, stream);
+}
+}  // namespace
+
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream) {
   if (!tma_ok(a)) {
     const dim3 grid((a.M + kT - 1) / kT, (a.N + kT - 1) / kT);
@@ -425,28 +504,15 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t 
   }
   int32_t* status = fp8_status_word();
   if (!status) return cudaErrorInvalidSymbol;
-  const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
-  const int rows = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 128;
-  const long long tiles = (a.N + 127) / 128 * ((static_cast<long long>(a.M) + rows - 1) / rows);
-  const long long slots = static_cast<long long>(num_sms) * (rows <= 32 ? 2 : 1);
-  // CTAs to a tile: more while all run at once and each still has eight blocks (4,096 x
-  // 7,168, one row: 18.2, 10.9, 6.4, 6.7 us with 1, 2, 4, 8; 7,168 x 2,048: 6.4, 4.7, 4.9)
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= slots && Kb >= 16 * split) split *= 2;
-  if (rows == 128) {
-    // Both kernels' times by what they were measured to take, in hundredths of a us: here
-    // 30 a block and 500 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
-    // all. (256 x 4,096 x 7,168: 15.4 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
-    // 7,168 x 2,048: 20.7 and 18.1; 8,192 x 4,096 x 7,168: 630 estimated and 160.)
-    const long long pairs = num_sms / 2;
-    const long long big = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + 255) / 256);
-    const long long here = (tiles * split + slots - 1) / slots * (30LL * ((Kb + split - 1) / split) + 500) + 100;
-    const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120) + 300;
-    if (there < here) return launch_fp8_many(a, status, num_sms, stream);
-  }
-  if (rows == 16) return launch_few<16>(a, split, status, stream);
-  if (rows == 32) return launch_few<32>(a, split, status, stream);
-  return launch_few<128>(a, split, status, stream);
+  return launch_tiles<false>(a, status, num_sms, stream);
+}
+
+// (the operands are the library's own: rows of whole 128-byte blocks, 256-byte aligned, and
+// weights checked by the caller)
+cudaError_t launch_fp8_swiglu(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream) {
+  int32_t* status = fp8_status_word();
+  if (!status) return cudaErrorInvalidSymbol;
+  return launch_tiles<true>(a, status, num_sms, stream);
 }
 
 int32_t* fp8_status_word() {

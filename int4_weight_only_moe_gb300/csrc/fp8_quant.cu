@@ -7,15 +7,11 @@
 // are zero or nearly so. The SwiGLU form quantises h = g / (1 + exp(-g)) * u of rows
 // [g | u] without storing h. A NaN in a block makes its scale and all its values NaN,
 // an infinity its scale infinite and itself NaN, so neither passes unseen.
-#include <cuda_fp8.h>
-
+#include "fp8_quant.cuh"
 #include "ops.cuh"
 
 namespace moe {
 namespace {
-
-constexpr float kE4m3Max = 448.0f;
-constexpr float kScaleFloor = 1.17549435e-38f;  // 2^-126
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -42,42 +38,6 @@ __device__ __forceinline__ void load_lane(const float* p, float (&v)[kLane]) {
     const float4 t = reinterpret_cast<const float4*>(p)[i];
     v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
   }
-}
-
-// SiLU(g) * u with the hardware's exponential and reciprocal: a few 2^-22 of the result,
-// of which e4m3 keeps 2^-4. Below -88, where the exponential overflows, the result is 0
-// (it is at most 1e-36 of u there).
-__device__ __forceinline__ float swiglu(float g, float u) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  return g * r * u;
-}
-
-// max(m, |v|) that keeps a NaN.
-__device__ __forceinline__ float max_nan(float m, float v) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(m), "f"(fabsf(v)));
-  return d;
-}
-
-// Scale of a block from its largest magnitude.
-__device__ __forceinline__ float block_scale(float amax) {
-  const float s = __fdiv_rn(amax, kE4m3Max);
-  return s != s ? s : fmaxf(s, kScaleFloor);
-}
-
-// x / s, correctly rounded, from r = 1 / s correctly rounded: q = x r, then one step with
-// the exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990). Only for scales in [2^-90, 2^90], where the remainder
-// stays in fp32's range.
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
-}
-
-__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
 template <bool kSwiglu, bool kVec, typename T>
@@ -107,23 +67,17 @@ __device__ __forceinline__ void load_chunk(const T* row, int col, int N, float (
 template <bool kVec>
 __device__ __forceinline__ void store_chunk(uint8_t* q, long long row_at, int col, int N, const float (&v)[kLane],
                                             float s) {
-  uint32_t w[kLane / 2];
-  if (s >= 0x1p-90f && s <= 0x1p90f) {
-    const float r = __frcp_rn(s);
+  const bool exact = quotient_ok(s);
+  const float r = __frcp_rn(s);
+  uint32_t w[kLane / 4];
 #pragma unroll
-    for (int i = 0; i < kLane / 2; ++i) w[i] = e4m3_pair(quotient(v[2 * i], s, r), quotient(v[2 * i + 1], s, r));
-  } else {
-#pragma unroll
-    for (int i = 0; i < kLane / 2; ++i) w[i] = e4m3_pair(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
-  }
+  for (int i = 0; i < kLane / 4; ++i) w[i] = e4m3_quad(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], s, r, exact);
   if (kVec) {
-    if (col < N)
-      *reinterpret_cast<uint4*>(q + row_at + col) =
-          make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+    if (col < N) *reinterpret_cast<uint4*>(q + row_at + col) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
     for (int i = 0; i < kLane; ++i)
-      if (col + i < N) q[row_at + col + i] = static_cast<uint8_t>(w[i >> 1] >> (8 * (i & 1)));
+      if (col + i < N) q[row_at + col + i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
   }
 }
 

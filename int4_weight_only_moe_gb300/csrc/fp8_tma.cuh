@@ -127,7 +127,7 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
 }
 
 // The product with the batch as the MMA's rows, in fp8_many.cu.
-cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream);
+cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream);
 // Device address of the products' status word, null on failure.
 int32_t* fp8_status_word();
 

@@ -61,7 +61,11 @@ struct Fp8MatmulArgs {
   int out_type;
   int M, N, K;
   bool weights_ready;   // `b` and `b_s` were written before the kernel in front of this one began
+  float* out_s;         // SwiGLU form: scales [M, N / 128] of `out`, which is e4m3 [M, N]
 };
+// The SwiGLU form: `b` has 2 N rows, gate then up (N a multiple of 128), and the output is
+// SiLU(gate) * up, quantised.
+cudaError_t launch_fp8_swiglu(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
 
 // Status word of the products (MOE_W4A16_STATUS_TIMEOUT when a wait gave up); clears it.

@@ -126,7 +126,7 @@ int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, cons
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
-  Fp8MatmulArgs g{a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K, false};
+  Fp8MatmulArgs g{a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K, false, nullptr};
   return done(launch_fp8_matmul(g, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -137,7 +137,7 @@ int moe_w4a16_fp8_status(int32_t* status, void* stream) {
 
 namespace {
 struct SharedLayout {
-  size_t q1, s1, gu, q2, s2, total;
+  size_t q1, s1, q2, s2, total;
 };
 SharedLayout shared_layout(int M, int K, int N) {
   SharedLayout L{};
@@ -145,7 +145,6 @@ SharedLayout shared_layout(int M, int K, int N) {
   size_t off = 0;
   L.q1 = off, off = align_up(off + m * K);
   L.s1 = off, off = align_up(off + m * blocks(K) * sizeof(float));
-  L.gu = off, off = align_up(off + m * 2 * N * sizeof(float));
   L.q2 = off, off = align_up(off + m * N);
   L.s2 = off, off = align_up(off + m * blocks(N) * sizeof(float));
   L.total = off;
@@ -169,6 +168,7 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
   if (M == 0) return MOE_W4A16_OK;
   if (!hidden || !w1 || !w1_s || !w2 || !w2_s || !out || !workspace) return bad("null pointer argument");
   if (misaligned(workspace, 256)) return bad("workspace must be 256-byte aligned");
+  if (misaligned(w1, 16) || misaligned(w2, 16)) return bad("w1 and w2 must be 16-byte aligned");
   if (misaligned(hidden, 2) || misaligned(w1_s, 4) || misaligned(w2_s, 4) || misaligned(add, 2) || misaligned(out, 2))
     return bad("a pointer is not aligned to its type");
   const SharedLayout L = shared_layout(M, K, N);
@@ -183,13 +183,11 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
   uint8_t* q2 = ws + L.q2;
   float* s1 = reinterpret_cast<float*>(ws + L.s1);
   float* s2 = reinterpret_cast<float*>(ws + L.s2);
-  float* gu = reinterpret_cast<float*>(ws + L.gu);
   e = launch_quantize(QuantArgs{hidden, kTypeBf16, K, M, K, q1, s1}, false, s);
   if (e == cudaSuccess)
-    e = launch_fp8_matmul(Fp8MatmulArgs{q1, K, s1, w1, K, w1_s, nullptr, gu, kTypeF32, M, 2 * N, K, true}, sms, s);
-  if (e == cudaSuccess) e = launch_quantize(QuantArgs{gu, kTypeF32, 2LL * N, M, N, q2, s2}, true, s);
+    e = launch_fp8_swiglu(Fp8MatmulArgs{q1, K, s1, w1, K, w1_s, nullptr, q2, kTypeF32, M, N, K, true, s2}, sms, s);
   if (e == cudaSuccess)
-    e = launch_fp8_matmul(Fp8MatmulArgs{q2, N, s2, w2, N, w2_s, add, out, kTypeBf16, M, K, N, true}, sms, s);
+    e = launch_fp8_matmul(Fp8MatmulArgs{q2, N, s2, w2, N, w2_s, add, out, kTypeBf16, M, K, N, true, nullptr}, sms, s);
   return done(e);
 }
 

@@ -8,11 +8,12 @@ block of 128 x 128 (weights, ``[ceil(N / 128), ceil(K / 128)]``).
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
-from . import (BF16, F32, _need, moe_w4a16_fp8_matmul, moe_w4a16_fp8_quantize, moe_w4a16_fp8_quantize_weight,
-               moe_w4a16_fp8_swiglu_quantize, moe_w4a16_shared_expert, moe_w4a16_shared_expert_workspace_size)
-from .routing import _lend, _rows
+from . import BF16, F32, _check, _need, lib, moe_w4a16_fp8_status, moe_w4a16_shared_expert_workspace_size
+from .routing import _dense, _handle, _new, _rows
 
 BLOCK = 128
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
@@ -24,62 +25,64 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _quantize(call, x, name, cols, scale_rows, q, s, stream):
-    stride = _rows(x, name, _FLOATS)
-    M = x.shape[0]
+def _bytes(t, shape, name):
+    """Address of a contiguous CUDA tensor of e4m3 values (or their bytes) of this shape."""
+    if t.dtype not in _E4M3 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, _BYTES, shape, name)
+    return t.data_ptr()
+
+
+def _quantize(call, x, name, parts, rows_to_a_scale, q, s, stream):
+    M, width, stride = _rows(x, name, _FLOATS)
+    cols = width // parts
+    scales = (M if rows_to_a_scale == 1 else _blocks(M), _blocks(cols))
     if q is None:
-        q = torch.empty((M, cols), dtype=torch.float8_e4m3fn, device=x.device)
-        _lend(stream, q)
-    else:
-        _need(q, _BYTES, (M, cols), "q")
+        q = _new((M, cols), torch.float8_e4m3fn, x, stream)
     if s is None:
-        s = torch.empty((scale_rows, _blocks(cols)), dtype=torch.float32, device=x.device)
-        _lend(stream, s)
-    else:
-        _need(s, ("float32",), (scale_rows, _blocks(cols)), "s")
-    call(x, _FLOATS[x.dtype], stride, M, cols, q, s, stream)
+        s = _new(scales, torch.float32, x, stream)
+    _check(call(x.data_ptr(), _FLOATS[x.dtype], stride, M, cols, _bytes(q, (M, cols), "q"),
+                _dense(s, torch.float32, scales, "s"), _handle(stream, x)))
     return q, s
 
 
 def quantize(x, q=None, s=None, stream=None):
     """``x`` [M, K] (bf16 or fp32) to ``(q e4m3 [M, K], s fp32 [M, ceil(K / 128)])``."""
-    return _quantize(moe_w4a16_fp8_quantize, x, "x", x.shape[-1], x.shape[0], q, s, stream)
+    return _quantize(lib().moe_w4a16_fp8_quantize, x, "x", 1, 1, q, s, stream)
 
 
 def swiglu_quantize(gate_up, q=None, s=None, stream=None):
     """SiLU(gate) * up of rows ``[gate | up]`` [M, 2 N], quantised: ``(q [M, N], s)``."""
     if gate_up.shape[-1] % 2:
         raise ValueError(f"gate_up: {gate_up.shape[-1]} columns, expected an even number")
-    return _quantize(moe_w4a16_fp8_swiglu_quantize, gate_up, "gate_up", gate_up.shape[-1] // 2, gate_up.shape[0],
-                     q, s, stream)
+    return _quantize(lib().moe_w4a16_fp8_swiglu_quantize, gate_up, "gate_up", 2, 1, q, s, stream)
 
 
 def quantize_weight(w, q=None, s=None, stream=None):
     """A weight [N, K] to ``(q e4m3 [N, K], s fp32 [ceil(N / 128), ceil(K / 128)])``."""
-    return _quantize(moe_w4a16_fp8_quantize_weight, w, "w", w.shape[-1], _blocks(w.shape[0]), q, s, stream)
+    return _quantize(lib().moe_w4a16_fp8_quantize_weight, w, "w", 1, BLOCK, q, s, stream)
 
 
 def matmul(a, a_s, b, b_s, add=None, out=None, out_dtype=torch.bfloat16, stream=None):
     """``(a a_s) (b b_s)^T`` (+ ``add``) of 8-bit ``a`` [M, K] and ``b`` [N, K]: [M, N] in
     ``out_dtype`` (bf16 or fp32; that of ``out`` where it is given)."""
-    lda, ldb = _rows(a, "a", _E4M3), _rows(b, "b", _E4M3)
-    M, K = a.shape
-    N = b.shape[0]
-    if b.shape[1] != K:
+    M, K, lda = _rows(a, "a", _E4M3)
+    N, b_cols, ldb = _rows(b, "b", _E4M3)
+    if b_cols != K:
         raise ValueError(f"b: shape {tuple(b.shape)}, expected {K} columns")
-    _need(a_s, ("float32",), (M, _blocks(K)), "a_s")
-    _need(b_s, ("float32",), (_blocks(N), _blocks(K)), "b_s")
-    if add is not None:
-        _need(add, ("bfloat16",), (M, N), "add")
+    sa = _dense(a_s, torch.float32, (M, _blocks(K)), "a_s")
+    sb = _dense(b_s, torch.float32, (_blocks(N), _blocks(K)), "b_s")
+    plus = 0 if add is None else _dense(add, torch.bfloat16, (M, N), "add")
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
-        _lend(stream, out)
-    else:
-        _need(out, ("bfloat16", "float32"), (M, N), "out")
+        out = _new((M, N), out_dtype, a, stream)
     if out.dtype not in _FLOATS:
-        raise ValueError(f"out_dtype: {out.dtype}, expected one of {tuple(_FLOATS)}")
-    moe_w4a16_fp8_matmul(a, lda, a_s, b, ldb, b_s, add, out, _FLOATS[out.dtype], M, N, K, stream)
+        raise ValueError(f"out: dtype {out.dtype}, expected one of {tuple(_FLOATS)}")
+    _check(lib().moe_w4a16_fp8_matmul(
+        a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, plus, _dense(out, out.dtype, (M, N), "out"), _FLOATS[out.dtype],
+        M, N, K, _handle(stream, a)))
     return out
+
+
+_workspace_size = functools.lru_cache(maxsize=256)(moe_w4a16_shared_expert_workspace_size)
 
 
 def shared_expert(hidden, w1, w1_s, w2, w2_s, add=None, out=None, workspace=None, stream=None):
@@ -91,23 +94,24 @@ def shared_expert(hidden, w1, w1_s, w2, w2_s, add=None, out=None, workspace=None
     ``moe_w4a16_shared_expert_workspace_size(M, K, N)`` bytes) is allocated where it is not
     given.
     """
-    M, K = hidden.shape
+    M, K = shape = hidden.shape
     N = w2.shape[1]
-    _need(hidden, ("bfloat16",), (M, K), "hidden")
-    _need(w1, _BYTES, (2 * N, K), "w1")
-    _need(w1_s, ("float32",), (_blocks(2 * N), _blocks(K)), "w1_s")
-    _need(w2, _BYTES, (K, N), "w2")
-    _need(w2_s, ("float32",), (_blocks(K), _blocks(N)), "w2_s")
-    if add is not None:
-        _need(add, ("bfloat16",), (M, K), "add")
+    x = _dense(hidden, torch.bfloat16, (M, K), "hidden")
+    kb, nb = _blocks(K), _blocks(N)
+    weights = (_bytes(w1, (2 * N, K), "w1"), _dense(w1_s, torch.float32, (_blocks(2 * N), kb), "w1_s"),
+               _bytes(w2, (K, N), "w2"), _dense(w2_s, torch.float32, (kb, nb), "w2_s"))
+    plus = 0 if add is None else _dense(add, torch.bfloat16, shape, "add")
     if out is None:
-        out = torch.empty((M, K), dtype=torch.bfloat16, device=hidden.device)
-        _lend(stream, out)
-    else:
-        _need(out, ("bfloat16",), (M, K), "out")
+        out = _new(shape, torch.bfloat16, hidden, stream)
+    y = _dense(out, torch.bfloat16, shape, "out")
     if workspace is None:
-        need = moe_w4a16_shared_expert_workspace_size(M, K, N)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=hidden.device)
-        _lend(stream, workspace)
-    moe_w4a16_shared_expert(hidden, w1, w1_s, w2, w2_s, add, out, M, K, N, workspace, stream)
+        workspace = _new((max(_workspace_size(M, K, N), 1),), torch.uint8, hidden, stream)
+    _check(lib().moe_w4a16_shared_expert(x, *weights, plus, y, M, K, N, workspace.data_ptr(), workspace.nbytes,
+                                         _handle(stream, hidden)))
     return out
+
+
+def status(stream=None) -> int:
+    """Status of the products on the current device since the last call (0: clean);
+    synchronises ``stream``."""
+    return moe_w4a16_fp8_status(stream)

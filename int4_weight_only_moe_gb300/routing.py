@@ -9,37 +9,51 @@ from __future__ import annotations
 
 import torch
 
-from . import BF16, F32, SCORE_SIGMOID, SCORE_SOFTMAX, _need, moe_w4a16_route_scored
+from . import BF16, F32, SCORE_SIGMOID, SCORE_SOFTMAX, _check, _need, lib
 
 _SCORES = {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _rows(t, name, types):
-    """Row stride of a 2-D CUDA tensor whose rows are contiguous."""
+    """(rows, columns, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected two dimensions")
     if t.dtype not in types:
         raise ValueError(f"{name}: dtype {t.dtype}, expected one of {tuple(types)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    (rows, cols), (stride, inner) = t.shape, t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name}: the values of a row must be contiguous")
-    stride = t.stride(0)
-    if rows <= 1:
-        return max(stride, cols)
     if stride < cols:
-        raise ValueError(f"{name}: rows overlap (stride {stride}, {cols} values)")
-    return stride
+        if rows > 1:
+            raise ValueError(f"{name}: rows overlap (stride {stride}, {cols} values)")
+        stride = cols
+    return rows, cols, stride
 
 
-def _lend(stream, *tensors):
-    """Tell the allocator that ``stream``, when not the current one, uses new tensors."""
+def _dense(t, dtype, shape, name):
+    """``t`` itself, when it is a contiguous CUDA tensor of this type and shape; its address."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _need(t, (str(dtype).removeprefix("torch."),), shape, name)
+    return t.data_ptr()
+
+
+def _handle(stream, t):
+    """Raw handle of ``stream``, or of the current stream of the device of ``t``."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return int(getattr(stream, "cuda_stream", stream))
+
+
+def _new(shape, dtype, like, stream):
+    """A new tensor on the device of ``like``; the allocator learns of a ``stream`` that is
+    not the current one."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
-        for t in tensors:
-            t.record_stream(s)
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
 
 
 def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_group=1, group_top=None,
@@ -50,24 +64,19 @@ def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_gro
     ``bias`` fp32 [E] takes part in the selection only. ``group_top`` (1 or 2) is how many
     of a group's largest values count for it; by default 2 with a bias, 1 without.
     """
-    stride = _rows(logits, "logits", _TYPES)
-    M, E = logits.shape
-    if scoring not in _SCORES:
+    M, E, stride = _rows(logits, "logits", _TYPES)
+    score = _SCORES.get(scoring)
+    if score is None:
         raise ValueError(f"scoring: {scoring!r}, expected one of {tuple(_SCORES)}")
-    if bias is not None:
-        _need(bias, ("float32",), (E,), "bias")
+    b = 0 if bias is None else _dense(bias, torch.float32, (E,), "bias")
     if group_top is None:
         group_top = 2 if bias is not None else 1
     if ids is None:
-        ids = torch.empty((M, topk), dtype=torch.int32, device=logits.device)
-        _lend(stream, ids)
-    else:
-        _need(ids, ("int32",), (M, topk), "ids")
+        ids = _new((M, topk), torch.int32, logits, stream)
     if weights is None:
-        weights = torch.empty((M, topk), dtype=torch.float32, device=logits.device)
-        _lend(stream, weights)
-    else:
-        _need(weights, ("float32",), (M, topk), "weights")
-    moe_w4a16_route_scored(logits, _TYPES[logits.dtype], stride, M, E, topk, _SCORES[scoring], bias, n_group,
-                           topk_group, group_top, bool(renormalize), scale, ids, weights, stream)
+        weights = _new((M, topk), torch.float32, logits, stream)
+    _check(lib().moe_w4a16_route_scored(
+        logits.data_ptr(), _TYPES[logits.dtype], stride, M, E, topk, score, b, n_group, topk_group, group_top,
+        renormalize, scale, _dense(ids, torch.int32, (M, topk), "ids"),
+        _dense(weights, torch.float32, (M, topk), "weights"), _handle(stream, logits)))
     return ids, weights
