@@ -102,43 +102,25 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 
-// A thread's sums to the output, in pieces of `piece` bytes that are whole and aligned:
-// 32, 8, or 0 for value by value.
-__device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, int n, const uint64_t (&acc)[kSums / 2],
-                                          int piece) {
+// A thread's sums to the output, 32 bytes at a time: rows of whole, aligned such pieces.
+__device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, int n, const uint64_t (&acc)[kSums / 2]) {
   const long long at = m * a.N + n;
   if (a.out_type == kTypeBf16) {
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at;
-    if (piece == 32) {
 #pragma unroll
-      for (int c = 0; c < kSums / 16; ++c) {
-        if (n + 16 * c >= a.N) break;
-        Words8 w, d;
-        if (a.add) d = ld_global_32b(a.add + at + 16 * c);
+    for (int c = 0; c < kSums / 16; ++c) {
+      if (n + 16 * c >= a.N) break;
+      Words8 w, d;
+      if (a.add) d = ld_global_32b(a.add + at + 16 * c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float2 y = unpack2(acc[8 * c + i]);
-          if (a.add) y.x += __uint_as_float(d.w[i] << 16), y.y += __uint_as_float(d.w[i] & 0xFFFF0000u);
-          w.w[i] = bf16x2(y.x, y.y);
-        }
-        st_global_32b(out + 16 * c, w);
+      for (int i = 0; i < 8; ++i) {
+        float2 y = unpack2(acc[8 * c + i]);
+        if (a.add) y.x += __uint_as_float(d.w[i] << 16), y.y += __uint_as_float(d.w[i] & 0xFFFF0000u);
+        w.w[i] = bf16x2(y.x, y.y);
       }
-      return;
+      st_global_32b(out + 16 * c, w);
     }
-    if (piece == 8) {
-#pragma unroll
-      for (int c = 0; c < kSums / 4; ++c) {
-        if (n + 4 * c >= a.N) break;
-        uint2 d = make_uint2(0u, 0u);  // the addend (0 adds nothing)
-        if (a.add) d = *reinterpret_cast<const uint2*>(a.add + at + 4 * c);
-        const float2 y = unpack2(acc[2 * c]), z = unpack2(acc[2 * c + 1]);
-        d.x = bf16x2(y.x + __uint_as_float(d.x << 16), y.y + __uint_as_float(d.x & 0xFFFF0000u));
-        d.y = bf16x2(z.x + __uint_as_float(d.y << 16), z.y + __uint_as_float(d.y & 0xFFFF0000u));
-        *reinterpret_cast<uint2*>(out + 4 * c) = d;
-      }
-      return;
-    }
-  } else if (piece == 32 && !a.add) {
+  } else {
     float* out = static_cast<float*>(a.out) + at;
 #pragma unroll
     for (int c = 0; c < kSums / 8; ++c) {
@@ -151,21 +133,50 @@ __device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, i
       }
       st_global_32b(out + 8 * c, w);
     }
-    return;
   }
+}
+
+// A warp's sums (32 rows from m0 on, 128 features) to an output of any alignment: 32
+// features at a time are transposed between the lanes, which then write consecutive
+// features of one row (value by value from its own row, a lane's stores cost 32 lines
+// each: 777 x 1,000 x 1,936 took 41 us).
+__device__ __forceinline__ void store_across(const Fp8MatmulArgs& a, long long m0, int n, int lane,
+                                             const uint64_t (&acc)[kSums / 2]) {
 #pragma unroll
-  for (int i = 0; i < kSums / 2; ++i) {
-    const float2 y = unpack2(acc[i]);
-    const float v[2] = {y.x, y.y};
+  for (int c = 0; c < kSums / 32; ++c) {
+    if (n + 32 * c >= a.N) break;
+    float x[32];  // [feature] of row `lane`, then [row] of feature `lane`
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int j = 2 * i + k;
-      if (n + j >= a.N) continue;
-      const float w = v[k] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at + j]) << 16) : 0.f);
-      if (a.out_type == kTypeBf16)
-        static_cast<__nv_bfloat16*>(a.out)[at + j] = __float2bfloat16_rn(w);
-      else
-        static_cast<float*>(a.out)[at + j] = w;
+    for (int i = 0; i < 16; ++i) {
+      const float2 y = unpack2(acc[16 * c + i]);
+      x[2 * i] = y.x, x[2 * i + 1] = y.y;
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) {
+      const bool high = lane & s;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (i & s) continue;
+        const float got = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + s], s);
+        if (high)
+          x[i] = got;
+        else
+          x[i + s] = got;
+      }
+    }
+    const int rows = n + 32 * c + lane < a.N ? static_cast<int>(a.M - m0 < 32 ? a.M - m0 : 32) : 0;
+    long long at = m0 * a.N + n + 32 * c + lane;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      if (r < rows) {
+        const float y = x[r] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at]) << 16) : 0.f);
+        if (a.out_type == kTypeBf16)
+          static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+        else
+          static_cast<float*>(a.out)[at] = y;
+      }
+      at += a.N;
+      asm volatile("" : "+l"(at));  // (one address at a time, not 32 in registers)
     }
   }
 }
@@ -203,10 +214,14 @@ __device__ __forceinline__ void store_quantized(const uint64_t (&acc)[kSums / 2]
   }
 }
 
-template <bool kSwiglu>
+// Where the sums go.
+enum Out { kOutPieces, kOutAcross, kOutSwiglu };
+
+template <Out kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
-                           const __grid_constant__ Fp8MatmulArgs a, int mt, int nt, int piece, int32_t* status) {
+                           const __grid_constant__ Fp8MatmulArgs a, int mt, int nt, int32_t* status) {
+  constexpr bool kSwiglu = kOut == kOutSwiglu;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -353,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t src = src0 + ac * kTileN;
         // the loads of a piece overlap the sums of the one before it
-        constexpr int kPiece = kSwiglu ? 16 : 32;  // (the SwiGLU form has no registers for 32)
+        constexpr int kPiece = kOut == kOutPieces ? 32 : 16;  // (the others have no registers for 32)
         constexpr int kPieces = kSums / kPiece;
         auto column = [](int c) { return c * kPiece + (kSwiglu && c >= kPieces / 2 ? kSums / 2 : 0); };
         uint32_t v[2][kPiece];
@@ -376,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++ac == 2) ac = 0, aph ^= 1u;
       }
       if (!kSwiglu) {
-        if (ok && live) store_row(a, m, n, acc, piece);
+        if (kOut == kOutPieces && ok && live) store_row(a, m, n, acc);
+        if (kOut == kOutAcross && ok) store_across(a, m - lane, n, lane, acc);
         continue;
       }
       // (bounded waits: a warp that gave up sends nothing, and its partner gives up too)
@@ -411,12 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 namespace {
-template <bool kSwiglu>
+template <Out kOut>
 cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
+  constexpr bool kSwiglu = kOut == kOutSwiglu;
   // pairs that can run at once (SMs that have a partner), asked once
   static int pairs = 0;
   if (pairs == 0) {
-    cudaError_t e = cudaFuncSetAttribute(fp8_matmul_many_kernel<kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(fp8_matmul_many_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -429,7 +446,7 @@ cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cu
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_many_kernel<kSwiglu>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_many_kernel<kOut>, &cfg);
     if (e != cudaSuccess) return e;
     pairs = n < 1 ? 1 : (n > num_sms / 2 ? num_sms / 2 : n);
   }
@@ -439,19 +456,18 @@ cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cu
   const int mt = (a.M + kTileM - 1) / kTileM, nt = kSwiglu ? a.N / kHalf : (a.N + kTileN - 1) / kTileN;
   const long long tiles = static_cast<long long>(mt) * nt;
   if (tiles > (1 << 30)) return cudaErrorInvalidValue;  // (7e13 outputs)
-  const uintptr_t where = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add);
-  const int piece = a.N % (a.out_type == kTypeBf16 ? 16 : 8) == 0 && where % 32 == 0 ? 32
-                    : a.N % 4 == 0 && where % 8 == 0                                ? 8
-                                                                                    : 0;
   const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? tiles : pairs);
-  return launch_cluster(fp8_matmul_many_kernel<kSwiglu>, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt, piece,
+  return launch_cluster(fp8_matmul_many_kernel<kOut>, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt,
                         status);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream) {
-  return swiglu ? launch_many<true>(a, status, num_sms, stream) : launch_many<false>(a, status, num_sms, stream);
+  if (swiglu) return launch_many<kOutSwiglu>(a, status, num_sms, stream);
+  const uintptr_t where = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add);
+  const bool pieces = a.N % (a.out_type == kTypeBf16 ? 16 : 8) == 0 && where % 32 == 0 && !(a.out_type == kTypeF32 && a.add);
+  return pieces ? launch_many<kOutPieces>(a, status, num_sms, stream) : launch_many<kOutAcross>(a, status, num_sms, stream);
 }
 
 }  // namespace moe
