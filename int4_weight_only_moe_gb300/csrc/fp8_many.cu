@@ -165,18 +165,30 @@ __device__ __forceinline__ void store_across(const Fp8MatmulArgs& a, long long m
       }
     }
     const int rows = n + 32 * c + lane < a.N ? static_cast<int>(a.M - m0 < 32 ? a.M - m0 : 32) : 0;
-    long long at = m0 * a.N + n + 32 * c + lane;
+    const long long first = m0 * a.N + n + 32 * c + lane;
+    if (a.add) {  // (all loads before the first store, which may be to the same array)
+      uint16_t d[32];
+      long long at = first;
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        d[r] = r < rows ? a.add[at] : 0;
+        at += a.N;
+        asm volatile("" : "+l"(at));  // (one address at a time, not 32 in registers)
+      }
+#pragma unroll
+      for (int r = 0; r < 32; ++r) x[r] += __uint_as_float(static_cast<uint32_t>(d[r]) << 16);
+    }
+    long long at = first;
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
       if (r < rows) {
-        const float y = x[r] + (a.add ? __uint_as_float(static_cast<uint32_t>(a.add[at]) << 16) : 0.f);
         if (a.out_type == kTypeBf16)
-          static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+          static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x[r]);
         else
-          static_cast<float*>(a.out)[at] = y;
+          static_cast<float*>(a.out)[at] = x[r];
       }
       at += a.N;
-      asm volatile("" : "+l"(at));  // (one address at a time, not 32 in registers)
+      asm volatile("" : "+l"(at));
     }
   }
 }
@@ -463,11 +475,14 @@ cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cu
 
 }  // namespace
 
+bool fp8_whole_pieces(const Fp8MatmulArgs& a) {
+  const uintptr_t where = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add);
+  return a.N % (a.out_type == kTypeBf16 ? 16 : 8) == 0 && where % 32 == 0 && !(a.out_type == kTypeF32 && a.add);
+}
+
 cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream) {
   if (swiglu) return launch_many<kOutSwiglu>(a, status, num_sms, stream);
-  const uintptr_t where = reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.add);
-  const bool pieces = a.N % (a.out_type == kTypeBf16 ? 16 : 8) == 0 && where % 32 == 0 && !(a.out_type == kTypeF32 && a.add);
-  return pieces ? launch_many<kOutPieces>(a, status, num_sms, stream) : launch_many<kOutAcross>(a, status, num_sms, stream);
+  return fp8_whole_pieces(a) ? launch_many<kOutPieces>(a, status, num_sms, stream) : launch_many<kOutAcross>(a, status, num_sms, stream);
 }
 
 }  // namespace moe

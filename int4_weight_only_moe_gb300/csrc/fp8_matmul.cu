@@ -178,10 +178,20 @@ __device__ __forceinline__ void join_pair(uint32_t at0, uint32_t at1, int split,
 __device__ __forceinline__ void store_out4(const Fp8MatmulArgs& a, long long m, int n, float4 y, bool vec) {
   const long long at = m * a.N + n;
   if (!vec) {
-    const float v[4] = {y.x, y.y, y.z, y.w};
+    float v[4] = {y.x, y.y, y.z, y.w};
+    if (a.add) {  // (all loads before the first store, which may be to the same array)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n + i < a.N) store_out(a, at + i, v[i]);
+      for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) v[i] += __uint_as_float(static_cast<uint32_t>(a.add[at + i]) << 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n + i >= a.N) break;
+      if (a.out_type == kTypeF32)
+        static_cast<float*>(a.out)[at + i] = v[i];
+      else
+        static_cast<__nv_bfloat16*>(a.out)[at + i] = __float2bfloat16_rn(v[i]);
+    }
     return;
   }
   if (n >= a.N) return;
@@ -498,12 +508,16 @@ cudaError_t launch_tiles(const Fp8MatmulArgs& a, int32_t* status, int num_sms, c
   if (rows == 128) {
     // Both kernels' times by what they were measured to take, in hundredths of a us: here
     // 30 a block and 500 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
-    // all. (256 x 4,096 x 7,168: 15.4 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
-    // 7,168 x 2,048: 20.7 and 18.1; 8,192 x 4,096 x 7,168: 630 estimated and 160.)
+    // all, and 800 a wave where its output cannot go in whole pieces, as much again with an
+    // addend. (256 x 4,096 x 7,168: 15.2 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
+    // 7,168 x 2,048: 20.7 and 18.1; 600 x 2,047 x 2,048 with an addend: 13.9 and 26.7;
+    // 8,192 x 4,096 x 7,168: 630 estimated and 160. The SwiGLU form's two weight boxes
+    // count 45 a block here.)
     const long long pairs = num_sms / 2;
-    const long long big = (static_cast<long long>(a.M) + 255) / 256 * ((a.N + 255) / 256) * (kSwiglu ? 2 : 1);
+    const long long big = (static_cast<long long>(a.M) + 255) / 256 * (kSwiglu ? a.N / 128 : (a.N + 255) / 256);
+    const long long odd = kSwiglu || fp8_whole_pieces(a) ? 0 : a.add ? 1600 : 800;
     const long long here = (tiles * split + slots - 1) / slots * ((kSwiglu ? 45LL : 30LL) * ((Kb + split - 1) / split) + 500) + 100;
-    const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120) + 300;
+    const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120 + odd) + 300;
     if (there < here) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
   }
   if (rows == 16) return launch_few<16, kSwiglu>(a, split, status, stream);

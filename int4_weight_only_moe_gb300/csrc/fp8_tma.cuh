@@ -126,7 +126,9 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   }
 }
 
-// The product with the batch as the MMA's rows, in fp8_many.cu.
+// The product of many rows, in fp8_many.cu, and whether its output goes in whole 32-byte
+// pieces (else it is transposed and written value by value).
+bool fp8_whole_pieces(const Fp8MatmulArgs& a);
 cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream);
 // Device address of the products' status word, null on failure.
 int32_t* fp8_status_word();
