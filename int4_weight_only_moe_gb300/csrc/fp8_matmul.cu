@@ -168,7 +168,11 @@ __device__ __forceinline__ float4 join_sums(uint32_t at) {
 __device__ __forceinline__ void join_pair(uint32_t at0, uint32_t at1, int split, float4* y0, float4* y1) {
   switch (split) {
     case 8: *y0 = join_sums<8>(at0), *y1 = join_sums<8>(at1); break;
+    case 7: *y0 = join_sums<7>(at0), *y1 = join_sums<7>(at1); break;
+    case 6: *y0 = join_sums<6>(at0), *y1 = join_sums<6>(at1); break;
+    case 5: *y0 = join_sums<5>(at0), *y1 = join_sums<5>(at1); break;
     case 4: *y0 = join_sums<4>(at0), *y1 = join_sums<4>(at1); break;
+    case 3: *y0 = join_sums<3>(at0), *y1 = join_sums<3>(at1); break;
     case 2: *y0 = join_sums<2>(at0), *y1 = join_sums<2>(at1); break;
     default: *y0 = join_sums<1>(at0), *y1 = join_sums<1>(at1);
   }
@@ -444,20 +448,76 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
 
 // ---------------------------------------------------------------- host
 
+constexpr int kMaxSplit = 8;
+
+// Clusters of `split` CTAs that run at once (SMs share a cluster only within their part of
+// the chip, so of eight at one CTA to an SM fewer fit than the SMs would hold); asked once.
+template <int kRows, bool kSwiglu>
+cudaError_t clusters_at_once(int split, int num_sms, int* clusters) {
+  using L = Few<kRows, kSwiglu>;
+  static int known[kMaxSplit + 1];
+  if (known[split] == 0) {
+    cudaError_t e =
+        cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split * num_sms);
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = split, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_few_kernel<kRows, kSwiglu>, &cfg);
+    if (e != cudaSuccess) return e;
+    // (the query counts one CTA to an SM; up to 32 rows two run there)
+    known[split] = (n < 1 ? 1 : n) * (L::kBatchIsM ? 1 : 2);
+  }
+  *clusters = known[split];
+  return cudaSuccess;
+}
+
+// CTAs to a tile: the number that leaves the busiest SM the fewest blocks, if all run at
+// once and have at least four each; the fewest CTAs of equal ones, or where the weights
+// stream in ahead of the rows the most (more of them fit: the shared expert of 4 tokens
+// 16.8 us with the down product over 2 CTAs, 15.2 over 4). Its share of the blocks, and
+// the waves of CTAs. (4,096 x 7,168, one row, 32 tiles of 56 blocks: 18.2,
+// 10.9, 6.1, 7.2, 6.7 us with 1, 2, 4, 6, 8 CTAs; 7,168 x 2,048, 56 tiles of 16: 6.4, 4.7,
+// 4.9 with 1, 2, 4.)
+template <int kRows, bool kSwiglu>
+cudaError_t choose_split(const Fp8MatmulArgs& a, int num_sms, int* split, int* share, long long* waves) {
+  const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
+  const long long tiles = (a.N + 127) / 128 * ((static_cast<long long>(a.M) + kRows - 1) / kRows);
+  int at_once = 0;
+  cudaError_t e = clusters_at_once<kRows, kSwiglu>(1, num_sms, &at_once);
+  if (e != cudaSuccess) return e;
+  *waves = (tiles + at_once - 1) / at_once;
+  *split = 1;
+  long long best = (tiles + num_sms - 1) / num_sms * Kb;
+  for (int c = 2; c <= kMaxSplit && Kb >= 4 * c && tiles * c <= 2LL * num_sms; ++c) {
+    e = clusters_at_once<kRows, kSwiglu>(c, num_sms, &at_once);
+    if (e != cudaSuccess) return e;
+    const long long blocks = (tiles * c + num_sms - 1) / num_sms * ((Kb + c - 1) / c);
+    if (tiles <= at_once && (blocks < best || (blocks == best && a.weights_ready))) best = blocks, *split = c;
+  }
+  *share = (Kb + *split - 1) / *split;
+  return cudaSuccess;
+}
+
 template <int kRows, bool kSwiglu>
 cudaError_t launch_few(const Fp8MatmulArgs& a, int split, int32_t* status, cudaStream_t stream) {
   using L = Few<kRows, kSwiglu>;
-  static const cudaError_t set =
-      cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-  if (set != cudaSuccess) return set;
   CUtensorMap wmap, xmap;
-  if (!make_byte_map(&wmap, a.b, L::kW * static_cast<long long>(a.N), a.K, a.ldb, 128) || !make_byte_map(&xmap, a.a, a.M, a.K, a.lda, kRows))
+  if (!make_byte_map(&wmap, a.b, L::kW * static_cast<long long>(a.N), a.K, a.ldb, 128) ||
+      !make_byte_map(&xmap, a.a, a.M, a.K, a.lda, kRows))
     return cudaErrorInvalidValue;
   const bool vec = a.N % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % (a.out_type == kTypeF32 ? 16 : 8) == 0 &&
                    reinterpret_cast<uintptr_t>(a.add) % 8 == 0;
   const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * split), static_cast<unsigned>((a.M + kRows - 1) / kRows));
-  return launch_cluster(fp8_matmul_few_kernel<kRows, kSwiglu>, grid, dim3(L::kThreads), L::kSmem, stream, split, wmap, xmap, a,
-                        split, vec, status);
+  return launch_cluster(fp8_matmul_few_kernel<kRows, kSwiglu>, grid, dim3(L::kThreads), L::kSmem, stream, split, wmap, xmap,
+                        a, split, vec, status);
 }
 
 }  // namespace
@@ -490,38 +550,37 @@ bool tma_ok(const Fp8MatmulArgs& a) {
 }  // namespace
 
 namespace {
+template <int kRows, bool kSwiglu>
+cudaError_t launch_split(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
+  int split = 1, share = 0;
+  long long waves = 0;
+  const cudaError_t e = choose_split<kRows, kSwiglu>(a, num_sms, &split, &share, &waves);
+  return e == cudaSuccess ? launch_few<kRows, kSwiglu>(a, split, status, stream) : e;
+}
+
 // Kernel and split by size.
 template <bool kSwiglu>
 cudaError_t launch_tiles(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
+  if (a.M <= 16) return launch_split<16, kSwiglu>(a, status, num_sms, stream);
+  if (a.M <= 32) return launch_split<32, kSwiglu>(a, status, num_sms, stream);
+  int split = 1, share = 0;
+  long long waves = 0;
+  const cudaError_t e = choose_split<128, kSwiglu>(a, num_sms, &split, &share, &waves);
+  if (e != cudaSuccess) return e;
+  // Both kernels' times by what they were measured to take, in hundredths of a us: here
+  // 30 a block and 500 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
+  // all, and 800 a wave where its output cannot go in whole pieces, as much again with an
+  // addend. (256 x 4,096 x 7,168: 15.2 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
+  // 7,168 x 2,048: 20.7 and 18.1; 600 x 2,047 x 2,048 with an addend: 13.9 and 26.7;
+  // 8,192 x 4,096 x 7,168: 630 estimated and 160. The SwiGLU form's two weight boxes
+  // count 45 a block here.)
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
-  const int rows = a.M <= 16 ? 16 : a.M <= 32 ? 32 : 128;
-  const long long tiles = (a.N + 127) / 128 * ((static_cast<long long>(a.M) + rows - 1) / rows);
-  const long long slots = static_cast<long long>(num_sms) * (rows <= 32 ? 2 : 1);
-  // CTAs to a tile: more while all run at once and each still has eight blocks (4,096 x
-  // 7,168, one row: 18.2, 10.9, 6.4, 6.7 us with 1, 2, 4, 8; 7,168 x 2,048: 6.4, 4.7, 4.9),
-  // or four where the weights stream in ahead of the rows. At one CTA to an SM at most
-  // four: not every cluster of eight finds room (the shared expert of 64 rows: 32.1 us
-  // with gate/up tiles over 8, 23.5 over 4).
-  const int most = rows == 128 ? 4 : 8, least = a.weights_ready ? 4 : 8;
-  int split = 1;
-  while (split < most && tiles * split * 2 <= slots && Kb >= 2 * least * split) split *= 2;
-  if (rows == 128) {
-    // Both kernels' times by what they were measured to take, in hundredths of a us: here
-    // 30 a block and 500 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
-    // all, and 800 a wave where its output cannot go in whole pieces, as much again with an
-    // addend. (256 x 4,096 x 7,168: 15.2 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
-    // 7,168 x 2,048: 20.7 and 18.1; 600 x 2,047 x 2,048 with an addend: 13.9 and 26.7;
-    // 8,192 x 4,096 x 7,168: 630 estimated and 160. The SwiGLU form's two weight boxes
-    // count 45 a block here.)
-    const long long pairs = num_sms / 2;
-    const long long big = (static_cast<long long>(a.M) + 255) / 256 * (kSwiglu ? a.N / 128 : (a.N + 255) / 256);
-    const long long odd = kSwiglu || fp8_whole_pieces(a) ? 0 : a.add ? 1600 : 800;
-    const long long here = (tiles * split + slots - 1) / slots * ((kSwiglu ? 45LL : 30LL) * ((Kb + split - 1) / split) + 500) + 100;
-    const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120 + odd) + 300;
-    if (there < here) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
-  }
-  if (rows == 16) return launch_few<16, kSwiglu>(a, split, status, stream);
-  if (rows == 32) return launch_few<32, kSwiglu>(a, split, status, stream);
+  const long long pairs = num_sms / 2;
+  const long long big = (static_cast<long long>(a.M) + 255) / 256 * (kSwiglu ? a.N / 128 : (a.N + 255) / 256);
+  const long long odd = kSwiglu || fp8_whole_pieces(a) ? 0 : a.add ? 1600 : 800;
+  const long long here = waves * ((kSwiglu ? 45LL : 30LL) * share + 500) + 100;
+  const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120 + odd) + 300;
+  if (there < here) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
   return launch_few<128, kSwiglu>(a, split, status, stream);
 }
 }  // namespace
