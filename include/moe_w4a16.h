@@ -292,6 +292,13 @@ int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, cons
  * streams count once they have finished. */
 int moe_w4a16_fp8_status(int32_t* status, void* stream);
 
+/* Settings of the 8-bit products' pipeline waits, for the whole process; they hold for
+ * calls that begin after this one returns.
+ *   MOE_W4A16_FP8_OPT_WAIT_LIMIT_US             as MOE_W4A16_OPT_WAIT_LIMIT_US
+ *   MOE_W4A16_FP8_OPT_TEST_WAIT_NEVER_COMPLETES as MOE_W4A16_OPT_TEST_WAIT_NEVER_COMPLETES */
+enum { MOE_W4A16_FP8_OPT_WAIT_LIMIT_US = 1, MOE_W4A16_FP8_OPT_TEST_WAIT_NEVER_COMPLETES = 2 };
+int moe_w4a16_fp8_set_option(int option, int value);
+
 /* Shared expert: the dense SwiGLU feed-forward that every token takes next to its
  * routed experts, with 8-bit block-scaled weights and activations:
  *   q1, s1 = quantize(hidden)              [g | u] = q1 s1 . (w1 w1_s)^T   (fp32)

@@ -63,7 +63,7 @@ constexpr int kStages = 5;
 constexpr int kMax = kStages * kStageBytes;  // SwiGLU: the rows' maxima [tile parity][quarter][half][32]
 constexpr int kBars = kMax + 2 * 1024;
 constexpr int kSmem = kBars + 256 + 1024;
-static_assert(8 * (2 * kStages + 4 + 1 + 4) + 8 <= 256, "barriers");
+static_assert(8 * (2 * kStages + 4 + 1 + 4 + 1) + 8 <= 256, "barriers");
 
 // acc (two sums) += v (two block sums) * s
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tfull = [&](int i) { return base + kBars + 8 * (2 * kStages + i); };   // each CTA's
   auto tempty = [&](int i) { return base + kBars + 8 * (2 * kStages + 2 + i); };  // leader's: both CTAs' warps
   const uint32_t drain = base + kBars + 8 * (2 * kStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kBars + 8 * (2 * kStages + 9));
-  auto met = [&](int i) { return drain + 8 + 8 * i; };  // a row quarter's two warps have their maxima
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + kBars + 8 * (2 * kStages + 10));
+  const uint32_t never = drain + 8;                         // (the test hook's)
+  auto met = [&](int i) { return drain + 16 + 8 * i; };  // a row quarter's two warps have their maxima
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   const int tiles = mt * nt;
   const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
-  const uint32_t limit = kWaitLimitKCyclesDefault;
+  const uint32_t limit = a.wait_kcycles;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&amap);
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), 2 * kEpiWarps);
     mbar_init(drain, 1);
+    mbar_init(never, 1);
     for (int i = 0; i < 4; ++i) mbar_init(met(i), 2);
     *abort_flag = 0;
     fence_mbar_init();
@@ -355,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ac = 0;
     uint32_t aph = 0, met_ph = 0;
     bool ok = true;
+    if (a.test_never_wait) ok = __all_sync(0xffffffffu, mbar_wait(never, 0, abort_flag, status, kStatusTimeout, limit));
     for (int t = pair; t < tiles && ok; t += pairs) {
       int im, in;
       tile_at(t, mt, nt, &im, &in);

@@ -7,6 +7,8 @@
 // block of `b`. A block's products are summed in fp32 unscaled; the scaled block sums
 // are added in fp32 and rounded once to the output type.
 #include <cuda_bf16.h>
+#include <atomic>
+
 #include "fp8_quant.cuh"
 #include "fp8_tma.cuh"
 
@@ -134,7 +136,7 @@ struct Few {
   static constexpr int kBars = kScales + kW * kScaleBox * 4;
   static constexpr int kSmem = kBars + 512 + 1024;
   static constexpr int kPart = kRows * 512;  // partial sums of a box
-  static_assert(kStages >= 2 && 8 * (2 * kStages + 2 * kAccs + 1) + 8 <= 512, "barriers");
+  static_assert(kStages >= 2 && 8 * (2 * kStages + 2 * kAccs + 2) + 8 <= 512, "barriers");
   static_assert(kStages * kStageBytes >= kW * kPart, "the partial sums fit the stages");
 };
 
@@ -227,7 +229,8 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
   auto tfull = [&](int i) { return base + L::kBars + 8 * (2 * L::kStages + i); };
   auto tempty = [&](int i) { return base + L::kBars + 8 * (2 * L::kStages + L::kAccs + i); };
   const uint32_t drain = base + L::kBars + 8 * (2 * L::kStages + 2 * L::kAccs);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kBars + 8 * (2 * L::kStages + 2 * L::kAccs + 1));
+  const uint32_t never = drain + 8;  // (the test hook's)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kBars + 8 * (2 * L::kStages + 2 * L::kAccs + 2));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   constexpr int kWarpTma = L::kEpiWarps, kWarpMma = L::kEpiWarps + 1;
 
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
   const int kb0 = static_cast<int>(static_cast<long long>(Kb) * rank / split);
   const int kb1 = static_cast<int>(static_cast<long long>(Kb) * (rank + 1) / split);
   constexpr uint32_t bytes = L::kStageBytes;
-  const uint32_t limit = kWaitLimitKCyclesDefault;
+  const uint32_t limit = a.wait_kcycles;
 
   if (threadIdx.x == 0) {
     tma_prefetch_map(&wmap);
@@ -248,6 +251,7 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
     for (int i = 0; i < L::kStages; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
     for (int i = 0; i < L::kAccs; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), L::kEpiWarps);
     mbar_init(drain, 1);
+    mbar_init(never, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
     int ac = 0;
     uint32_t aph = 0;
     bool ok = true;  // (a warp that gave up goes on without sums: the others meet it at the barrier)
+    if (a.test_never_wait) ok = __all_sync(0xffffffffu, mbar_wait(never, 0, abort_flag, status, kStatusTimeout, limit));
     for (int kb = kb0; kb < kb1; ++kb) {
       const int at = (kb - kb0) % L::kScaleRun;
       if (at == 0) {  // both scales of the next blocks, multiplied
@@ -558,9 +563,14 @@ cudaError_t launch_split(const Fp8MatmulArgs& a, int32_t* status, int num_sms, c
   return e == cudaSuccess ? launch_few<kRows, kSwiglu>(a, split, status, stream) : e;
 }
 
+// Settings of the whole process (moe_w4a16_fp8_set_option).
+std::atomic<int> g_wait_us{0}, g_test_never_wait{0};
+
 // Kernel and split by size.
 template <bool kSwiglu>
-cudaError_t launch_tiles(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
+cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStream_t stream) {
+  a.wait_kcycles = wait_limit_kcycles(static_cast<unsigned long long>(g_wait_us.load(std::memory_order_relaxed)));
+  a.test_never_wait = g_test_never_wait.load(std::memory_order_relaxed);
   if (a.M <= 16) return launch_split<16, kSwiglu>(a, status, num_sms, stream);
   if (a.M <= 32) return launch_split<32, kSwiglu>(a, status, num_sms, stream);
   int split = 1, share = 0;
@@ -601,6 +611,16 @@ cudaError_t launch_fp8_swiglu(const Fp8MatmulArgs& a, int num_sms, cudaStream_t 
   int32_t* status = fp8_status_word();
   if (!status) return cudaErrorInvalidSymbol;
   return launch_tiles<true>(a, status, num_sms, stream);
+}
+
+bool fp8_set_option(int option, int value) {
+  if (option == 1 && value >= 0)
+    g_wait_us.store(value);
+  else if (option == 2 && (value == 0 || value == 1))
+    g_test_never_wait.store(value);
+  else
+    return false;
+  return true;
 }
 
 int32_t* fp8_status_word() {

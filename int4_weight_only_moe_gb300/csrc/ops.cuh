@@ -62,12 +62,17 @@ struct Fp8MatmulArgs {
   int M, N, K;
   bool weights_ready;   // `b` and `b_s` were written before the kernel in front of this one began
   float* out_s;         // SwiGLU form: scales [M, N / 128] of `out`, which is e4m3 [M, N]
+  uint32_t wait_kcycles;  // longest pipeline wait in units of 1,024 cycles, and the test hook: the
+  int test_never_wait;    // sums first wait for what never comes (both set at launch)
 };
 // The SwiGLU form: `b` has 2 N rows, gate then up (N a multiple of 128), and the output is
 // SiLU(gate) * up, quantised.
 cudaError_t launch_fp8_swiglu(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
 
+// Settings of the products' pipeline waits (MOE_W4A16_FP8_OPT_*); false: no such option
+// or value.
+bool fp8_set_option(int option, int value);
 // Status word of the products (MOE_W4A16_STATUS_TIMEOUT when a wait gave up); clears it.
 cudaError_t fp8_status(int32_t* out, cudaStream_t stream);
 

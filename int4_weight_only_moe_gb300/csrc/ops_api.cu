@@ -126,8 +126,12 @@ int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, cons
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
-  Fp8MatmulArgs g{a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K, false, nullptr};
+  Fp8MatmulArgs g{a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K, false, nullptr, 0, 0};
   return done(launch_fp8_matmul(g, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_w4a16_fp8_set_option(int option, int value) {
+  return fp8_set_option(option, value) ? MOE_W4A16_OK : bad("unknown option, or a value out of its range");
 }
 
 int moe_w4a16_fp8_status(int32_t* status, void* stream) {
@@ -185,9 +189,9 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
   float* s2 = reinterpret_cast<float*>(ws + L.s2);
   e = launch_quantize(QuantArgs{hidden, kTypeBf16, K, M, K, q1, s1}, false, s);
   if (e == cudaSuccess)
-    e = launch_fp8_swiglu(Fp8MatmulArgs{q1, K, s1, w1, K, w1_s, nullptr, q2, kTypeF32, M, N, K, true, s2}, sms, s);
+    e = launch_fp8_swiglu(Fp8MatmulArgs{q1, K, s1, w1, K, w1_s, nullptr, q2, kTypeF32, M, N, K, true, s2, 0, 0}, sms, s);
   if (e == cudaSuccess)
-    e = launch_fp8_matmul(Fp8MatmulArgs{q2, N, s2, w2, N, w2_s, add, out, kTypeBf16, M, K, N, true, nullptr}, sms, s);
+    e = launch_fp8_matmul(Fp8MatmulArgs{q2, N, s2, w2, N, w2_s, add, out, kTypeBf16, M, K, N, true, nullptr, 0, 0}, sms, s);
   return done(e);
 }
 

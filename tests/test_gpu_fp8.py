@@ -335,3 +335,30 @@ def test_shared_expert_replays_from_a_cuda_graph():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, fp8.shared_expert(x, *w))
+
+
+# ------------------------------------------------------------------------------- give-up
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 512, 2048), (20, 512, 2048), (100, 256, 1024), (1200, 2048, 1024)])
+def test_wait_limit_gives_up_cleanly(M, N, K):
+    """A wait that nothing completes runs out: the call returns, the status says so, and the
+    next call is right (one size for each kernel)."""
+    import int4_weight_only_moe_gb300 as pkg
+    ops = operands(M, N, K, M)
+    x, w = rand((M, K), 1), expert(K, N, 2)
+    want, whole = fp8.matmul(*ops), fp8.shared_expert(x, *w)
+    assert fp8.status() == 0
+    pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, 1000)
+    pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_TEST_WAIT_NEVER_COMPLETES, 1)
+    try:
+        fp8.matmul(*ops)
+        assert fp8.status() == pkg.STATUS_TIMEOUT
+        fp8.shared_expert(x, *w)
+        assert fp8.status() == pkg.STATUS_TIMEOUT
+    finally:
+        pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_TEST_WAIT_NEVER_COMPLETES, 0)
+        pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, 0)
+    assert fp8.status() == 0
+    assert torch.equal(fp8.matmul(*ops), want) and torch.equal(fp8.shared_expert(x, *w), whole)
+    assert fp8.status() == 0

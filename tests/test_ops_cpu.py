@@ -130,6 +130,11 @@ def test_shared_expert_refusals(lib):
         assert lib.moe_w4a16_shared_expert(*args) == rc, (at, value)
 
 
+def test_set_option_refusals(lib):
+    for option, value, rc in [(0, 0, INVALID), (3, 1, INVALID), (1, -1, INVALID), (2, 2, INVALID), (1, 0, OK), (2, 0, OK)]:
+        assert lib.moe_w4a16_fp8_set_option(option, value) == rc
+
+
 def test_python_calls_refuse_host_tensors_and_shapes():
     import torch
     from int4_weight_only_moe_gb300 import fp8, routing
