@@ -85,10 +85,11 @@ constexpr int kThreads = 256;
 constexpr int kPerCta = kThreads / kLanes;  // blocks, or rows of a weight block
 
 // kLanes threads to a block of 128 columns, kLane values each. Bound by memory: 8,191 x
-// 2,048 SwiGLU pairs (84 MB) in 15.0 us, 5.6 TB/s; with
-// full-precision exponentials and divisions, eight values a thread, 28 us, by its instructions.
+// 2,048 SwiGLU pairs (84 MB) in 14.4 us, 5.9 TB/s (15.2 with 6 CTAs to an SM instead of
+// 8). With full-precision exponentials and divisions and eight values a thread its
+// instructions bound it: 28 us.
 template <bool kSwiglu, bool kVec, typename T>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(QuantArgs a, uint32_t blocks) {
+__global__ void __launch_bounds__(kThreads, 8) quantize_kernel(QuantArgs a, uint32_t blocks) {
   pdl_wait();
   pdl_launch_dependents();
   const uint32_t nb = (a.N + kScaleBlock - 1) / kScaleBlock;

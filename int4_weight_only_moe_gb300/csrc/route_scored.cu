@@ -16,7 +16,7 @@
 // n_group lanes to a group), so that lower lane, then lower slot, is the lower id: the
 // tie rule costs nothing. The lanes' best, sorted, give a bound that leaves little more
 // than topk candidates; those move one to a lane and count the better ones. Bound by
-// its instructions: 16,384 tokens of 384 experts, top-8, take 13.0 us (26 MB of logits
+// its instructions: 16,384 tokens of 384 experts, top-8, take 12.6 us (26 MB of logits
 // could be read in 3.9); with topk rounds of a warp-wide maximum instead, 16.5.
 //
 // All arithmetic is fp32. The selection's scores come from the hardware's exponential and
@@ -29,7 +29,7 @@
 namespace moe {
 namespace {
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 128;
 
 // Order-preserving map of a float to an unsigned integer, and back; NaN ranks as
 // -infinity. 0 is below every value: no candidate. (A choice is never -0: scores are
@@ -98,8 +98,10 @@ __device__ __forceinline__ Best2 run_best2(F key) {
 
 // C: slots of a lane, a multiple of 4 (the run length c <= C). `vec`: rows, runs and the
 // bias allow loads of four values.
+// (The warps an SM holds hide the selection's chain of exchanges: 64 of them for runs of up
+// to 8 -- 4,097 x 160 takes 4.9 us, 6.8 with the registers left free -- 48 and 40 up to 16.)
 template <int C, bool kSoftmax, typename T>
-__global__ void __launch_bounds__(kRouteThreads) route_scored_kernel(RouteScoredArgs a, int P, int c, bool vec) {
+__global__ void __launch_bounds__(kRouteThreads, C <= 8 ? 16 : C <= 12 ? 12 : C <= 16 ? 10 : 1) route_scored_kernel(RouteScoredArgs a, int P, int c, bool vec) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
