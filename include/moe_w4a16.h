@@ -307,10 +307,12 @@ int moe_w4a16_fp8_set_option(int option, int value);
  *   w2 [K, N], w2_s [K/128, N/128];  add bf16 [M, K] (the routed experts' output) or
  *   NULL, may be `out`;  out bf16 [M, K];  all contiguous, w1 and w2 16-byte aligned
  *   workspace  >= moe_w4a16_shared_expert_workspace_size(M, K, N) bytes (0 for a shape
- *   that is not supported), 256-byte aligned; holds nothing between calls
+ *   that is not supported), 256-byte aligned; holds nothing between calls. NULL: the call
+ *   takes and returns it in stream order from a memory pool of the library's own, which
+ *   keeps up to 64 MiB (workspace_bytes is then not looked at)
  * K % 128 == 0, N % 128 == 0. M == 0 is a no-op. Three launches on `stream` (quantise;
- * gate/up product, SwiGLU and quantise; down product), allocates nothing, no host
- * synchronisation. */
+ * gate/up product, SwiGLU and quantise; down product), with a workspace allocates
+ * nothing, no host synchronisation. */
 size_t moe_w4a16_shared_expert_workspace_size(int M, int K, int N);
 int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const float* w1_s, const uint8_t* w2,
                             const float* w2_s, const uint16_t* add, uint16_t* out, int M, int K, int N,

@@ -1,4 +1,6 @@
 // C entry points of the operators around the routed experts: argument checks and launches.
+#include <atomic>
+
 #include "../../include/moe_w4a16.h"
 #include "ops.cuh"
 
@@ -33,6 +35,42 @@ int num_sms(cudaError_t* err) {
   *err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   if (*err == cudaSuccess && keep) cached[dev] = n;
   return n;
+}
+
+// Stream-ordered memory pool of the current device, for calls without a workspace; keeps
+// up to 64 MiB between calls.
+cudaMemPool_t scratch_pool(cudaError_t* err) {
+  static std::atomic<cudaMemPool_t> pools[64];
+  int dev = 0;
+  *err = cudaGetDevice(&dev);
+  if (*err != cudaSuccess) return nullptr;
+  if (dev < 0 || dev >= 64) {
+    *err = cudaErrorInvalidDevice;
+    return nullptr;
+  }
+  cudaMemPool_t pool = pools[dev].load();
+  if (pool) return pool;
+  // (also during a stream capture, which this touches nothing of)
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  *err = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (*err != cudaSuccess) return nullptr;
+  cudaMemPoolProps props = {};
+  props.allocType = cudaMemAllocationTypePinned;
+  props.location.type = cudaMemLocationTypeDevice;
+  props.location.id = dev;
+  *err = cudaMemPoolCreate(&pool, &props);
+  if (*err == cudaSuccess) {
+    unsigned long long keep = 64ull << 20;
+    *err = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    cudaMemPool_t none = nullptr;
+    if (*err != cudaSuccess || !pools[dev].compare_exchange_strong(none, pool)) {
+      cudaMemPoolDestroy(pool);
+      pool = *err == cudaSuccess ? none : nullptr;  // (another thread's)
+    }
+  }
+  const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+  if (*err == cudaSuccess) *err = back;
+  return *err == cudaSuccess ? pool : nullptr;
 }
 
 int check_quant(const void* x, int x_type, long long row_stride, int M, int cols, int width, const void* q,
@@ -170,19 +208,25 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
   if (!shared_shape_ok(M, K, N))
     return shape("need 0 <= M <= 2^30 and K, N positive multiples of 128 (at most 2^22 and 2^21)");
   if (M == 0) return MOE_W4A16_OK;
-  if (!hidden || !w1 || !w1_s || !w2 || !w2_s || !out || !workspace) return bad("null pointer argument");
+  if (!hidden || !w1 || !w1_s || !w2 || !w2_s || !out) return bad("null pointer argument");
   if (misaligned(workspace, 256)) return bad("workspace must be 256-byte aligned");
   if (misaligned(w1, 16) || misaligned(w2, 16)) return bad("w1 and w2 must be 16-byte aligned");
   if (misaligned(hidden, 2) || misaligned(w1_s, 4) || misaligned(w2_s, 4) || misaligned(add, 2) || misaligned(out, 2))
     return bad("a pointer is not aligned to its type");
   const SharedLayout L = shared_layout(M, K, N);
-  if (workspace_bytes < L.total)
+  if (workspace && workspace_bytes < L.total)
     return report_error(MOE_W4A16_WORKSPACE_TOO_SMALL, "workspace too small (moe_w4a16_shared_expert_workspace_size)");
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
   auto s = static_cast<cudaStream_t>(stream);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  void* scratch = nullptr;
+  if (!workspace) {
+    cudaMemPool_t pool = scratch_pool(&e);
+    if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&scratch, L.total, pool, s);
+    if (e != cudaSuccess) return done(e);
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace ? workspace : scratch);
   uint8_t* q1 = ws + L.q1;
   uint8_t* q2 = ws + L.q2;
   float* s1 = reinterpret_cast<float*>(ws + L.s1);
@@ -192,6 +236,10 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
     e = launch_fp8_swiglu(Fp8MatmulArgs{q1, K, s1, w1, K, w1_s, nullptr, q2, kTypeF32, M, N, K, true, s2, 0, 0}, sms, s);
   if (e == cudaSuccess)
     e = launch_fp8_matmul(Fp8MatmulArgs{q2, N, s2, w2, N, w2_s, add, out, kTypeBf16, M, K, N, true, nullptr, 0, 0}, sms, s);
+  if (scratch) {
+    const cudaError_t freed = cudaFreeAsync(scratch, s);
+    if (e == cudaSuccess) e = freed;
+  }
   return done(e);
 }
 

@@ -82,6 +82,7 @@ def matmul(a, a_s, b, b_s, add=None, out=None, out_dtype=torch.bfloat16, stream=
     return out
 
 
+_POOL_BYTES = 16 << 20
 _workspace_size = functools.lru_cache(maxsize=256)(moe_w4a16_shared_expert_workspace_size)
 
 
@@ -90,9 +91,10 @@ def shared_expert(hidden, w1, w1_s, w2, w2_s, add=None, out=None, workspace=None
     routed experts' output): bf16 [M, K].
 
     ``w1`` [2 N, K] holds the gate rows, then the up rows, ``w2`` [K, N] the down
-    projection. ``workspace`` (uint8, of
-    ``moe_w4a16_shared_expert_workspace_size(M, K, N)`` bytes) is allocated where it is not
-    given.
+    projection. ``workspace``: uint8, of
+    ``moe_w4a16_shared_expert_workspace_size(M, K, N)`` bytes; where it is not given, up to
+    16 MiB come from the library's stream-ordered pool (a third of the time of a tensor's
+    allocation, which a small batch's call would wait for), more from torch.
     """
     M, K = shape = hidden.shape
     N = w2.shape[1]
@@ -104,10 +106,10 @@ def shared_expert(hidden, w1, w1_s, w2, w2_s, add=None, out=None, workspace=None
     if out is None:
         out = _new(shape, torch.bfloat16, hidden, stream)
     y = _dense(out, torch.bfloat16, shape, "out")
-    if workspace is None:
-        workspace = _new((max(_workspace_size(M, K, N), 1),), torch.uint8, hidden, stream)
-    _check(lib().moe_w4a16_shared_expert(x, *weights, plus, y, M, K, N, workspace.data_ptr(), workspace.nbytes,
-                                         _handle(stream, hidden)))
+    if workspace is None and (need := _workspace_size(M, K, N)) > _POOL_BYTES:
+        workspace = _new((need,), torch.uint8, hidden, stream)
+    ws, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
+    _check(lib().moe_w4a16_shared_expert(x, *weights, plus, y, M, K, N, ws, size, _handle(stream, hidden)))
     return out
 
 

@@ -321,6 +321,24 @@ def test_shared_expert_workspace_stream_and_empty():
         fp8.shared_expert(x, *w, workspace=ws[:-1])
 
 
+def test_shared_expert_takes_its_workspace_from_the_pool_or_torch():
+    # (below and above the pool's limit; calls in flight on two streams do not share it)
+    from int4_weight_only_moe_gb300 import moe_w4a16_shared_expert_workspace_size as size
+    K, N = 2048, 256
+    w = expert(K, N, 5)
+    for M in (64, 9000):
+        assert (size(M, K, N) > fp8._POOL_BYTES) == (M == 9000)
+        x, y = rand((M, K), 1), rand((M, K), 2)
+        ws = torch.empty(size(M, K, N), dtype=torch.uint8, device="cuda")
+        want = [fp8.shared_expert(t, *w, workspace=ws).clone() for t in (x, y)]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        got = [[fp8.shared_expert(t, *w, stream=s) for t, s in zip((x, y), streams)] for _ in range(8)]
+        torch.cuda.synchronize()
+        for pair in got:
+            assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+
+
 def test_shared_expert_replays_from_a_cuda_graph():
     K, N = 512, 256
     w = expert(K, N, 4)

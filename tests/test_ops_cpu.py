@@ -122,7 +122,7 @@ def test_shared_expert_refusals(lib):
     assert need > 0 and size(8, 256, 128) >= need
     assert size(-1, 256, 128) == 0 and size(4, 200, 128) == 0 and size(4, 256, 96) == 0
     good = [BUF, BUF, BUF, BUF, BUF, None, BUF, 4, 256, 128, BUF, need, None]
-    for at, value, rc in [(i, None, INVALID) for i in (0, 1, 2, 3, 4, 6, 10)] + [
+    for at, value, rc in [(i, None, INVALID) for i in (0, 1, 2, 3, 4, 6)] + [
             (7, -1, SHAPE), (8, 200, SHAPE), (9, 96, SHAPE), (8, 0, SHAPE), (11, need - 1, WORKSPACE),
             (10, ctypes.c_void_p(272), INVALID), (2, ctypes.c_void_p(258), INVALID), (7, 0, OK)]:
         args = list(good)
