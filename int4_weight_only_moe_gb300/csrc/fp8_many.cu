@@ -22,7 +22,8 @@
 //
 // Warps: 0..7 sums and output, 8 copies (one lane of each CTA, both counting on the
 // leader's barriers), 9 the MMAs (the leader's), 10 and 11 idle. Persistent: a pair
-// takes every (number of pairs)-th tile. 8,192 x 4,096 x 7,168: 161 us, 2,990 TFLOP/s.
+// takes every (number of pairs)-th tile. 8,192 x 4,096 x 7,168: 160 to 164 us, 3,000
+// TFLOP/s (185 us in a loop of seconds, at the power limit).
 #include <cuda_bf16.h>
 
 #include "fp8_quant.cuh"
