@@ -355,12 +355,18 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
           float sb[L::kW];
 #pragma unroll
           for (int w = 0; w < L::kW; ++w) sb[w] = a.b_s[static_cast<long long>((n0 + w * a.N) / kScaleBlock) * Kb + kb + lane];
-#pragma unroll 4
-          for (int j = warp; j < kRows; j += L::kEpiWarps) {
-            const float sa = j < rows ? a.a_s[(m0 + j) * Kb + kb + lane] : 0.f;
+          constexpr int kEach = kRows / L::kEpiWarps;
+          float sa[kEach];  // (all loads before the first store: one latency)
 #pragma unroll
-            for (int w = 0; w < L::kW; ++w) scales[w * L::kScaleBox + lane * L::kScaleRow + j] = sa * sb[w];
+          for (int i = 0; i < kEach; ++i) {
+            const int j = warp + i * L::kEpiWarps;
+            sa[i] = j < rows ? a.a_s[(m0 + j) * Kb + kb + lane] : 0.f;
           }
+#pragma unroll
+          for (int i = 0; i < kEach; ++i)
+#pragma unroll
+            for (int w = 0; w < L::kW; ++w)
+              scales[w * L::kScaleBox + lane * L::kScaleRow + warp + i * L::kEpiWarps] = sa[i] * sb[w];
         }
         named_bar_sync(1, L::kEpiThreads);
       }
