@@ -34,8 +34,9 @@ __global__ void __launch_bounds__(256) fp8_matmul_plain_kernel(Fp8MatmulArgs a) 
   pdl_wait();
   pdl_launch_dependents();
   __shared__ float sa[kStep][kT + 1], sb[kStep][kT + 1];
-  const long long m0 = static_cast<long long>(blockIdx.x) * kT;
-  const int n0 = blockIdx.y * kT;
+  const uint32_t tiles_m = (static_cast<uint32_t>(a.M) + kT - 1) / kT;
+  const long long m0 = static_cast<long long>(blockIdx.x % tiles_m) * kT;
+  const long long n0 = static_cast<long long>(blockIdx.x / tiles_m) * kT;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   float acc[4][4] = {};
@@ -68,8 +69,8 @@ __global__ void __launch_bounds__(256) fp8_matmul_plain_kernel(Fp8MatmulArgs a) 
       const float s = m < a.M ? a.a_s[m * Kb + kb] : 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx + 16 * j;
-        if (n < a.N) acc[i][j] = fmaf(part[i][j], s * a.b_s[static_cast<long long>(n / kScaleBlock) * Kb + kb], acc[i][j]);
+        const long long n = n0 + tx + 16 * j;
+        if (n < a.N) acc[i][j] = fmaf(part[i][j], s * a.b_s[n / kScaleBlock * Kb + kb], acc[i][j]);
       }
     }
   }
@@ -78,7 +79,7 @@ __global__ void __launch_bounds__(256) fp8_matmul_plain_kernel(Fp8MatmulArgs a) 
     const long long m = m0 + ty + 16 * i;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx + 16 * j;
+      const long long n = n0 + tx + 16 * j;
       if (m < a.M && n < a.N) store_out(a, m * a.N + n, acc[i][j]);
     }
   }
@@ -86,17 +87,18 @@ __global__ void __launch_bounds__(256) fp8_matmul_plain_kernel(Fp8MatmulArgs a) 
 
 // ---------------------------------------------------------------- few rows
 //
-// A batch of few rows reads every weight once and does little with it. Up to 32 rows the
-// weights are the MMA's 128 rows (M) and the batch its columns (N = 16 or 32), so one
+// A batch of few rows reads every weight once and does little with it. Up to 64 rows the
+// weights are the MMA's 128 rows (M) and the batch its columns (N = 16, 32 or 64), so one
 // token costs 16 columns, not 128 rows, and a thread sums one weight row over the batch.
-// From 33 rows on the batch is the MMA's 128 rows and 128 weights its columns: a thread
+// From 65 rows on the batch is the MMA's 128 rows and 128 weights its columns: a thread
 // sums one batch row, whose scale is one number a block (with the weights as rows it has
-// one for each column, and 128 columns took 850 cycles a block). A tile's reduction is
-// split over the CTAs of a cluster, so that every SM streams weights; the fp32 partial
-// sums meet in distributed shared memory and are added in the order of the ranks (the
-// same result every time).
+// one for each column, and 128 columns took 850 cycles a block; 64 columns pay: 33 x 7,168
+// x 2,048 takes 6.5 us, 7.6 with the batch as rows). A tile's reduction is split over the
+// CTAs of a cluster, so that every SM streams weights; the fp32 partial sums meet in
+// distributed shared memory and are added in the order of the ranks (the same result every
+// time). Sent by bulk copies instead of read where they are added they took 0.3 us longer.
 //
-// Warps of a CTA: the first four (eight for 128 columns, half of the columns each) take
+// Warps of a CTA: the first four (eight from 64 rows on, half of the columns each) take
 // the block sums out of tensor memory, scale them and add them to the running sums in
 // registers; then one that copies (one lane; a stage is 128 x 128 weight bytes and the
 // batch's 128 bytes per row) and one that issues the MMAs (four of 32 reduction elements
@@ -110,22 +112,24 @@ constexpr int kMaxStages = 10;
 
 __device__ int32_t g_fp8_status;
 
-template <int kRows, bool kSwiglu>  // batch rows of a tile: 16, 32 or 128
+template <int kRows, bool kSwiglu>  // batch rows of a tile: 16, 32, 64 or 128
 struct Few {
   static constexpr bool kBatchIsM = kRows == 128;
   static constexpr int kW = kSwiglu ? 2 : 1;               // weight boxes
   static constexpr int kBoxCols = kBatchIsM ? 128 : kRows;  // accumulator columns of a box
   static constexpr int kAccCols = kW * kBoxCols;
-  static constexpr int kAccs = 4 * kAccCols <= 512 ? 4 : 512 / kAccCols;
+  // CTAs to an SM, by registers and shared memory
+  static constexpr int kPerSm = kBatchIsM || (kRows == 64 && kSwiglu) ? 1 : 2;
+  static constexpr int kCols = 512 / kPerSm;  // of tensor memory
+  static constexpr int kAccs = 4 * kAccCols <= kCols ? 4 : kCols / kAccCols;
   static constexpr int kTmem = kAccs * kAccCols;
-  static constexpr int kEpiWarps = kBatchIsM ? 8 : 4;
+  static constexpr int kEpiWarps = kRows >= 64 ? 8 : 4;
   static constexpr int kEpiThreads = kEpiWarps * 32;
   static constexpr int kThreads = kEpiThreads + 64;
   static constexpr int kMine = kBoxCols / (kEpiWarps / 4);  // columns of a box for a thread
   static constexpr int kPiece = kMine < 32 ? kMine : 32;
   static constexpr int kStageBytes = kW * kWTile + kRows * 128;
-  // two CTAs to an SM up to 32 rows
-  static constexpr int kRoom = (kBatchIsM ? 226 : 113) * 1024;
+  static constexpr int kRoom = 226 * 1024 / kPerSm;
   static constexpr int kScaleRun = kBatchIsM && kSwiglu ? 16 : 32;  // blocks whose scales are staged at a time
   static constexpr int kScaleRow = kRows + 4;  // (padded: the staging's stores spread over the banks)
   static constexpr int kScaleBox = kScaleRun * kScaleRow;
@@ -381,7 +385,7 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
         for (int c = 0; c < L::kMine / L::kPiece; ++c) {
           uint32_t v[L::kPiece];
           tmem_piece(src0 + ac * L::kAccCols + w * L::kBoxCols + c * L::kPiece, v);
-          const float4* sc = reinterpret_cast<const float4*>(table + c * L::kPiece);
+          const float4* sc = reinterpret_cast<const float4*>(table + c0 + c * L::kPiece);
           tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < L::kPiece / 4; ++q) {
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
       } else {
 #pragma unroll
         for (int j = 0; j < L::kMine; ++j)
-          if (j < rows) *reinterpret_cast<float*>(part + part_at(j, row / 4) + (row & 3) * 4) = acc[w][j];
+          if (c0 + j < rows) *reinterpret_cast<float*>(part + part_at(c0 + j, row / 4) + (row & 3) * 4) = acc[w][j];
       }
     }
   }
@@ -483,8 +487,8 @@ cudaError_t clusters_at_once(int split, int num_sms, int* clusters) {
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_few_kernel<kRows, kSwiglu>, &cfg);
     if (e != cudaSuccess) return e;
-    // (the query counts one CTA to an SM; up to 32 rows two run there)
-    known[split] = (n < 1 ? 1 : n) * (L::kBatchIsM ? 1 : 2);
+    // (the query counts one CTA to an SM)
+    known[split] = (n < 1 ? 1 : n) * L::kPerSm;
   }
   *clusters = known[split];
   return cudaSuccess;
@@ -579,16 +583,19 @@ cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStre
   a.test_never_wait = g_test_never_wait.load(std::memory_order_relaxed);
   if (a.M <= 16) return launch_split<16, kSwiglu>(a, status, num_sms, stream);
   if (a.M <= 32) return launch_split<32, kSwiglu>(a, status, num_sms, stream);
+  if (a.M <= 64) return launch_split<64, kSwiglu>(a, status, num_sms, stream);
   int split = 1, share = 0;
   long long waves = 0;
   const cudaError_t e = choose_split<128, kSwiglu>(a, num_sms, &split, &share, &waves);
   if (e != cudaSuccess) return e;
   // Both kernels' times by what they were measured to take, in hundredths of a us: here
-  // 30 a block and 500 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
+  // 30 a block and 400 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
   // all, and 800 a wave where its output cannot go in whole pieces, as much again with an
-  // addend. (256 x 4,096 x 7,168: 15.2 us here, 23.9 there; 512 rows 23.9 and 24.5; 600 x
-  // 7,168 x 2,048: 20.7 and 18.1; 600 x 2,047 x 2,048 with an addend: 13.9 and 26.7;
-  // 8,192 x 4,096 x 7,168: 630 estimated and 160. The SwiGLU form's two weight boxes
+  // addend. (256 x 4,096 x 7,168: 14.2 us here, 24.4
+  // there; 512 rows 22.4 and 24.6; 640 x 7,168 x 2,048: 19.2 and 18.5; 2,048 x 1,000 x
+  // 1,936 in fp32: 10.8 and 11.1; 600 x 2,047 x 2,048 with an addend: 13.9 and 26.7; 2,048
+  // x 4,096 x 7,168: 88.7 and 47.7. Of 77 sizes two were chosen 6% too slow.)
+  // (The SwiGLU form's two weight boxes
   // count 45 a block here.)
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   const long long pairs = num_sms / 2;
@@ -596,14 +603,15 @@ cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStre
   const long long odd = kSwiglu || fp8_whole_pieces(a) ? 0 : a.add ? 1600 : 800;
   const long long here = waves * ((kSwiglu ? 45LL : 30LL) * share + 500) + 100;
   const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120 + odd) + 300;
-  if (there < here) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
+  // (a grid's second dimension ends at 65,535 tiles of 128 rows)
+  if (there < here || a.M > 65535LL * 128) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
   return launch_few<128, kSwiglu>(a, split, status, stream);
 }
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream) {
   if (!tma_ok(a)) {
-    const dim3 grid((a.M + kT - 1) / kT, (a.N + kT - 1) / kT);
+    const dim3 grid(static_cast<unsigned>((a.M + kT - 1LL) / kT * ((a.N + kT - 1LL) / kT)));
     return launch_k(fp8_matmul_plain_kernel, grid, dim3(256), 0, stream, true, a);
   }
   int32_t* status = fp8_status_word();

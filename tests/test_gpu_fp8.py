@@ -195,6 +195,28 @@ def test_product_strides_and_alignment():
         assert not buf[:off].any() and not buf[off + 70 * 300:].any()
 
 
+@pytest.mark.parametrize("M", [33, 40, 49, 64, 65])
+def test_product_of_33_to_64_rows(M):
+    for N, K in ((130, 144), (700, 640), (1152, 2048), (7168, 256)):
+        ops = operands(M, N, K, 3 * M)
+        add = rand((M, N), 5)
+        check_product(fp8.matmul(*ops, add=add), *ops, add=add)
+    w, x = expert(1024, 384, M), rand((M, 1024), 2)
+    assert_close(bf16_tensor_to_f64(fp8.shared_expert(x, *w)), expert_reference(x, w), "shared expert")
+
+
+@pytest.mark.parametrize("M,N,K", [(65535 * 128 + 5, 1, 16), (1, 65535 * 64 + 5, 8)])
+def test_product_with_more_tiles_than_a_grid_dimension(M, N, K):
+    # (small whole numbers: every sum is exact)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = torch.randint(-4, 5, (M, K), generator=g, device="cuda").float()
+    b = torch.randint(-4, 5, (N, K), generator=g, device="cuda").float()
+    a_s = torch.ones(M, 1, device="cuda")
+    b_s = torch.full(((N + 127) // 128, 1), 0.5, device="cuda")
+    out = fp8.matmul(a.to(torch.float8_e4m3fn), a_s, b.to(torch.float8_e4m3fn), b_s, out_dtype=torch.float32)
+    assert torch.equal(out.view(-1), (a * b).sum(1) * 0.5)
+
+
 @pytest.mark.parametrize("M,N", [(3, 256), (90, 700), (600, 512)])
 def test_add_in_place(M, N):
     ops = operands(M, N, 640, 9)
@@ -358,7 +380,7 @@ def test_shared_expert_replays_from_a_cuda_graph():
 # ------------------------------------------------------------------------------- give-up
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 512, 2048), (20, 512, 2048), (100, 256, 1024), (1200, 2048, 1024)])
+@pytest.mark.parametrize("M,N,K", [(4, 512, 2048), (20, 512, 2048), (50, 512, 2048), (100, 256, 1024), (1200, 2048, 1024)])
 def test_wait_limit_gives_up_cleanly(M, N, K):
     """A wait that nothing completes runs out: the call returns, the status says so, and the
     next call is right (one size for each kernel)."""
