@@ -60,11 +60,21 @@ constexpr int kHalf = 128;                 // rows, and features, of a CTA
 constexpr int kSums = kTileN / 2;          // of a thread: one row, 128 features
 constexpr int kOperand = 128 * 128;        // bytes of a box
 constexpr int kStageBytes = 2 * kOperand;
-constexpr int kStages = 5;
-constexpr int kMax = kStages * kStageBytes;  // SwiGLU: the rows' maxima [tile parity][quarter][half][32]
+// Where the sums go: whole 32-byte pieces of a row, any alignment (without and with
+// addends, for whose registers the sums of the one would pay), or SwiGLU and e4m3.
+enum Out { kOutPieces, kOutAcross, kOutAcrossAdd, kOutSwiglu };
+__host__ __device__ constexpr bool across(Out out) { return out == kOutAcross || out == kOutAcrossAdd; }
+// Shared memory: maxima, barriers, stages, and for any alignment a tile of 32 rows x 65
+// sums for each summing warp, which costs a stage.
+__host__ __device__ constexpr int stages(Out out) { return across(out) ? 4 : 5; }
+constexpr int kMax = 0;  // SwiGLU: the rows' maxima [tile parity][quarter][half][32]
 constexpr int kBars = kMax + 2 * 1024;
-constexpr int kSmem = kBars + 256 + 1024;
-static_assert(8 * (2 * kStages + 4 + 1 + 4 + 1) + 8 <= 256, "barriers");
+constexpr int kStage0 = 3 * 1024;
+constexpr int kWide = 64, kAcrossWarp = 32 * (kWide + 1) * 4;
+__host__ __device__ constexpr int across_at(Out out) { return kStage0 + stages(out) * kStageBytes; }
+__host__ __device__ constexpr int smem_bytes(Out out) { return across_at(out) + (across(out) ? kEpiWarps * kAcrossWarp : 0) + 1024; }
+static_assert(kBars + 8 * (2 * 5 + 4 + 1 + 4 + 1) + 8 <= kStage0, "barriers");
+static_assert(smem_bytes(kOutAcross) <= 227 * 1024, "shared memory of a CTA");
 
 // acc (two sums) += v (two block sums) * s
 __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
@@ -137,67 +147,83 @@ __device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, i
   }
 }
 
-// A warp's sums (32 rows from m0 on, 128 features) to an output of any alignment: 32
-// features at a time are transposed between the lanes, which then write consecutive
-// features of one row (value by value from its own row, a lane's stores cost 32 lines
-// each: 777 x 1,000 x 1,936 took 41 us).
-__device__ __forceinline__ void store_across(const Fp8MatmulArgs& a, long long m0, int n, int lane,
-                                             const uint64_t (&acc)[kSums / 2]) {
-#pragma unroll
-  for (int c = 0; c < kSums / 32; ++c) {
-    if (n + 32 * c >= a.N) break;
-    float x[32];  // [feature] of row `lane`, then [row] of feature `lane`
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 y = unpack2(acc[16 * c + i]);
-      x[2 * i] = y.x, x[2 * i + 1] = y.y;
-    }
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-      const bool high = lane & s;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        if (i & s) continue;
-        const float got = __shfl_xor_sync(0xffffffffu, high ? x[i] : x[i + s], s);
-        if (high)
-          x[i] = got;
-        else
-          x[i + s] = got;
-      }
-    }
-    const int rows = n + 32 * c + lane < a.N ? static_cast<int>(a.M - m0 < 32 ? a.M - m0 : 32) : 0;
-    const long long first = m0 * a.N + n + 32 * c + lane;
-    if (a.add) {  // (all loads before the first store, which may be to the same array)
-      uint16_t d[32];
-      long long at = first;
-#pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        d[r] = r < rows ? a.add[at] : 0;
-        at += a.N;
-        asm volatile("" : "+l"(at));  // (one address at a time, not 32 in registers)
-      }
-#pragma unroll
-      for (int r = 0; r < 32; ++r) x[r] += __uint_as_float(static_cast<uint32_t>(d[r]) << 16);
-    }
-    long long at = first;
-#pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      if (r < rows) {
-        if (a.out_type == kTypeBf16)
-          static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x[r]);
-        else
-          static_cast<float*>(a.out)[at] = x[r];
-      }
-      at += a.N;
-      asm volatile("" : "+l"(at));
-    }
-  }
-}
-
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+
+// A warp's sums (32 rows from m0 on, 128 features) to an output of any alignment: 64
+// features at a time go through shared memory (`tile`: 32 rows of 65), and a lane writes
+// two features of a row at once, from the row's first even address on: 128 bytes or more
+// of a row to a store, so that few sectors are written in parts. (8,192 x 4,095 x 1,024
+// takes 66 us; 84 with 32 features and one to a store, whether transposed by exchanges or
+// through shared memory; 40 is what 4,096 features take.)
+template <bool kAdd, typename T, typename T2>
+__device__ __forceinline__ void store_across(const Fp8MatmulArgs& a, long long m0, int n, int lane,
+                                             const uint64_t (&acc)[kSums / 2], uint32_t tile) {
+  const int rows = static_cast<int>(a.M - m0 < 32 ? a.M - m0 : 32);
+  constexpr int kOnce = 8;  // rows
+  const int N = a.N;
+#pragma unroll
+  for (int c = 0; c < kSums / kWide; ++c) {
+    if (n + kWide * c >= N) break;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kWide / 2; ++i) {
+      const float2 y = unpack2(acc[kWide / 2 * c + i]);
+      st_shared_f32(tile + (lane * (kWide + 1) + 2 * i) * 4, y.x);
+      st_shared_f32(tile + (lane * (kWide + 1) + 2 * i + 1) * 4, y.y);
+    }
+    __syncwarp();
+    const int left = min(kWide, N - n - kWide * c);
+    const long long first = m0 * N + n + kWide * c;
+    T* out = static_cast<T*>(a.out) + first;
+    const uint32_t odd = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out) / sizeof(T));
+    // features e0 and e1 = e0 + 1 of a row; at odd addresses the last lane's are 63 and 0
+    auto place = [&](int r, int* e0, int* e1) {
+      *e0 = 2 * lane + ((odd + static_cast<uint32_t>(r) * static_cast<uint32_t>(N)) & 1);
+      *e1 = (*e0 + 1) % kWide;
+    };
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += kOnce) {
+      uint16_t d0[kOnce], d1[kOnce];
+      if (kAdd) {  // (all loads before the first store, which may be to the same array, and none conditional)
+#pragma unroll
+        for (int i = 0; i < kOnce; ++i) {
+          int e0, e1;
+          place(r0 + i, &e0, &e1);
+          const uint16_t* p = a.add + first + static_cast<long long>(min(r0 + i, rows - 1)) * N;
+          d0[i] = p[min(e0, left - 1)], d1[i] = p[min(e1, left - 1)];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) {
+        const int r = r0 + i;
+        int e0, e1;
+        place(r, &e0, &e1);
+        const uint32_t row = tile + r * (kWide + 1) * 4;
+        float y0 = ld_shared_f32(row + e0 * 4), y1 = ld_shared_f32(row + e1 * 4);
+        if (kAdd) {
+          y0 += __uint_as_float(static_cast<uint32_t>(d0[i]) << 16);
+          y1 += __uint_as_float(static_cast<uint32_t>(d1[i]) << 16);
+        }
+        if (r >= rows) break;
+        T* to = out + static_cast<long long>(r) * N;
+        T2 w;
+        if constexpr (sizeof(T) == 2)
+          w = __floats2bfloat162_rn(y0, y1);
+        else
+          w = make_float2(y0, y1);
+        if (e1 > e0 && e1 < left) {
+          *reinterpret_cast<T2*>(to + e0) = w;
+        } else {
+          if (e0 < left) to[e0] = w.x;
+          if (e1 < e0) to[e1] = w.y;
+        }
+      }
+    }
+  }
+}
 
 // SiLU(gate) * up of a thread's 64 features (the first half of its sums are the gate's, the
 // other the up projection's), into the first half; the largest magnitude.
@@ -227,14 +253,12 @@ __device__ __forceinline__ void store_quantized(const uint64_t (&acc)[kSums / 2]
   }
 }
 
-// Where the sums go.
-enum Out { kOutPieces, kOutAcross, kOutSwiglu };
-
 template <Out kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     fp8_matmul_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                            const __grid_constant__ Fp8MatmulArgs a, int mt, int nt, int32_t* status) {
   constexpr bool kSwiglu = kOut == kOutSwiglu;
+  constexpr int kStages = stages(kOut);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -297,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * kStageBytes);
           const uint32_t bar = map_rank(full(st), 0);
-          tma_load_2d_pair(base + st * kStageBytes, &amap, kb * 128, m0, bar, keep);
-          tma_load_2d_pair(base + st * kStageBytes + kOperand, &bmap, kb * 128, n0, bar, keep);
+          tma_load_2d_pair(base + kStage0 + st * kStageBytes, &amap, kb * 128, m0, bar, keep);
+          tma_load_2d_pair(base + kStage0 + st * kStageBytes + kOperand, &bmap, kb * 128, n0, bar, keep);
           if (++issued == 4 * kStages) issued = 2 * kStages;
           if (++st == kStages) st = 0, ph ^= 1u;
         }
@@ -326,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           if (leader) {
-            const uint64_t ad = sw128_kmajor_desc(base + st * kStageBytes);
-            const uint64_t bd = sw128_kmajor_desc(base + st * kStageBytes + kOperand);
+            const uint64_t ad = sw128_kmajor_desc(base + kStage0 + st * kStageBytes);
+            const uint64_t bd = sw128_kmajor_desc(base + kStage0 + st * kStageBytes + kOperand);
 #pragma unroll
             for (int i = 0; i < 4; ++i)  // (32 bytes on: 2 descriptor units)
               tc_mma_e4m3_pair(tmem + ac * kTileN, ad + 2 * i, bd + 2 * i, idesc, i > 0);
@@ -370,6 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* bs = a.b_s + static_cast<long long>(kSwiglu ? in : min(n / kScaleBlock, nb - 1)) * Kb;
       const long long up = kSwiglu ? static_cast<long long>(nb) * Kb : 0;  // from a gate block's scales to its up block's
       float sa = *as, sb = *bs, sb2 = bs[up];
+      if (!kSwiglu && kOut != kOutAcross && a.add && live)  // (the addends are in L2 when the sums are done)
+        for (int f = n; f < a.N && f < n + kSums; f += 64) prefetch_l2(a.add + static_cast<long long>(m) * a.N + f);
       uint64_t acc[kSums / 2];
 #pragma unroll
       for (int i = 0; i < kSums / 2; ++i) acc[i] = 0;
@@ -408,7 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!kSwiglu) {
         if (kOut == kOutPieces && ok && live) store_row(a, m, n, acc);
-        if (kOut == kOutAcross && ok) store_across(a, m - lane, n, lane, acc);
+        if (across(kOut) && ok) {
+          constexpr bool kAdd = kOut == kOutAcrossAdd;
+          const uint32_t tile = base + across_at(kOut) + warp * kAcrossWarp;
+          if (a.out_type == kTypeBf16)
+            store_across<kAdd, __nv_bfloat16, __nv_bfloat162>(a, m - lane, n, lane, acc, tile);
+          else
+            store_across<kAdd, float, float2>(a, m - lane, n, lane, acc, tile);
+        }
         continue;
       }
       // (bounded waits: a warp that gave up sends nothing, and its partner gives up too)
@@ -450,12 +483,12 @@ cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cu
   static int pairs = 0;
   if (pairs == 0) {
     cudaError_t e = cudaFuncSetAttribute(fp8_matmul_many_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSmem);
+                                         smem_bytes(kOut));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem_bytes(kOut);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
@@ -473,7 +506,7 @@ cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cu
   const long long tiles = static_cast<long long>(mt) * nt;
   if (tiles > (1 << 30)) return cudaErrorInvalidValue;  // (7e13 outputs)
   const unsigned grid = 2u * static_cast<unsigned>(tiles < pairs ? tiles : pairs);
-  return launch_cluster(fp8_matmul_many_kernel<kOut>, dim3(grid), dim3(kThreads), kSmem, stream, 2, amap, bmap, a, mt, nt,
+  return launch_cluster(fp8_matmul_many_kernel<kOut>, dim3(grid), dim3(kThreads), smem_bytes(kOut), stream, 2, amap, bmap, a, mt, nt,
                         status);
 }
 
@@ -486,7 +519,8 @@ bool fp8_whole_pieces(const Fp8MatmulArgs& a) {
 
 cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream) {
   if (swiglu) return launch_many<kOutSwiglu>(a, status, num_sms, stream);
-  return fp8_whole_pieces(a) ? launch_many<kOutPieces>(a, status, num_sms, stream) : launch_many<kOutAcross>(a, status, num_sms, stream);
+  if (fp8_whole_pieces(a)) return launch_many<kOutPieces>(a, status, num_sms, stream);
+  return a.add ? launch_many<kOutAcrossAdd>(a, status, num_sms, stream) : launch_many<kOutAcross>(a, status, num_sms, stream);
 }
 
 }  // namespace moe

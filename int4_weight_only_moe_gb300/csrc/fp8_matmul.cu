@@ -189,10 +189,13 @@ __device__ __forceinline__ void store_out4(const Fp8MatmulArgs& a, long long m, 
   const long long at = m * a.N + n;
   if (!vec) {
     float v[4] = {y.x, y.y, y.z, y.w};
-    if (a.add) {  // (all loads before the first store, which may be to the same array)
+    if (n >= a.N) return;
+    if (a.add) {  // (all loads before the first store, which may be to the same array, and none conditional)
+      uint16_t d[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (n + i < a.N) v[i] += __uint_as_float(static_cast<uint32_t>(a.add[at + i]) << 16);
+      for (int i = 0; i < 4; ++i) d[i] = a.add[at + min(i, a.N - 1 - n)];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(static_cast<uint32_t>(d[i]) << 16);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -338,6 +341,11 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
   } else {
     pdl_wait();
     if (threadIdx.x == 0) pdl_launch_dependents();
+    if (!kSwiglu && a.add)  // (the addends of the rows that this CTA will write, to L2)
+      for (int i = threadIdx.x; rank + split * (i >> 1) < rows; i += L::kEpiThreads) {
+        const int n = n0 + (i & 1) * 64;
+        if (n < a.N) prefetch_l2(a.add + (m0 + rank + split * (i >> 1)) * a.N + n);
+      }
     const int row = (warp & 3) * 32 + lane;
     const int c0 = (warp >> 2) * L::kMine;  // first column
     const uint32_t src0 = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c0;
@@ -589,19 +597,17 @@ cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStre
   const cudaError_t e = choose_split<128, kSwiglu>(a, num_sms, &split, &share, &waves);
   if (e != cudaSuccess) return e;
   // Both kernels' times by what they were measured to take, in hundredths of a us: here
-  // 30 a block and 400 a wave of CTAs; there 40 a block and 120 a wave of pairs, 300 in
-  // all, and 800 a wave where its output cannot go in whole pieces, as much again with an
-  // addend. (256 x 4,096 x 7,168: 14.2 us here, 24.4
-  // there; 512 rows 22.4 and 24.6; 640 x 7,168 x 2,048: 19.2 and 18.5; 2,048 x 1,000 x
-  // 1,936 in fp32: 10.8 and 11.1; 600 x 2,047 x 2,048 with an addend: 13.9 and 26.7; 2,048
-  // x 4,096 x 7,168: 88.7 and 47.7. Of 77 sizes two were chosen 6% too slow.)
-  // (The SwiGLU form's two weight boxes
-  // count 45 a block here.)
+  // 30 a block and 500 a wave of CTAs, 300 more with an addend from the second on; there 40 a block and 120 a
+  // wave of pairs, 300 in all, and 300 a wave where its output cannot go in whole pieces,
+  // 700 with an addend. (256 x 4,096 x 7,168: 14.2 us here, 24.4 there; 512 rows 22.4 and
+  // 24.6; 640 x 7,168 x 2,048: 19.2 and 18.5; 2,048 x 1,000 x 1,936 in fp32: 10.8 and
+  // 11.1; 2,048 x 2,047 x 1,024: 15.0 and 11.7, with an addend 21.5 and 15.1; 8,192 x
+  // 4,095 x 7,168: 316 and 193. The SwiGLU form's two weight boxes count 45 a block here.)
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   const long long pairs = num_sms / 2;
   const long long big = (static_cast<long long>(a.M) + 255) / 256 * (kSwiglu ? a.N / 128 : (a.N + 255) / 256);
-  const long long odd = kSwiglu || fp8_whole_pieces(a) ? 0 : a.add ? 1600 : 800;
-  const long long here = waves * ((kSwiglu ? 45LL : 30LL) * share + 500) + 100;
+  const long long odd = kSwiglu || fp8_whole_pieces(a) ? 0 : a.add ? 700 : 300;
+  const long long here = waves * ((kSwiglu ? 45LL : 30LL) * share + 500) + 100 + (a.add ? 300 * (waves - 1) : 0);
   const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120 + odd) + 300;
   // (a grid's second dimension ends at 65,535 tiles of 128 rows)
   if (there < here || a.M > 65535LL * 128) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
