@@ -11,7 +11,7 @@
 // What bounds it: the way out of tensor memory. A block's MMAs take 512 cycles, its sums
 // 450 of loads and additions plus about 550 from the last MMA to the first load and from
 // the release to the next MMA, with two accumulators in turn: 750 cycles a block. The
-// loads of 32 columns run one piece ahead of the sums (of 16 columns: +4%).
+// loads of 16 columns run one piece ahead of the sums.
 // Measured and not kept: halves of an accumulator handed back one by one (up to +15%),
 // 16 summing warps (+12%), scales staged in shared memory by other warps (+10%), output
 // through shared memory and the copy engine (+5%), copies into L2 six blocks ahead (+2%).
@@ -60,9 +60,9 @@ constexpr int kHalf = 128;                 // rows, and features, of a CTA
 constexpr int kSums = kTileN / 2;          // of a thread: one row, 128 features
 constexpr int kOperand = 128 * 128;        // bytes of a box
 constexpr int kStageBytes = 2 * kOperand;
-// Where the sums go: whole 32-byte pieces of a row, any alignment (without and with
-// addends, for whose registers the sums of the one would pay), or SwiGLU and e4m3.
-enum Out { kOutPieces, kOutAcross, kOutAcrossAdd, kOutSwiglu };
+// Where the sums go: whole 32-byte pieces of a row, any alignment (both without and with
+// addends, for whose registers the sums would pay), or SwiGLU and e4m3.
+enum Out { kOutPieces, kOutPiecesAdd, kOutAcross, kOutAcrossAdd, kOutSwiglu };
 __host__ __device__ constexpr bool across(Out out) { return out == kOutAcross || out == kOutAcrossAdd; }
 // Shared memory: maxima, barriers, stages, and for any alignment a tile of 32 rows x 65
 // sums for each summing warp, which costs a stage.
@@ -93,9 +93,6 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
   return v;
 }
 
-__device__ __forceinline__ void tmem_piece(uint32_t src, uint32_t (&v)[16]) { tmem_ld16(src, v); }
-__device__ __forceinline__ void tmem_piece(uint32_t src, uint32_t (&v)[32]) { tmem_ld32(src, v); }
-
 // Tile `t` of a grid of mt x nt: bands of 8 row tiles, features outer inside a band, so
 // that the pairs at work together share rows and features in L2.
 constexpr int kBand = 8;
@@ -121,12 +118,10 @@ __device__ __forceinline__ void store_row(const Fp8MatmulArgs& a, long long m, i
 #pragma unroll
     for (int c = 0; c < kSums / 16; ++c) {
       if (n + 16 * c >= a.N) break;
-      Words8 w, d;
-      if (a.add) d = ld_global_32b(a.add + at + 16 * c);
+      Words8 w;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float2 y = unpack2(acc[8 * c + i]);
-        if (a.add) y.x += __uint_as_float(d.w[i] << 16), y.y += __uint_as_float(d.w[i] & 0xFFFF0000u);
+        const float2 y = unpack2(acc[8 * c + i]);
         w.w[i] = bf16x2(y.x, y.y);
       }
       st_global_32b(out + 16 * c, w);
@@ -151,6 +146,33 @@ __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) { return __uint_as_float(ld_shared_u32(addr)); }
+
+// The same with addends, bf16, four pieces' loads at a time (8,192 x 7,168 x 2,048: 124 us,
+// 134 one by one, 98 without addends).
+__device__ __forceinline__ void store_row_add(const Fp8MatmulArgs& a, long long m, int n,
+                                              const uint64_t (&acc)[kSums / 2]) {
+  if (n >= a.N) return;
+  const long long at = m * a.N + n;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at;
+  constexpr int kOnce = 4;  // pieces
+#pragma unroll
+  for (int c0 = 0; c0 < kSums / 16; c0 += kOnce) {
+    Words8 d[kOnce];  // (all loads before the first store, which may be to the same array)
+#pragma unroll
+    for (int c = 0; c < kOnce; ++c) d[c] = ld_global_32b(a.add + (n + 16 * (c0 + c) < a.N ? at + 16 * (c0 + c) : at));
+#pragma unroll
+    for (int c = 0; c < kOnce; ++c) {
+      if (n + 16 * (c0 + c) >= a.N) break;
+      Words8 w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 y = unpack2(acc[8 * (c0 + c) + i]);
+        w.w[i] = bf16x2(y.x + __uint_as_float(d[c].w[i] << 16), y.y + __uint_as_float(d[c].w[i] & 0xFFFF0000u));
+      }
+      st_global_32b(out + 16 * (c0 + c), w);
+    }
+  }
+}
 
 // A warp's sums (32 rows from m0 on, 128 features) to an output of any alignment: 64
 // features at a time go through shared memory (`tile`: 32 rows of 65), and a lane writes
@@ -394,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float* bs = a.b_s + static_cast<long long>(kSwiglu ? in : min(n / kScaleBlock, nb - 1)) * Kb;
       const long long up = kSwiglu ? static_cast<long long>(nb) * Kb : 0;  // from a gate block's scales to its up block's
       float sa = *as, sb = *bs, sb2 = bs[up];
-      if (!kSwiglu && kOut != kOutAcross && a.add && live)  // (the addends are in L2 when the sums are done)
+      if ((kOut == kOutPiecesAdd || kOut == kOutAcrossAdd) && live)  // (the addends are in L2 when the sums are done)
         for (int f = n; f < a.N && f < n + kSums; f += 64) prefetch_l2(a.add + static_cast<long long>(m) * a.N + f);
       uint64_t acc[kSums / 2];
 #pragma unroll
@@ -410,16 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t src = src0 + ac * kTileN;
         // the loads of a piece overlap the sums of the one before it
-        constexpr int kPiece = kOut == kOutPieces ? 32 : 16;  // (the others have no registers for 32)
+        constexpr int kPiece = 16;  // (pieces of 32 leave the outputs' forms short of registers)
         constexpr int kPieces = kSums / kPiece;
         auto column = [](int c) { return c * kPiece + (kSwiglu && c >= kPieces / 2 ? kSums / 2 : 0); };
         uint32_t v[2][kPiece];
-        tmem_piece(src, v[0]);
+        tmem_ld16(src, v[0]);
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {
           tmem_ld_wait();
           if (c + 1 < kPieces) {
-            tmem_piece(src + column(c + 1), v[(c + 1) & 1]);
+            tmem_ld16(src + column(c + 1), v[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
@@ -434,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!kSwiglu) {
         if (kOut == kOutPieces && ok && live) store_row(a, m, n, acc);
+        if (kOut == kOutPiecesAdd && ok && live) store_row_add(a, m, n, acc);
         if (across(kOut) && ok) {
           constexpr bool kAdd = kOut == kOutAcrossAdd;
           const uint32_t tile = base + across_at(kOut) + warp * kAcrossWarp;
@@ -519,7 +542,8 @@ bool fp8_whole_pieces(const Fp8MatmulArgs& a) {
 
 cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream) {
   if (swiglu) return launch_many<kOutSwiglu>(a, status, num_sms, stream);
-  if (fp8_whole_pieces(a)) return launch_many<kOutPieces>(a, status, num_sms, stream);
+  if (fp8_whole_pieces(a))
+    return a.add ? launch_many<kOutPiecesAdd>(a, status, num_sms, stream) : launch_many<kOutPieces>(a, status, num_sms, stream);
   return a.add ? launch_many<kOutAcrossAdd>(a, status, num_sms, stream) : launch_many<kOutAcross>(a, status, num_sms, stream);
 }
 

@@ -598,15 +598,15 @@ cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStre
   if (e != cudaSuccess) return e;
   // Both kernels' times by what they were measured to take, in hundredths of a us: here
   // 30 a block and 500 a wave of CTAs, 300 more with an addend from the second on; there 40 a block and 120 a
-  // wave of pairs, 300 in all, and 300 a wave where its output cannot go in whole pieces,
-  // 700 with an addend. (256 x 4,096 x 7,168: 14.2 us here, 24.4 there; 512 rows 22.4 and
+  // wave of pairs, 300 in all, and 300 a wave where its output cannot go in whole pieces;
+  // with an addend 180 and 700. (256 x 4,096 x 7,168: 14.2 us here, 24.4 there; 512 rows 22.4 and
   // 24.6; 640 x 7,168 x 2,048: 19.2 and 18.5; 2,048 x 1,000 x 1,936 in fp32: 10.8 and
   // 11.1; 2,048 x 2,047 x 1,024: 15.0 and 11.7, with an addend 21.5 and 15.1; 8,192 x
   // 4,095 x 7,168: 316 and 193. The SwiGLU form's two weight boxes count 45 a block here.)
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   const long long pairs = num_sms / 2;
   const long long big = (static_cast<long long>(a.M) + 255) / 256 * (kSwiglu ? a.N / 128 : (a.N + 255) / 256);
-  const long long odd = kSwiglu || fp8_whole_pieces(a) ? 0 : a.add ? 700 : 300;
+  const long long odd = kSwiglu ? 0 : fp8_whole_pieces(a) ? (a.add ? 180 : 0) : a.add ? 700 : 300;
   const long long here = waves * ((kSwiglu ? 45LL : 30LL) * share + 500) + 100 + (a.add ? 300 * (waves - 1) : 0);
   const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120 + odd) + 300;
   // (a grid's second dimension ends at 65,535 tiles of 128 rows)
