@@ -309,7 +309,8 @@ int moe_w4a16_fp8_set_option(int option, int value);
  *   workspace  >= moe_w4a16_shared_expert_workspace_size(M, K, N) bytes (0 for a shape
  *   that is not supported), 256-byte aligned; holds nothing between calls. NULL: the call
  *   takes and returns it in stream order from a memory pool of the library's own, which
- *   keeps up to 64 MiB (workspace_bytes is then not looked at)
+ *   keeps up to 64 MiB (workspace_bytes is then not looked at); in a stream capture that
+ *   makes memory nodes of the graph, which allow it one launch at a time
  * K % 128 == 0, N % 128 == 0. M == 0 is a no-op. Three launches on `stream` (quantise;
  * gate/up product, SwiGLU and quantise; down product), with a workspace allocates
  * nothing, no host synchronisation. */

@@ -10,6 +10,10 @@ Tolerances, from the arithmetic:
   ulp (2^-23) of the sum of magnitudes, with 128 terms to a block and one more per
   block; bf16 outputs by 2^-8 of the result more.
 * shared expert: the framework's tolerance of the feed-forward (its bf16 output)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -359,6 +363,27 @@ def test_shared_expert_takes_its_workspace_from_the_pool_or_torch():
         torch.cuda.synchronize()
         for pair in got:
             assert torch.equal(pair[0], want[0]) and torch.equal(pair[1], want[1])
+
+
+def test_first_call_of_a_process_may_be_captured():
+    code = """
+import torch
+from int4_weight_only_moe_gb300 import fp8
+M, K, N = 100, 1024, 512
+bytes_ = lambda *n: torch.randint(0, 100, n, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+h = torch.randn(M, K, device="cuda").bfloat16()
+w = (bytes_(2 * N, K), torch.rand(8, 8, device="cuda") * 0.01, bytes_(K, N), torch.rand(8, 4, device="cuda") * 0.01)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y = fp8.shared_expert(h, *w)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, fp8.shared_expert(h, *w)) and fp8.status() == 0 and y.isfinite().all()
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_shared_expert_replays_from_a_cuda_graph():
