@@ -353,6 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rank == 0)
         for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
           mbar_drain(full(i % kStages), (i / kStages) & 1);
+      // ... and, in either CTA, after the MMAs' last signals have: each of them is a write to
+      // this CTA's shared memory that travels on its own, and one that was seen says nothing
+      // about the others
+      for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        if (!mbar_wait(empty(i % kStages), (i / kStages) & 1, abort_flag, status, kStatusTimeout, limit)) break;
+      if (rank != 0) mbar_drain(drain, 0);  // (the leader's own is waited for where it is sent)
       if (*abort_flag) {  // (the other CTA's copies count on the leader's barriers: give them 2 ms)
         const long long c0 = clock64();
         while (clock64() - c0 < 4000000) {

@@ -302,6 +302,9 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
       // shared memory is released only after the last copies have landed, whoever gave up
       for (int i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
         mbar_drain(full(i % L::kStages), (i / L::kStages) & 1);
+      // (and the MMAs' last signals, which are writes to it too)
+      for (int i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
+        if (!mbar_wait(empty(i % L::kStages), (i / L::kStages) & 1, abort_flag, status, kStatusTimeout, limit)) break;
     }
   } else if (warp == kWarpMma) {
     constexpr uint32_t idesc = idesc_e4m3_f32(128, L::kBatchIsM ? L::kAccCols : L::kBoxCols);
