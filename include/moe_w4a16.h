@@ -220,7 +220,9 @@ int moe_w4a16_forward_partial(moe_w4a16_t h, const uint16_t* hidden, const int32
                               void* workspace, size_t workspace_bytes, void* stream);
 int moe_w4a16_finalize(const float* acc, uint16_t* out, long long n, void* stream);
 
-/* ---- operators around the routed experts ------------------------------- */
+/* ---- operators around the routed experts -------------------------------
+ * They launch on the current device: every pointer is that device's, and `stream` too
+ * (the Python calls check it). */
 
 /* Element types of the floating inputs and outputs below. */
 enum { MOE_W4A16_F32 = 0, MOE_W4A16_BF16 = 1 };

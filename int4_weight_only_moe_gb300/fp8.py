@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import BF16, F32, _check, _need, lib, moe_w4a16_fp8_status, moe_w4a16_shared_expert_workspace_size
-from .routing import _dense, _handle, _new, _rows
+from .routing import _dense, _device, _handle, _new, _on, _rows
 
 BLOCK = 128
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
@@ -25,23 +25,26 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _bytes(t, shape, name):
-    """Address of a contiguous CUDA tensor of e4m3 values (or their bytes) of this shape."""
-    if t.dtype not in _E4M3 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _bytes(t, shape, name, dev):
+    """Address of a contiguous tensor of e4m3 values (or their bytes) of this shape on
+    device ``dev``."""
+    if t.dtype not in _E4M3 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _need(t, _BYTES, shape, name)
+        _on(t, dev, name)
     return t.data_ptr()
 
 
 def _quantize(call, x, name, parts, rows_to_a_scale, q, s, stream):
     M, width, stride = _rows(x, name, _FLOATS)
+    dev = _device(x, name)
     cols = width // parts
     scales = (M if rows_to_a_scale == 1 else _blocks(M), _blocks(cols))
     if q is None:
         q = _new((M, cols), torch.float8_e4m3fn, x, stream)
     if s is None:
         s = _new(scales, torch.float32, x, stream)
-    _check(call(x.data_ptr(), _FLOATS[x.dtype], stride, M, cols, _bytes(q, (M, cols), "q"),
-                _dense(s, torch.float32, scales, "s"), _handle(stream, x)))
+    _check(call(x.data_ptr(), _FLOATS[x.dtype], stride, M, cols, _bytes(q, (M, cols), "q", dev),
+                _dense(s, torch.float32, scales, "s", dev), _handle(stream, dev)))
     return q, s
 
 
@@ -67,18 +70,20 @@ def matmul(a, a_s, b, b_s, add=None, out=None, out_dtype=torch.bfloat16, stream=
     ``out_dtype`` (bf16 or fp32; that of ``out`` where it is given)."""
     M, K, lda = _rows(a, "a", _E4M3)
     N, b_cols, ldb = _rows(b, "b", _E4M3)
+    dev = _device(a, "a")
+    _on(b, dev, "b")
     if b_cols != K:
         raise ValueError(f"b: shape {tuple(b.shape)}, expected {K} columns")
-    sa = _dense(a_s, torch.float32, (M, _blocks(K)), "a_s")
-    sb = _dense(b_s, torch.float32, (_blocks(N), _blocks(K)), "b_s")
-    plus = 0 if add is None else _dense(add, torch.bfloat16, (M, N), "add")
+    sa = _dense(a_s, torch.float32, (M, _blocks(K)), "a_s", dev)
+    sb = _dense(b_s, torch.float32, (_blocks(N), _blocks(K)), "b_s", dev)
+    plus = 0 if add is None else _dense(add, torch.bfloat16, (M, N), "add", dev)
     if out is None:
         out = _new((M, N), out_dtype, a, stream)
     if out.dtype not in _FLOATS:
         raise ValueError(f"out: dtype {out.dtype}, expected one of {tuple(_FLOATS)}")
     _check(lib().moe_w4a16_fp8_matmul(
-        a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, plus, _dense(out, out.dtype, (M, N), "out"), _FLOATS[out.dtype],
-        M, N, K, _handle(stream, a)))
+        a.data_ptr(), lda, sa, b.data_ptr(), ldb, sb, plus, _dense(out, out.dtype, (M, N), "out", dev), _FLOATS[out.dtype],
+        M, N, K, _handle(stream, dev)))
     return out
 
 
@@ -98,18 +103,24 @@ def shared_expert(hidden, w1, w1_s, w2, w2_s, add=None, out=None, workspace=None
     """
     M, K = shape = hidden.shape
     N = w2.shape[1]
-    x = _dense(hidden, torch.bfloat16, (M, K), "hidden")
+    dev = _device(hidden, "hidden")
+    x = _dense(hidden, torch.bfloat16, (M, K), "hidden", dev)
     kb, nb = _blocks(K), _blocks(N)
-    weights = (_bytes(w1, (2 * N, K), "w1"), _dense(w1_s, torch.float32, (_blocks(2 * N), kb), "w1_s"),
-               _bytes(w2, (K, N), "w2"), _dense(w2_s, torch.float32, (kb, nb), "w2_s"))
-    plus = 0 if add is None else _dense(add, torch.bfloat16, shape, "add")
+    weights = (_bytes(w1, (2 * N, K), "w1", dev), _dense(w1_s, torch.float32, (_blocks(2 * N), kb), "w1_s", dev),
+               _bytes(w2, (K, N), "w2", dev), _dense(w2_s, torch.float32, (kb, nb), "w2_s", dev))
+    plus = 0 if add is None else _dense(add, torch.bfloat16, shape, "add", dev)
     if out is None:
         out = _new(shape, torch.bfloat16, hidden, stream)
-    y = _dense(out, torch.bfloat16, shape, "out")
+    y = _dense(out, torch.bfloat16, shape, "out", dev)
     if workspace is None and (need := _workspace_size(M, K, N)) > _POOL_BYTES:
         workspace = _new((need,), torch.uint8, hidden, stream)
-    ws, size = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.nbytes)
-    _check(lib().moe_w4a16_shared_expert(x, *weights, plus, y, M, K, N, ws, size, _handle(stream, hidden)))
+    ws = size = 0
+    if workspace is not None:
+        _on(workspace, dev, "workspace")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws, size = workspace.data_ptr(), workspace.nbytes
+    _check(lib().moe_w4a16_shared_expert(x, *weights, plus, y, M, K, N, ws, size, _handle(stream, dev)))
     return out
 
 

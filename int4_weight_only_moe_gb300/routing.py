@@ -33,17 +33,36 @@ def _rows(t, name, types):
     return rows, cols, stride
 
 
-def _dense(t, dtype, shape, name):
-    """``t`` itself, when it is a contiguous CUDA tensor of this type and shape; its address."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _device(t, name):
+    """Index of the device of ``t``, which has to be the current one: that is where the
+    library launches."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return dev
+
+
+def _on(t, dev, name):
+    """Refuses a tensor that is not on device ``dev``."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+
+
+def _dense(t, dtype, shape, name, dev):
+    """``t`` itself, when it is a contiguous tensor of this type and shape on device
+    ``dev``; its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _need(t, (str(dtype).removeprefix("torch."),), shape, name)
+        _on(t, dev, name)
     return t.data_ptr()
 
 
-def _handle(stream, t):
-    """Raw handle of ``stream``, or of the current stream of the device of ``t``."""
+def _handle(stream, dev):
+    """Raw handle of ``stream``, or of the current stream of device ``dev``."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return int(getattr(stream, "cuda_stream", stream))
 
 
@@ -65,10 +84,11 @@ def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_gro
     of a group's largest values count for it; by default 2 with a bias, 1 without.
     """
     M, E, stride = _rows(logits, "logits", _TYPES)
+    dev = _device(logits, "logits")
     score = _SCORES.get(scoring)
     if score is None:
         raise ValueError(f"scoring: {scoring!r}, expected one of {tuple(_SCORES)}")
-    b = 0 if bias is None else _dense(bias, torch.float32, (E,), "bias")
+    b = 0 if bias is None else _dense(bias, torch.float32, (E,), "bias", dev)
     if group_top is None:
         group_top = 2 if bias is not None else 1
     if ids is None:
@@ -77,6 +97,6 @@ def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_gro
         weights = _new((M, topk), torch.float32, logits, stream)
     _check(lib().moe_w4a16_route_scored(
         logits.data_ptr(), _TYPES[logits.dtype], stride, M, E, topk, score, b, n_group, topk_group, group_top,
-        renormalize, scale, _dense(ids, torch.int32, (M, topk), "ids"),
-        _dense(weights, torch.float32, (M, topk), "weights"), _handle(stream, logits)))
+        renormalize, scale, _dense(ids, torch.int32, (M, topk), "ids", dev),
+        _dense(weights, torch.float32, (M, topk), "weights", dev), _handle(stream, dev)))
     return ids, weights
