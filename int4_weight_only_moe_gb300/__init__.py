@@ -138,6 +138,34 @@ def _stream(stream) -> int:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+def _torch_stream(stream, device):
+    """``stream`` (a torch stream or a raw handle) as a torch stream; None: the current one."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+
+
+def _new(shape, dtype, device, stream=None, zero=False):
+    """A new tensor for kernels on ``stream`` (None: the current one), in that stream's
+    order: memory that the allocator gives out on the current stream may still be in use by
+    work queued there. It is not given out again before the current stream, where the caller
+    goes on with it, is done with it either."""
+    import torch
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    s, here = _torch_stream(stream, device), torch.cuda.current_stream(device)
+    if s == here:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(s):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 _DTYPES: dict = {}
 
 
@@ -394,7 +422,7 @@ class MoEW4A16:
         else:
             moe_w4a16_pack_ex(self.handle, w1_q, w1_s, w2_q, w2_s, layout, w1_g_idx, w2_g_idx, stream)
 
-    def ensure_workspace(self, M: int, host_staging: bool = False):
+    def ensure_workspace(self, M: int, host_staging: bool = False, stream=None):
         # (asked every call: the size depends on the handle's options, which the
         # caller may change between calls)
         need = moe_w4a16_workspace_size(self.handle, M)
@@ -402,7 +430,9 @@ class MoEW4A16:
             need += moe_w4a16_host_staging_size(self.handle, M)
         if self.workspace is None or self.workspace.numel() < need:
             import torch
-            self.workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
+            if self.workspace is not None:  # (a call in flight on `stream` may still use it)
+                self.workspace.record_stream(_torch_stream(stream, self.workspace.device))
+            self.workspace = _new((need,), torch.uint8, "cuda", stream)
         return self.workspace
 
     def forward(self, hidden, topk_ids, topk_weights, out=None, stream=None):
@@ -412,9 +442,9 @@ class MoEW4A16:
         _need(topk_ids, ("int32",), (M, self.topk), "topk_ids")
         _need(topk_weights, ("float32",), (M, self.topk), "topk_weights")
         if out is None:
-            out = torch.empty((M, self.K), dtype=torch.bfloat16, device=hidden.device)
+            out = _new((M, self.K), torch.bfloat16, hidden.device, stream)
         _need(out, _BITS16, (M, self.K), "out")
-        ws = self.ensure_workspace(M)
+        ws = self.ensure_workspace(M, stream=stream)
         moe_w4a16_forward(self.handle, hidden, topk_ids, topk_weights, out, M, ws, stream)
         return out
 
@@ -426,9 +456,9 @@ class MoEW4A16:
         _need(topk_ids, ("int32",), (M, self.topk), "topk_ids")
         _need(topk_weights, ("float32",), (M, self.topk), "topk_weights")
         if partial is None:
-            partial = torch.empty((M, self.K), dtype=torch.float32, device=hidden.device)
+            partial = _new((M, self.K), torch.float32, hidden.device, stream)
         _need(partial, ("float32",), (M, self.K), "partial")
-        ws = self.ensure_workspace(M)
+        ws = self.ensure_workspace(M, stream=stream)
         moe_w4a16_forward_partial(self.handle, hidden, topk_ids, topk_weights, partial, M, ws, stream)
         return partial
 
@@ -437,8 +467,8 @@ class MoEW4A16:
         import torch
         M = router_logits.shape[0]
         _need(router_logits, ("float32",), (M, self.E_total), "router_logits")
-        ids = torch.empty((M, self.topk), dtype=torch.int32, device=router_logits.device)
-        w = torch.empty((M, self.topk), dtype=torch.float32, device=router_logits.device)
+        ids = _new((M, self.topk), torch.int32, router_logits.device, stream)
+        w = _new((M, self.topk), torch.float32, router_logits.device, stream)
         moe_w4a16_route(router_logits, M, self.E_total, self.topk, ids, w, stream)
         return ids, w
 
@@ -449,11 +479,11 @@ class MoEW4A16:
         _need(hidden, _BITS16, (M, self.K), "hidden")
         _need(router_logits, ("float32",), (M, self.E_total), "router_logits")
         if out is None:
-            out = torch.empty((M, self.K), dtype=torch.bfloat16, device=hidden.device)
+            out = _new((M, self.K), torch.bfloat16, hidden.device, stream)
         _need(out, _BITS16, (M, self.K), "out")
-        ids = torch.empty((M, self.topk), dtype=torch.int32, device=hidden.device)
-        w = torch.empty((M, self.topk), dtype=torch.float32, device=hidden.device)
-        ws = self.ensure_workspace(M)
+        ids = _new((M, self.topk), torch.int32, hidden.device, stream)
+        w = _new((M, self.topk), torch.float32, hidden.device, stream)
+        ws = self.ensure_workspace(M, stream=stream)
         moe_w4a16_forward_logits(self.handle, hidden, router_logits, ids, w, out, M, ws, stream)
         return out, ids, w
 
@@ -463,7 +493,7 @@ class MoEW4A16:
         _need(topk_ids, ("int32",), (M, self.topk), "topk_ids", device=False)
         _need(topk_weights, ("float32",), (M, self.topk), "topk_weights", device=False)
         _need(out, _BITS16, (M, self.K), "out", device=False)
-        ws = self.ensure_workspace(M, host_staging=True)
+        ws = self.ensure_workspace(M, host_staging=True, stream=stream)
         moe_w4a16_forward_host(self.handle, hidden, topk_ids, topk_weights, out, M, ws, stream)
         return out
 
@@ -473,12 +503,12 @@ class MoEW4A16:
     def accumulator(self, M: int, stream=None):
         """fp32 [M, K] output accumulator of the last forward (before the bf16 rounding)."""
         import torch
-        acc = torch.zeros((M, self.K), dtype=torch.float32, device="cuda")
+        acc = _new((M, self.K), torch.float32, "cuda", stream, zero=True)
         moe_w4a16_read_accumulator(self.handle, self.workspace, M, acc, stream)
         return acc
 
     def intermediate(self, M: int, stream=None):
         import torch
-        h_rows = torch.zeros((M * self.topk, self.N), dtype=torch.float32, device="cuda")
+        h_rows = _new((M * self.topk, self.N), torch.float32, "cuda", stream, zero=True)
         moe_w4a16_read_intermediate(self.handle, self.workspace, M, h_rows, stream)
         return h_rows

@@ -37,9 +37,9 @@ def allreduce_partial(partial, group=None):
 def finalize(acc, out=None, stream=None):
     """bf16 round-to-nearest-even of an fp32 [M, K] sum, on the device."""
     import torch
-    from . import moe_w4a16_finalize
+    from . import _new, moe_w4a16_finalize
     if out is None:
-        out = torch.empty(acc.shape, dtype=torch.bfloat16, device=acc.device)
+        out = _new(acc.shape, torch.bfloat16, acc.device, stream)
     moe_w4a16_finalize(acc, out, stream)
     return out
 

@@ -12,8 +12,8 @@ import functools
 
 import torch
 
-from . import BF16, F32, _check, _need, lib, moe_w4a16_fp8_status, moe_w4a16_shared_expert_workspace_size
-from .routing import _dense, _device, _handle, _new, _on, _rows
+from . import BF16, F32, _check, _need, _new, lib, moe_w4a16_fp8_status, moe_w4a16_shared_expert_workspace_size
+from .routing import _dense, _device, _handle, _on, _rows
 
 BLOCK = 128
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
@@ -40,9 +40,9 @@ def _quantize(call, x, name, parts, rows_to_a_scale, q, s, stream):
     cols = width // parts
     scales = (M if rows_to_a_scale == 1 else _blocks(M), _blocks(cols))
     if q is None:
-        q = _new((M, cols), torch.float8_e4m3fn, x, stream)
+        q = _new((M, cols), torch.float8_e4m3fn, x.device, stream)
     if s is None:
-        s = _new(scales, torch.float32, x, stream)
+        s = _new(scales, torch.float32, x.device, stream)
     _check(call(x.data_ptr(), _FLOATS[x.dtype], stride, M, cols, _bytes(q, (M, cols), "q", dev),
                 _dense(s, torch.float32, scales, "s", dev), _handle(stream, dev)))
     return q, s
@@ -78,7 +78,7 @@ def matmul(a, a_s, b, b_s, add=None, out=None, out_dtype=torch.bfloat16, stream=
     sb = _dense(b_s, torch.float32, (_blocks(N), _blocks(K)), "b_s", dev)
     plus = 0 if add is None else _dense(add, torch.bfloat16, (M, N), "add", dev)
     if out is None:
-        out = _new((M, N), out_dtype, a, stream)
+        out = _new((M, N), out_dtype, a.device, stream)
     if out.dtype not in _FLOATS:
         raise ValueError(f"out: dtype {out.dtype}, expected one of {tuple(_FLOATS)}")
     _check(lib().moe_w4a16_fp8_matmul(
@@ -110,10 +110,10 @@ def shared_expert(hidden, w1, w1_s, w2, w2_s, add=None, out=None, workspace=None
                _bytes(w2, (K, N), "w2", dev), _dense(w2_s, torch.float32, (kb, nb), "w2_s", dev))
     plus = 0 if add is None else _dense(add, torch.bfloat16, shape, "add", dev)
     if out is None:
-        out = _new(shape, torch.bfloat16, hidden, stream)
+        out = _new(shape, torch.bfloat16, hidden.device, stream)
     y = _dense(out, torch.bfloat16, shape, "out", dev)
     if workspace is None and (need := _workspace_size(M, K, N)) > _POOL_BYTES:
-        workspace = _new((need,), torch.uint8, hidden, stream)
+        workspace = _new((need,), torch.uint8, hidden.device, stream)
     ws = size = 0
     if workspace is not None:
         _on(workspace, dev, "workspace")

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import torch
 
-from . import BF16, F32, SCORE_SIGMOID, SCORE_SOFTMAX, _check, _need, lib
+from . import BF16, F32, SCORE_SIGMOID, SCORE_SOFTMAX, _check, _need, _new, lib
 
 _SCORES = {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -66,15 +66,6 @@ def _handle(stream, dev):
     return int(getattr(stream, "cuda_stream", stream))
 
 
-def _new(shape, dtype, like, stream):
-    """A new tensor on the device of ``like``; the allocator learns of a ``stream`` that is
-    not the current one."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
-    return t
-
-
 def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_group=1, group_top=None,
                  renormalize=True, scale=1.0, ids=None, weights=None, stream=None):
     """Scores, biased and group-limited top-k and weights of ``logits`` [M, E] (fp32 or
@@ -92,9 +83,9 @@ def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_gro
     if group_top is None:
         group_top = 2 if bias is not None else 1
     if ids is None:
-        ids = _new((M, topk), torch.int32, logits, stream)
+        ids = _new((M, topk), torch.int32, logits.device, stream)
     if weights is None:
-        weights = _new((M, topk), torch.float32, logits, stream)
+        weights = _new((M, topk), torch.float32, logits.device, stream)
     _check(lib().moe_w4a16_route_scored(
         logits.data_ptr(), _TYPES[logits.dtype], stride, M, E, topk, score, b, n_group, topk_group, group_top,
         renormalize, scale, _dense(ids, torch.int32, (M, topk), "ids", dev),
