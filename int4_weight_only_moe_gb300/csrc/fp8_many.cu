@@ -508,11 +508,15 @@ namespace {
 template <Out kOut>
 cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
   constexpr bool kSwiglu = kOut == kOutSwiglu;
-  // pairs that can run at once (SMs that have a partner), asked once
-  static int pairs = 0;
+  // pairs that can run at once (SMs that have a partner); sets the kernel up for the device
+  static PerDevice<int> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* entry = known.of(dev);
+  int pairs = entry ? entry->load() : 0;
   if (pairs == 0) {
-    cudaError_t e = cudaFuncSetAttribute(fp8_matmul_many_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes(kOut));
+    e = cudaFuncSetAttribute(fp8_matmul_many_kernel<kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kOut));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2));
@@ -527,6 +531,7 @@ cudaError_t launch_many(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cu
     e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_many_kernel<kOut>, &cfg);
     if (e != cudaSuccess) return e;
     pairs = n < 1 ? 1 : (n > num_sms / 2 ? num_sms / 2 : n);
+    if (entry) entry->store(pairs);
   }
   CUtensorMap amap, bmap;
   if (!make_byte_map(&amap, a.a, a.M, a.K, a.lda, kHalf) || !make_byte_map(&bmap, a.b, (kSwiglu ? 2LL : 1LL) * a.N, a.K, a.ldb, kHalf))

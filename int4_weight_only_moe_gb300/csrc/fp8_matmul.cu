@@ -7,7 +7,6 @@
 // block of `b`. A block's products are summed in fp32 unscaled; the scaled block sums
 // are added in fp32 and rounded once to the output type.
 #include <cuda_bf16.h>
-#include <atomic>
 
 #include "fp8_quant.cuh"
 #include "fp8_tma.cuh"
@@ -476,32 +475,34 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
 
 constexpr int kMaxSplit = 8;
 
-// Clusters of `split` CTAs that run at once (SMs share a cluster only within their part of
-// the chip, so of eight at one CTA to an SM fewer fit than the SMs would hold); asked once.
+// Clusters of `split` CTAs that run at once on device `dev`, the current one (SMs share a
+// cluster only within their part of the chip, so of eight at one CTA to an SM fewer fit than
+// the SMs would hold); sets the kernel up for the device when it is first asked.
 template <int kRows, bool kSwiglu>
-cudaError_t clusters_at_once(int split, int num_sms, int* clusters) {
+cudaError_t clusters_at_once(int dev, int split, int num_sms, int* clusters) {
   using L = Few<kRows, kSwiglu>;
-  static int known[kMaxSplit + 1];
-  if (known[split] == 0) {
-    cudaError_t e =
-        cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(split * num_sms);
-    cfg.blockDim = dim3(L::kThreads);
-    cfg.dynamicSmemBytes = L::kSmem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = split, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_few_kernel<kRows, kSwiglu>, &cfg);
-    if (e != cudaSuccess) return e;
-    // (the query counts one CTA to an SM)
-    known[split] = (n < 1 ? 1 : n) * L::kPerSm;
-  }
-  *clusters = known[split];
+  static PerDevice<int> known[kMaxSplit + 1];
+  std::atomic<int>* entry = known[split].of(dev);
+  *clusters = entry ? entry->load() : 0;
+  if (*clusters) return cudaSuccess;
+  cudaError_t e =
+      cudaFuncSetAttribute(fp8_matmul_few_kernel<kRows, kSwiglu>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split * num_sms);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = split, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, fp8_matmul_few_kernel<kRows, kSwiglu>, &cfg);
+  if (e != cudaSuccess) return e;
+  // (the query counts one CTA to an SM)
+  *clusters = (n < 1 ? 1 : n) * L::kPerSm;
+  if (entry) entry->store(*clusters);
   return cudaSuccess;
 }
 
@@ -516,14 +517,15 @@ template <int kRows, bool kSwiglu>
 cudaError_t choose_split(const Fp8MatmulArgs& a, int num_sms, int* split, int* share, long long* waves) {
   const int Kb = (a.K + kScaleBlock - 1) / kScaleBlock;
   const long long tiles = (a.N + 127) / 128 * ((static_cast<long long>(a.M) + kRows - 1) / kRows);
-  int at_once = 0;
-  cudaError_t e = clusters_at_once<kRows, kSwiglu>(1, num_sms, &at_once);
+  int at_once = 0, dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = clusters_at_once<kRows, kSwiglu>(dev, 1, num_sms, &at_once);
   if (e != cudaSuccess) return e;
   *waves = (tiles + at_once - 1) / at_once;
   *split = 1;
   long long best = (tiles + num_sms - 1) / num_sms * Kb;
   for (int c = 2; c <= kMaxSplit && Kb >= 4 * c && tiles * c <= 2LL * num_sms; ++c) {
-    e = clusters_at_once<kRows, kSwiglu>(c, num_sms, &at_once);
+    e = clusters_at_once<kRows, kSwiglu>(dev, c, num_sms, &at_once);
     if (e != cudaSuccess) return e;
     const long long blocks = (tiles * c + num_sms - 1) / num_sms * ((Kb + c - 1) / c);
     if (tiles <= at_once && (blocks < best || (blocks == best && a.weights_ready))) best = blocks, *split = c;
@@ -647,14 +649,16 @@ bool fp8_set_option(int option, int value) {
 }
 
 int32_t* fp8_status_word() {
-  // (one context per device in a process; asked once per device)
-  static int32_t* cached[64];
+  // (one context per device in a process)
+  static PerDevice<int32_t*> known;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
-  if (dev >= 0 && dev < 64 && cached[dev]) return cached[dev];
+  std::atomic<int32_t*>* entry = known.of(dev);
+  if (entry)
+    if (int32_t* word = entry->load()) return word;
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_fp8_status) != cudaSuccess) return nullptr;
-  if (dev >= 0 && dev < 64) cached[dev] = static_cast<int32_t*>(p);
+  if (entry) entry->store(static_cast<int32_t*>(p));
   return static_cast<int32_t*>(p);
 }
 

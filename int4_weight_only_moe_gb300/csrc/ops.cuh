@@ -2,6 +2,7 @@
 // block quantisers and the 8-bit block-scaled product (each in its own translation
 // unit; argument checks are in ops_api.cu).
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -18,6 +19,16 @@ constexpr int kMaxGroups = 32;
 
 // Records `msg` as this thread's last error and returns `code` (api.cu).
 int report_error(int code, const char* msg);
+
+// What is asked once for each device, by any thread (kernel attributes, occupancy and
+// symbols' addresses hold for one device): the entry of device `dev`, null for a device
+// beyond the table, which is asked every time. A zero is not known yet.
+constexpr int kMaxDevices = 64;
+template <typename T>
+struct PerDevice {
+  std::atomic<T> entry[kMaxDevices];
+  std::atomic<T>* of(int dev) { return dev >= 0 && dev < kMaxDevices ? &entry[dev] : nullptr; }
+};
 
 struct RouteScoredArgs {
   const void* logits;  // [M, E], rows row_stride elements apart

@@ -1,6 +1,4 @@
 // C entry points of the operators around the routed experts: argument checks and launches.
-#include <atomic>
-
 #include "../../include/moe_w4a16.h"
 #include "ops.cuh"
 
@@ -23,32 +21,33 @@ bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 int blocks(int n) { return (n + kScaleBlock - 1) / kScaleBlock; }
 
-// SM count of the current device, asked once per device.
+// SM count of the current device.
 int num_sms(cudaError_t* err) {
-  static int cached[64];
+  static PerDevice<int> known;
   int dev = 0;
   *err = cudaGetDevice(&dev);
   if (*err != cudaSuccess) return 0;
-  const bool keep = dev >= 0 && dev < 64;
-  if (keep && cached[dev]) return cached[dev];
-  int n = 0;
+  std::atomic<int>* entry = known.of(dev);
+  int n = entry ? entry->load() : 0;
+  if (n) return n;
   *err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  if (*err == cudaSuccess && keep) cached[dev] = n;
+  if (*err == cudaSuccess && entry) entry->store(n);
   return n;
 }
 
 // Stream-ordered memory pool of the current device, for calls without a workspace; keeps
 // up to 64 MiB between calls.
 cudaMemPool_t scratch_pool(cudaError_t* err) {
-  static std::atomic<cudaMemPool_t> pools[64];
+  static PerDevice<cudaMemPool_t> pools;
   int dev = 0;
   *err = cudaGetDevice(&dev);
   if (*err != cudaSuccess) return nullptr;
-  if (dev < 0 || dev >= 64) {
+  std::atomic<cudaMemPool_t>* entry = pools.of(dev);
+  if (!entry) {
     *err = cudaErrorInvalidDevice;
     return nullptr;
   }
-  cudaMemPool_t pool = pools[dev].load();
+  cudaMemPool_t pool = entry->load();
   if (pool) return pool;
   // (also during a stream capture, which this touches nothing of)
   cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
@@ -63,7 +62,7 @@ cudaMemPool_t scratch_pool(cudaError_t* err) {
     unsigned long long keep = 64ull << 20;
     *err = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
     cudaMemPool_t none = nullptr;
-    if (*err != cudaSuccess || !pools[dev].compare_exchange_strong(none, pool)) {
+    if (*err != cudaSuccess || !entry->compare_exchange_strong(none, pool)) {
       cudaMemPoolDestroy(pool);
       pool = *err == cudaSuccess ? none : nullptr;  // (another thread's)
     }

@@ -1,0 +1,84 @@
+"""The host code of the operators around the routed experts without a GPU: the compiled
+objects linked to a fake CUDA runtime (fake_cuda_runtime.cpp) that logs what is launched."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+OBJECTS = ["route_scored.o", "fp8_quant.o", "fp8_matmul.o", "fp8_many.o", "ops_api.o"]
+BUF = ctypes.c_void_p(4096)  # never read
+F32, BF16 = 0, 1
+
+
+@pytest.fixture(scope="module")
+def library(tmp_path_factory):
+    from int4_weight_only_moe_gb300 import _build
+    _build.build()
+    objects = [os.path.join(_build.BUILD, o) for o in OBJECTS]
+    if not all(map(os.path.exists, objects)):
+        _build.build(force=True)
+    out = str(tmp_path_factory.mktemp("fake") / "libops_fake.so")
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_build.nvcc()))), "include")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-O1", "-w", "-I", include, "-o", out,
+                    os.path.join(here, "fake_cuda_runtime.cpp"), *objects, "-Wl,-Bsymbolic", "-Wl,-z,defs"], check=True)
+    return out
+
+
+@pytest.fixture
+def lib(library, tmp_path):
+    # (a copy of its own: nothing that the code keeps is left over from another test)
+    path = str(tmp_path / "libops_fake.so")
+    with open(library, "rb") as src, open(path, "wb") as dst:
+        dst.write(src.read())
+    L = ctypes.CDLL(path)
+    from int4_weight_only_moe_gb300 import _SIGNATURES
+    for name in ("moe_w4a16_fp8_matmul", "moe_w4a16_shared_expert", "moe_w4a16_fp8_status"):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = _SIGNATURES[name]
+    return L
+
+
+def launched(lib):
+    """(device, kernel, grid, cluster) of every launch so far."""
+    out = []
+    for i in range(lib.fake_launches()):
+        dev, cluster, name, grid = ctypes.c_int(), ctypes.c_int(), ctypes.create_string_buffer(400), (ctypes.c_uint * 3)()
+        lib.fake_launch(i, ctypes.byref(dev), name, 400, grid, ctypes.byref(cluster))
+        out.append((dev.value, name.value.decode(), tuple(grid), cluster.value))
+    return out
+
+
+def matmul(lib, M, N, K, add=None, out=BUF, out_type=BF16):
+    return lib.moe_w4a16_fp8_matmul(BUF, K, BUF, BUF, K, BUF, add, out, out_type, M, N, K, None)
+
+
+def shared(lib, M, K, N):
+    return lib.moe_w4a16_shared_expert(BUF, BUF, BUF, BUF, BUF, None, BUF, M, K, N, BUF, 1 << 40, None)
+
+
+def test_every_device_is_set_up(lib):
+    sizes = [(M, 4096, 7168) for M in (1, 20, 50, 100)] + [(4096, 4096, 1024), (4096, 4095, 1024)]
+    seen = []
+    for dev in (0, 1, 5, 0, 70):
+        lib.fake_device(dev)
+        lib.fake_clear()
+        for M, N, K in sizes:
+            assert matmul(lib, M, N, K) == 0, (dev, M)
+            assert matmul(lib, M, N, K, add=BUF) == 0, (dev, M)
+        for M in (1, 20, 50, 100, 4096):
+            assert shared(lib, M, 1024, 512) == 0, (dev, M)
+        got = launched(lib)
+        assert {d for d, *_ in got} == {dev}
+        seen.append([rest for _, *rest in got])
+    assert all(s == seen[0] for s in seen)
+
+
+def test_a_device_is_asked_once(lib):
+    for dev in (0, 1):
+        lib.fake_device(dev)
+        matmul(lib, 1, 4096, 7168), matmul(lib, 4096, 4096, 1024)
+        lib.fake_clear()
+        matmul(lib, 1, 4096, 7168), matmul(lib, 4096, 4096, 1024)
+        assert lib.fake_launches() == 2 and lib.fake_calls(b"cudaOccupancyMaxActiveClusters") == 0
