@@ -301,9 +301,6 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
       // shared memory is released only after the last copies have landed, whoever gave up
       for (int i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
         mbar_drain(full(i % L::kStages), (i / L::kStages) & 1);
-      // (and the MMAs' last signals, which are writes to it too)
-      for (int i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
-        if (!mbar_wait(empty(i % L::kStages), (i / L::kStages) & 1, abort_flag, status, kStatusTimeout, limit)) break;
     }
   } else if (warp == kWarpMma) {
     constexpr uint32_t idesc = idesc_e4m3_f32(128, L::kBatchIsM ? L::kAccCols : L::kBoxCols);
@@ -461,6 +458,12 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
         if (two) store_out4(a, m0 + j + step, n, y1, vec);
       }
     }
+  } else if (warp == kWarpTma && lane == 0 && !*abort_flag) {
+    // ... and after the MMAs' last signals, which are writes to it too (here, beside the
+    // joining, they cost nothing; ahead of the barrier 0.3 us)
+    const int it = kb1 - kb0;
+    for (int i = it > L::kStages ? it - L::kStages : 0; i < it; ++i)
+      if (!mbar_wait(empty(i % L::kStages), (i / L::kStages) & 1, abort_flag, status, kStatusTimeout, limit)) break;
   }
   __syncwarp();
   if (split > 1) cluster_sync();  // no CTA leaves while another reads its sums
