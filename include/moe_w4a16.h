@@ -301,6 +301,15 @@ int moe_w4a16_fp8_status(int32_t* status, void* stream);
 enum { MOE_W4A16_FP8_OPT_WAIT_LIMIT_US = 1, MOE_W4A16_FP8_OPT_TEST_WAIT_NEVER_COMPLETES = 2 };
 int moe_w4a16_fp8_set_option(int option, int value);
 
+/* The kernel that an 8-bit product of this shape takes, without launching it. stage 0:
+ * moe_w4a16_fp8_matmul with 16-byte aligned operands; 1: the shared expert's gate/up product
+ * (N its features, K the hidden size); 2: its down product. add and out: only their
+ * alignment and whether add is NULL count.
+ *   plan[0]  rows of `a` to a tile: 16, 32, 64 or 128 (weights streamed, few rows), 256
+ *            (many rows), 0 (CUDA cores);  plan[1]  CTAs to a tile */
+int moe_w4a16_fp8_plan_debug(int stage, const uint16_t* add, const void* out, int out_type, int M, int N, int K,
+                             int32_t* plan);
+
 /* Shared expert: the dense SwiGLU feed-forward that every token takes next to its
  * routed experts, with 8-bit block-scaled weights and activations:
  *   q1, s1 = quantize(hidden)              [g | u] = q1 s1 . (w1 w1_s)^T   (fp32)

@@ -25,7 +25,7 @@ __all__ = [
     "STATUS_BAD_SCHEDULE",
     "moe_w4a16_route_scored", "moe_w4a16_fp8_quantize", "moe_w4a16_fp8_swiglu_quantize",
     "moe_w4a16_fp8_quantize_weight", "moe_w4a16_fp8_matmul", "moe_w4a16_shared_expert_workspace_size",
-    "moe_w4a16_shared_expert", "moe_w4a16_fp8_status", "moe_w4a16_fp8_set_option",
+    "moe_w4a16_shared_expert", "moe_w4a16_fp8_status", "moe_w4a16_fp8_set_option", "moe_w4a16_fp8_plan_debug",
     "FP8_OPT_WAIT_LIMIT_US", "FP8_OPT_TEST_WAIT_NEVER_COMPLETES", "F32", "BF16", "SCORE_SOFTMAX", "SCORE_SIGMOID",
 ]
 
@@ -83,6 +83,7 @@ _SIGNATURES = {
     "moe_w4a16_fp8_quantize_weight": (_c_int, [_vp, _c_int, _c_ll, _c_int, _c_int, _vp, _vp, _vp]),
     "moe_w4a16_fp8_matmul": (_c_int, [_vp, _c_ll, _vp, _vp, _c_ll, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                                       _vp]),
+    "moe_w4a16_fp8_plan_debug": (_c_int, [_c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, ctypes.POINTER(ctypes.c_int32)]),
     "moe_w4a16_fp8_set_option": (_c_int, [_c_int, _c_int]),
     "moe_w4a16_fp8_status": (_c_int, [ctypes.POINTER(ctypes.c_int32), _vp]),
     "moe_w4a16_shared_expert_workspace_size": (_c_size, [_c_int, _c_int, _c_int]),
@@ -348,6 +349,13 @@ def moe_w4a16_fp8_quantize_weight(w, w_type, row_stride, N, K, q, s, stream=None
 def moe_w4a16_fp8_matmul(a, lda, a_s, b, ldb, b_s, add, out, out_type, M, N, K, stream=None):
     _check(lib().moe_w4a16_fp8_matmul(_ptr(a), lda, _ptr(a_s), _ptr(b), ldb, _ptr(b_s), _ptr(add), _ptr(out),
                                       out_type, M, N, K, _stream(stream)))
+
+
+def moe_w4a16_fp8_plan_debug(stage, add, out, out_type, M, N, K):
+    """(rows of a tile, CTAs to a tile) of the kernel that a product of this shape takes."""
+    plan = (ctypes.c_int32 * 2)()
+    _check(lib().moe_w4a16_fp8_plan_debug(stage, _ptr(add), _ptr(out), out_type, M, N, K, plan))
+    return plan[0], plan[1]
 
 
 def moe_w4a16_fp8_set_option(option: int, value: int):

@@ -581,29 +581,21 @@ bool tma_ok(const Fp8MatmulArgs& a) {
 }  // namespace
 
 namespace {
-template <int kRows, bool kSwiglu>
-cudaError_t launch_split(const Fp8MatmulArgs& a, int32_t* status, int num_sms, cudaStream_t stream) {
-  int split = 1, share = 0;
-  long long waves = 0;
-  const cudaError_t e = choose_split<kRows, kSwiglu>(a, num_sms, &split, &share, &waves);
-  return e == cudaSuccess ? launch_few<kRows, kSwiglu>(a, split, status, stream) : e;
-}
-
 // Settings of the whole process (moe_w4a16_fp8_set_option).
 std::atomic<int> g_wait_us{0}, g_test_never_wait{0};
 
 // Kernel and split by size.
 template <bool kSwiglu>
-cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStream_t stream) {
-  a.wait_kcycles = wait_limit_kcycles(static_cast<unsigned long long>(g_wait_us.load(std::memory_order_relaxed)));
-  a.test_never_wait = g_test_never_wait.load(std::memory_order_relaxed);
-  if (a.M <= 16) return launch_split<16, kSwiglu>(a, status, num_sms, stream);
-  if (a.M <= 32) return launch_split<32, kSwiglu>(a, status, num_sms, stream);
-  if (a.M <= 64) return launch_split<64, kSwiglu>(a, status, num_sms, stream);
+cudaError_t plan_tiles(const Fp8MatmulArgs& a, int num_sms, Fp8Plan* plan) {
   int split = 1, share = 0;
   long long waves = 0;
-  const cudaError_t e = choose_split<128, kSwiglu>(a, num_sms, &split, &share, &waves);
-  if (e != cudaSuccess) return e;
+  plan->rows = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 ? 64 : 128;
+  const cudaError_t e = a.M <= 16   ? choose_split<16, kSwiglu>(a, num_sms, &split, &share, &waves)
+                        : a.M <= 32 ? choose_split<32, kSwiglu>(a, num_sms, &split, &share, &waves)
+                        : a.M <= 64 ? choose_split<64, kSwiglu>(a, num_sms, &split, &share, &waves)
+                                    : choose_split<128, kSwiglu>(a, num_sms, &split, &share, &waves);
+  plan->split = split;
+  if (e != cudaSuccess || a.M <= 64) return e;
   // Both kernels' times by what they were measured to take, in hundredths of a us: here
   // 30 a block and 500 a wave of CTAs, 300 more with an addend from the second on; there 40 a block and 120 a
   // wave of pairs, 300 in all, and 300 a wave where its output cannot go in whole pieces;
@@ -618,10 +610,32 @@ cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStre
   const long long here = waves * ((kSwiglu ? 45LL : 30LL) * share + 500) + 100 + (a.add ? 300 * (waves - 1) : 0);
   const long long there = (big + pairs - 1) / pairs * (40LL * Kb + 120 + odd) + 300;
   // (a grid's second dimension ends at 65,535 tiles of 128 rows)
-  if (there < here || a.M > 65535LL * 128) return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
-  return launch_few<128, kSwiglu>(a, split, status, stream);
+  if (there < here || a.M > 65535LL * 128) *plan = Fp8Plan{256, 2};
+  return cudaSuccess;
+}
+
+template <bool kSwiglu>
+cudaError_t launch_tiles(Fp8MatmulArgs a, int32_t* status, int num_sms, cudaStream_t stream) {
+  a.wait_kcycles = wait_limit_kcycles(static_cast<unsigned long long>(g_wait_us.load(std::memory_order_relaxed)));
+  a.test_never_wait = g_test_never_wait.load(std::memory_order_relaxed);
+  Fp8Plan plan;
+  const cudaError_t e = plan_tiles<kSwiglu>(a, num_sms, &plan);
+  if (e != cudaSuccess) return e;
+  switch (plan.rows) {
+    case 16: return launch_few<16, kSwiglu>(a, plan.split, status, stream);
+    case 32: return launch_few<32, kSwiglu>(a, plan.split, status, stream);
+    case 64: return launch_few<64, kSwiglu>(a, plan.split, status, stream);
+    case 128: return launch_few<128, kSwiglu>(a, plan.split, status, stream);
+    default: return launch_fp8_many(a, kSwiglu, status, num_sms, stream);
+  }
 }
 }  // namespace
+
+cudaError_t fp8_plan(const Fp8MatmulArgs& a, bool swiglu, int num_sms, Fp8Plan* plan) {
+  *plan = Fp8Plan{0, 1};
+  if (!tma_ok(a)) return cudaSuccess;
+  return swiglu ? plan_tiles<true>(a, num_sms, plan) : plan_tiles<false>(a, num_sms, plan);
+}
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream) {
   if (!tma_ok(a)) {

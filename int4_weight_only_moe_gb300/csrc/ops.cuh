@@ -80,6 +80,12 @@ struct Fp8MatmulArgs {
 // SiLU(gate) * up, quantised.
 cudaError_t launch_fp8_swiglu(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, int num_sms, cudaStream_t stream);
+// What a product takes: batch rows of a tile (16, 32, 64 or 128: the few-row kernel; 256: the
+// many-row one; 0: the CUDA cores) and CTAs to a tile.
+struct Fp8Plan {
+  int rows, split;
+};
+cudaError_t fp8_plan(const Fp8MatmulArgs& a, bool swiglu, int num_sms, Fp8Plan* plan);
 
 // Settings of the products' pipeline waits (MOE_W4A16_FP8_OPT_*); false: no such option
 // or value.

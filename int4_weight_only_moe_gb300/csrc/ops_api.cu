@@ -167,6 +167,26 @@ int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, cons
   return done(launch_fp8_matmul(g, sms, static_cast<cudaStream_t>(stream)));
 }
 
+int moe_w4a16_fp8_plan_debug(int stage, const uint16_t* add, const void* out, int out_type, int M, int N, int K,
+                             int32_t* plan) {
+  if (stage < 0 || stage > 2) return bad("stage must be 0, 1 or 2");
+  if (out_type != MOE_W4A16_F32 && out_type != MOE_W4A16_BF16)
+    return bad("out_type must be MOE_W4A16_F32 or MOE_W4A16_BF16");
+  if (M < 1 || N < 1 || K < 1) return bad("need M, N and K >= 1");
+  if (M > kMaxRows || N > kMaxCols || K > kMaxCols) return shape("too large (at most M = 2^30, N = K = 2^22)");
+  if (stage > 0 && (N % kScaleBlock != 0 || K % kScaleBlock != 0)) return shape("N and K must be multiples of 128");
+  if (!plan) return bad("null pointer argument");
+  cudaError_t e;
+  const int sms = num_sms(&e);
+  if (e != cudaSuccess) return done(e);
+  const Fp8MatmulArgs g{nullptr, K, nullptr, nullptr, K, nullptr, add, const_cast<void*>(out), out_type, M, N, K, stage > 0,
+                        nullptr, 0, 0};
+  Fp8Plan p{};
+  e = fp8_plan(g, stage == 1, sms, &p);
+  plan[0] = p.rows, plan[1] = p.split;
+  return done(e);
+}
+
 int moe_w4a16_fp8_set_option(int option, int value) {
   return fp8_set_option(option, value) ? MOE_W4A16_OK : bad("unknown option, or a value out of its range");
 }

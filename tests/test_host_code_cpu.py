@@ -34,7 +34,8 @@ def lib(library, tmp_path):
         dst.write(src.read())
     L = ctypes.CDLL(path)
     from int4_weight_only_moe_gb300 import _SIGNATURES
-    for name in ("moe_w4a16_fp8_matmul", "moe_w4a16_shared_expert", "moe_w4a16_fp8_status"):
+    for name in ("moe_w4a16_fp8_matmul", "moe_w4a16_shared_expert", "moe_w4a16_fp8_status",
+                 "moe_w4a16_fp8_plan_debug"):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = _SIGNATURES[name]
     return L
@@ -82,3 +83,39 @@ def test_a_device_is_asked_once(lib):
         lib.fake_clear()
         matmul(lib, 1, 4096, 7168), matmul(lib, 4096, 4096, 1024)
         assert lib.fake_launches() == 2 and lib.fake_calls(b"cudaOccupancyMaxActiveClusters") == 0
+
+
+KERNELS = {16: "few_kernelILi16E", 32: "few_kernelILi32E", 64: "few_kernelILi64E", 128: "few_kernelILi128E",
+           256: "many_kernel", 0: "plain_kernel"}
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 32, 40, 64, 65, 100, 200, 300, 700, 3000])
+def test_the_plan_is_what_is_launched(lib, M):
+    plan = (ctypes.c_int32 * 2)()
+    for N, K in ((130, 16), (1024, 512), (4096, 7168), (2047, 272), (640, 1000)):
+        for add in (None, BUF):
+            for out in (BUF, ctypes.c_void_p(4098)):
+                lib.fake_clear()
+                assert matmul(lib, M, N, K, add=add, out=out) == 0
+                assert lib.moe_w4a16_fp8_plan_debug(0, add, out, BF16, M, N, K, plan) == 0
+                (_, kernel, _, cluster), = launched(lib)
+                assert KERNELS[plan[0]] in kernel and plan[1] == cluster
+    for K, N in ((256, 128), (7168, 2048), (2048, 384), (4096, 512)):
+        lib.fake_clear()
+        assert shared(lib, M, K, N) == 0
+        _, up, down = launched(lib)
+        assert lib.moe_w4a16_fp8_plan_debug(1, None, BUF, BF16, M, N, K, plan) == 0
+        assert KERNELS[plan[0]] in up[1] and plan[1] == up[3]
+        assert lib.moe_w4a16_fp8_plan_debug(2, None, BUF, BF16, M, K, N, plan) == 0
+        assert KERNELS[plan[0]] in down[1] and plan[1] == down[3]
+
+
+def test_plan_refusals(lib):
+    plan = (ctypes.c_int32 * 2)()
+    good = [0, None, BUF, BF16, 4, 128, 256, plan]
+    for at, value, rc in [(0, 3, -1), (0, -1, -1), (3, 7, -1), (4, 0, -1), (5, 0, -1), (6, 0, -1), (5, 1 << 23, -2),
+                          (7, None, -1)]:
+        args = list(good)
+        args[at] = value
+        assert lib.moe_w4a16_fp8_plan_debug(*args) == rc
+    assert lib.moe_w4a16_fp8_plan_debug(1, None, BUF, BF16, 4, 100, 256, plan) == -2
