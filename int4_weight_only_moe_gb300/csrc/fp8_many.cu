@@ -368,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpMma && rank == 0) {
       const uint32_t idesc = idesc_e4m3_f32(kTileM, kTileN);
       const bool leader = elect_one();
+      pdl_wait();  // (the waits' clocks start behind the preceding kernel: the copies come no earlier)
       int st = 0, ac = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;

@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(Few<kRows, kSwiglu>::kThreads)
   } else if (warp == kWarpMma) {
     constexpr uint32_t idesc = idesc_e4m3_f32(128, L::kBatchIsM ? L::kAccCols : L::kBoxCols);
     const bool leader = elect_one();
+    pdl_wait();  // (the waits' clocks start behind the preceding kernel: the rows come no earlier)
     int st = 0, ac = 0;
     uint32_t ph = 0, aph = 0;
     for (int kb = kb0; kb < kb1; ++kb) {

@@ -108,3 +108,31 @@ def test_wait_limit_of_shared_experts(M, K, N, rows):
     assert plan(1, M, N, K) == rows
     w, x = expert(K, N, M), rand((M, K), 2)
     gives_up(lambda: fp8.shared_expert(x, *w))
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 512, 2048), (20, 512, 2048), (50, 512, 2048), (100, 256, 1024), (2048, 2048, 512),
+                                   (2049, 2047, 144)])
+def test_wait_limit_does_not_count_the_kernel_in_front(M, N, K):
+    # (in front: a product of 8 CTAs that lets the next one start at once and takes many times the limit)
+    deep = 1 << 22
+    a, b = torch.zeros(1, deep, dtype=torch.uint8, device="cuda"), torch.zeros(128, deep, dtype=torch.uint8, device="cuda")
+    a_s, b_s = torch.ones(1, deep // 128, device="cuda"), torch.ones(1, deep // 128, device="cuda")
+    ops = operands(M, N, K, M)
+    want = fp8.matmul(*ops)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    fp8.matmul(a, a_s, b, b_s)
+    assert fp8.status() == 0
+    begin.record()
+    fp8.matmul(a, a_s, b, b_s)
+    end.record()
+    end.synchronize()
+    limit = 25  # us, of at least 4 cycles a nanosecond: about 50 at this part's clock
+    assert begin.elapsed_time(end) * 1e3 > 10 * limit
+    pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, limit)
+    try:
+        fp8.matmul(a, a_s, b, b_s)
+        got = fp8.matmul(*ops)
+        assert fp8.status() == 0
+    finally:
+        pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, 0)
+    assert torch.equal(got, want)
