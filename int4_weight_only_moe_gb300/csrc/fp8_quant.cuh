@@ -36,10 +36,11 @@ __device__ __forceinline__ float block_scale(float amax) {
 // x / s, correctly rounded, from r = 1 / s correctly rounded: q = x r, then one step with
 // the exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990). Only for scales in [2^-90, 2^90], where the remainder
-// stays in fp32's range.
+// stays in fp32's range. (The remainder is taken as q s - x: x - q s would be +0 for x = -0
+// and make the quotient +0.)
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
+  return fmaf(-fmaf(q, s, -x), r, q);
 }
 
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
