@@ -15,13 +15,21 @@
 // One warp per token. Lane l holds a run of consecutive experts of one group (32 /
 // n_group lanes to a group), so that lower lane, then lower slot, is the lower id: the
 // tie rule costs nothing. The lanes' best, sorted, give a bound that leaves little more
-// than topk candidates; those move one to a lane and count the better ones. Bound by
-// its instructions: 16,384 tokens of 384 experts, top-8, take 12.5 us (26 MB of logits
-// could be read in 3.9); with topk rounds of a warp-wide maximum instead, 16.5.
+// than topk candidates; those move one to a lane and count the better ones.
+// 16,384 tokens of 384 experts, top-8, take 12.3 us with sigmoid and bias (26 MB of logits
+// could be read in 3.9), 11.0 without a bias; with topk rounds of a warp-wide maximum
+// instead, 16.5. Neither the issue slots (59%) nor memory (20%) are full: what bounds it is
+// the latency of a token's loads and of its chain of exchanges, beside which a warp has
+// nothing else to do.
 //
-// All arithmetic is fp32. The selection's scores come from the hardware's exponential and
-// reciprocal (a few 2^-22 of the score, so that values closer than that may rank either
-// way; equal logits stay equal), the weights of the chosen from the full-precision ones.
+// Without a bias the logits themselves are ranked, whose order the scores keep (a softmax's
+// from 104 below the row's largest on, where fp32 has only 0, count as equal). With one, and
+// for the sum of a group's two, the scores come from the hardware's exponential and
+// reciprocal, results below 2^-126 kept: a few 2^-22 of the score, and |x| 2^-23 more for an
+// exponent x (rounded before the exponential), so that values closer than that may rank
+// either way; equal logits stay equal. The weights of the chosen take the full-precision
+// exponential and divisions; a softmax divides by the sum of the short ones, whose errors
+// count by their terms' share (x exp(-x) 2^-23: below 2^-22 in all). All arithmetic is fp32.
 #include <cfloat>
 
 #include "ops.cuh"
@@ -32,8 +40,8 @@ namespace {
 constexpr int kRouteThreads = 128;
 
 // Order-preserving map of a float to an unsigned integer, and back; NaN ranks as
-// -infinity. 0 is below every value: no candidate. (A choice is never -0: scores are
-// not negative.)
+// -infinity. 0 is below every value: no candidate. (A choice is never -0: what is ranked
+// had a bias or +0 added.)
 __device__ __forceinline__ uint32_t order_key(float c) {
   const uint32_t u = __float_as_uint(fmaxf(c, -INFINITY));
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
@@ -60,6 +68,19 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 constexpr float kLog2e = 1.44269504f;
+
+// The selection's score of a logit v plus b (`top`: the row's largest, `rz` 1 / the softmax's
+// sum), results below 2^-126 kept: the softmax's exponential as a square, the sigmoid as
+// 16 / (1 + exp(-v)) / 16, which is a normal number wherever exp(-v) is finite.
+template <bool kSoftmax>
+__device__ __forceinline__ float score_plus(float v, float top, float rz, float b) {
+  if (kSoftmax) {
+    const float root = exp2_fast((v - top) * (0.5f * kLog2e));
+    return fmaf(root * root, rz, b);
+  }
+  return fmaf(rcp_fast(fmaf(exp2_fast(-v * kLog2e), 0.0625f, 0.0625f)), 0.0625f, b);
+}
+constexpr float kSoftmaxReach = 104.f;  // exp(-104) is 0 in fp32
 
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const float4 t = *reinterpret_cast<const float4*>(p);
@@ -100,7 +121,7 @@ __device__ __forceinline__ Best2 run_best2(F key) {
 // bias allow loads of four values.
 // (The warps an SM holds hide the selection's chain of exchanges: 64 of them for runs of up
 // to 8 -- 4,097 x 160 takes 4.9 us, 6.8 with the registers left free -- 48 and 40 up to 16.)
-template <int C, bool kSoftmax, typename T>
+template <int C, bool kSoftmax, bool kBias, typename T>
 __global__ void __launch_bounds__(kRouteThreads, C <= 8 ? 16 : C <= 12 ? 12 : C <= 16 ? 10 : 1) route_scored_kernel(RouteScoredArgs a, int P, int c, bool vec) {
   pdl_wait();
   pdl_launch_dependents();
@@ -112,23 +133,26 @@ __global__ void __launch_bounds__(kRouteThreads, C <= 8 ? 16 : C <= 12 ? 12 : C 
   const int n = g < a.n_group ? min(c, gs - base) : 0;  // (may be negative: no experts)
   const int e0 = g * gs + base;
   const T* row = static_cast<const T*>(a.logits) + t * a.row_stride;
-  float v[C], bias[C];
+  float v[C], bias[kBias ? C : 1];
   if (vec) {
 #pragma unroll
     for (int i = 0; i < C; i += 4) {
       float q[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, b[4] = {0.f, 0.f, 0.f, 0.f};
       if (i < n) {
+        if (kBias) load4(a.bias + e0 + i, b);
         load4(row + e0 + i, q);
-        if (a.bias) load4(a.bias + e0 + i, b);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[i + k] = clean_logit(q[k]), bias[i + k] = b[k];
+      for (int k = 0; k < 4; ++k) {
+        v[i + k] = clean_logit(q[k]);
+        if (kBias) bias[i + k] = b[k];
+      }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       v[i] = i < n ? clean_logit(to_f32(row[e0 + i])) : -INFINITY;
-      bias[i] = i < n && a.bias ? a.bias[e0 + i] : 0.f;
+      if (kBias) bias[i] = i < n ? a.bias[e0 + i] : 0.f;
     }
   }
   float top = 0.f, z = 1.f, rz = 1.f;
@@ -151,8 +175,14 @@ __global__ void __launch_bounds__(kRouteThreads, C <= 8 ? 16 : C <= 12 ? 12 : C 
   uint32_t key[C];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    const float s = kSoftmax ? exp2_fast((v[i] - top) * kLog2e) * rz : rcp_fast(1.0f + exp2_fast(-v[i] * kLog2e));
-    key[i] = order_key(v[i] == -INFINITY ? -INFINITY : s + bias[i]);
+    float choice;
+    if constexpr (kBias) {
+      choice = v[i] == -INFINITY ? -INFINITY : score_plus<kSoftmax>(v[i], top, rz, bias[i]);
+    } else {
+      const bool none = kSoftmax && v[i] < top - kSoftmaxReach && v[i] != -INFINITY;
+      choice = (none ? -FLT_MAX : v[i]) + 0.f;
+    }
+    key[i] = order_key(choice);
   }
   if (n < C) {
 #pragma unroll
@@ -167,7 +197,11 @@ __global__ void __launch_bounds__(kRouteThreads, C <= 8 ? 16 : C <= 12 ? 12 : C 
       t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
       t1 = fmaxf(t1, o1);
     }
-    const uint32_t mine = order_key(a.group_top == 2 && t2 != -INFINITY ? t1 + t2 : t1);
+    if (kBias)
+      t1 = a.group_top == 2 && t2 != -INFINITY ? t1 + t2 : t1;
+    else if (a.group_top == 2 && t1 != -INFINITY)
+      t1 = score_plus<kSoftmax>(t1, top, rz, t2 == -INFINITY ? 0.f : score_plus<kSoftmax>(t2, top, rz, 0.f));
+    const uint32_t mine = order_key(t1);
     int ahead = 0;
     for (int j = 0; j < a.n_group; ++j) {
       const uint32_t other = __shfl_sync(0xffffffffu, mine, j * P);
@@ -263,7 +297,7 @@ __global__ void __launch_bounds__(kRouteThreads, C <= 8 ? 16 : C <= 12 ? 12 : C 
   }
 }
 
-template <bool kSoftmax, typename T>
+template <bool kSoftmax, bool kBias, typename T>
 cudaError_t launch_typed(const RouteScoredArgs& a, cudaStream_t stream) {
   int groups = 1;
   while (groups < a.n_group) groups *= 2;
@@ -275,19 +309,23 @@ cudaError_t launch_typed(const RouteScoredArgs& a, cudaStream_t stream) {
   constexpr int per = kRouteThreads / 32;
   const dim3 grid((static_cast<unsigned>(a.M) + per - 1) / per);
   auto go = [&](auto kernel) { return launch_k(kernel, grid, dim3(kRouteThreads), 0, stream, true, a, P, c, vec); };
-  if (c <= 4) return go(route_scored_kernel<4, kSoftmax, T>);
-  if (c <= 8) return go(route_scored_kernel<8, kSoftmax, T>);
-  if (c <= 12) return go(route_scored_kernel<12, kSoftmax, T>);
-  if (c <= 16) return go(route_scored_kernel<16, kSoftmax, T>);
-  if (c <= 32) return go(route_scored_kernel<32, kSoftmax, T>);
-  return go(route_scored_kernel<64, kSoftmax, T>);  // (c <= 60: at most 1,024 experts, over half of the lanes in use)
+  if (c <= 4) return go(route_scored_kernel<4, kSoftmax, kBias, T>);
+  if (c <= 8) return go(route_scored_kernel<8, kSoftmax, kBias, T>);
+  if (c <= 12) return go(route_scored_kernel<12, kSoftmax, kBias, T>);
+  if (c <= 16) return go(route_scored_kernel<16, kSoftmax, kBias, T>);
+  if (c <= 32) return go(route_scored_kernel<32, kSoftmax, kBias, T>);
+  return go(route_scored_kernel<64, kSoftmax, kBias, T>);  // (c <= 60: at most 1,024 experts, over half of the lanes in use)
 }
 
 }  // namespace
 
 cudaError_t launch_route_scored(const RouteScoredArgs& a, cudaStream_t stream) {
-  if (a.logits_type == kTypeF32) return a.softmax ? launch_typed<true, float>(a, stream) : launch_typed<false, float>(a, stream);
-  return a.softmax ? launch_typed<true, uint16_t>(a, stream) : launch_typed<false, uint16_t>(a, stream);
+  auto go = [&](auto value) {
+    using T = decltype(value);
+    if (a.softmax) return a.bias ? launch_typed<true, true, T>(a, stream) : launch_typed<true, false, T>(a, stream);
+    return a.bias ? launch_typed<false, true, T>(a, stream) : launch_typed<false, false, T>(a, stream);
+  };
+  return a.logits_type == kTypeF32 ? go(float{}) : go(uint16_t{});
 }
 
 }  // namespace moe
