@@ -247,8 +247,8 @@ enum { MOE_W4A16_SCORE_SOFTMAX = 0, MOE_W4A16_SCORE_SIGMOID = 1 };
  * Without a bias the logits are ranked themselves (group_top 1: the groups by their largest),
  * so that scores which 32 bits would round to the same number keep their order; a softmax's
  * more than 104 below the row's largest logit are 0, and equal. With a bias values closer
- * than a few 2^-22 of the score (2^-23 of it for each unit of the exponent more) may rank
- * either way.
+ * than a few 2^-22 of the score (2^-23 of it for each unit of the exponent more), or than
+ * 2^-148, may rank either way.
  * Equal values: the lower group, the lower expert id. A logit of -infinity or NaN
  * marks an expert that is not to be chosen: it ranks behind every other one of the
  * groups that stay, counts nothing in its group's value, and where a row holds too few

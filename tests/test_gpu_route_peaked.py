@@ -69,3 +69,18 @@ def test_sigmoid_scores_below_the_normal_numbers():
     l[0, 5], l[0, 2] = -87.4, -88.0
     ids, _ = routing.route_scored(dev(l), 3, scoring="sigmoid", bias=torch.zeros(8, device="cuda"))
     assert ids.tolist() == [[5, 2, 0]]
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("far", [1, 5, 20, 40, 60, 70])
+def test_scores_further_apart_than_the_stated_error_keep_their_order(scoring, far):
+    # neighbours differ by twice the error of a score, 4 x 2^-22 + far 2^-23 of it, and by two
+    # ulps of the logits' own rounding (scores of 3e-37 and more: below 2^-126 their own spacing counts)
+    E = 32
+    step = 2 * (4 * 2.0 ** -22 + far * 2.0 ** -23) + 2 * float(np.spacing(np.float32(far)))
+    rng = np.random.default_rng(far)
+    l = np.empty((200, E), np.float32)
+    for t in range(200):
+        l[t, rng.permutation(E)] = np.concatenate([[0.0], -far * (1 + 0.2 * rng.random()) - step * np.arange(E - 1)])
+    ids, _ = routing.route_scored(dev(l), E, scoring=scoring, bias=torch.zeros(E, device="cuda"))
+    np.testing.assert_array_equal(ids.cpu().numpy(), np.argsort(-l, 1, kind="stable"))
