@@ -375,7 +375,8 @@ def moe_w4a16_shared_expert_workspace_size(M: int, K: int, N: int) -> int:
 def moe_w4a16_shared_expert(hidden, w1, w1_s, w2, w2_s, add, out, M, K, N, workspace, stream=None):
     _check(lib().moe_w4a16_shared_expert(_ptr(hidden), _ptr(w1), _ptr(w1_s), _ptr(w2), _ptr(w2_s), _ptr(add),
                                          _ptr(out), M, K, N, _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+                                         0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                         _stream(stream)))
 
 
 class MoEW4A16:

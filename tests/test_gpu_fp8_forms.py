@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import int4_weight_only_moe_gb300 as pkg
-from int4_weight_only_moe_gb300 import BF16, F32, fp8
+from int4_weight_only_moe_gb300 import BF16, F32, fp8, routing
 from tests.gpu_helpers import assert_close, bf16_tensor_to_f64
 from tests.test_gpu_fp8 import (_built, check_product, expert, expert_reference, operands,  # noqa: F401 (a fixture)
                                 rand)
@@ -136,3 +136,36 @@ def test_wait_limit_does_not_count_the_kernel_in_front(M, N, K):
     finally:
         pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, 0)
     assert torch.equal(got, want)
+
+
+def test_plain_binding():
+    # (the calls of the C header as they are, without the checks of fp8 and routing)
+    M, K, N = 20, 256, 128
+    x, w = rand((M, K), 1), rand((N, K), 2, 0.05)
+    new = lambda *shape, dtype: torch.empty(shape, dtype=dtype, device="cuda")
+    byte = lambda t: t.view(torch.uint8)
+    a, a_s, b, b_s = fp8.quantize(x) + fp8.quantize_weight(w)
+    q, s = new(M, K, dtype=torch.uint8), new(M, 2, dtype=torch.float32)
+    pkg.moe_w4a16_fp8_quantize(x, BF16, K, M, K, q, s)
+    assert torch.equal(q, byte(a)) and torch.equal(s, a_s)
+    q, s = new(N, K, dtype=torch.uint8), new(1, 2, dtype=torch.float32)
+    pkg.moe_w4a16_fp8_quantize_weight(w, BF16, K, N, K, q, s)
+    assert torch.equal(q, byte(b)) and torch.equal(s, b_s)
+    q, s = new(M, N, dtype=torch.uint8), new(M, 1, dtype=torch.float32)
+    pkg.moe_w4a16_fp8_swiglu_quantize(x, BF16, K, M, N, q, s)
+    want = fp8.swiglu_quantize(x)
+    assert torch.equal(q, byte(want[0])) and torch.equal(s, want[1])
+    out = new(M, N, dtype=torch.float32)
+    pkg.moe_w4a16_fp8_matmul(a, K, a_s, b, K, b_s, None, out, F32, M, N, K)
+    assert torch.equal(out, fp8.matmul(a, a_s, b, b_s, out_dtype=torch.float32))
+    ids, wts = new(M, 8, dtype=torch.int32), new(M, 8, dtype=torch.float32)
+    pkg.moe_w4a16_route_scored(x, BF16, K, M, K, 8, pkg.SCORE_SIGMOID, None, 1, 1, 1, True, 1.0, ids, wts)
+    want = routing.route_scored(x, 8)
+    assert torch.equal(ids, want[0]) and torch.equal(wts, want[1])
+    e = expert(K, N, 3)
+    want = fp8.shared_expert(x, *e)
+    ws = new(pkg.moe_w4a16_shared_expert_workspace_size(M, K, N), dtype=torch.uint8)
+    for workspace in (ws, None):
+        out = new(M, K, dtype=torch.bfloat16)
+        pkg.moe_w4a16_shared_expert(x, *e, None, out, M, K, N, workspace)
+        assert torch.equal(out, want)

@@ -93,3 +93,18 @@ def test_every_tensor_has_to_be_on_the_current_device(launches, name):
     with pytest.raises(ValueError, match="current device"):
         call(t)
     assert len(launches) == 1
+
+
+def test_plain_binding_without_a_workspace(launches, monkeypatch):
+    import int4_weight_only_moe_gb300 as pkg
+    seen = {}
+
+    class Lib:
+        def moe_w4a16_shared_expert(self, *args):
+            seen["args"] = args
+            return 0
+
+    monkeypatch.setattr(pkg, "lib", Lib)
+    t = {k: Tensor(*v) for k, v in CALLS["shared"][1].items()}
+    pkg.moe_w4a16_shared_expert(t["x"], t["w1"], t["w1_s"], t["w2"], t["w2_s"], None, t["out"], 4, 256, 128, None, stream=0)
+    assert seen["args"][5] == 0 and seen["args"][7:12] == (4, 256, 128, 0, 0)
