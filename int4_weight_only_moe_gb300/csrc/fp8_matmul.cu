@@ -683,8 +683,12 @@ int32_t* fp8_status_word() {
 cudaError_t fp8_status(int32_t* out, cudaStream_t stream) {
   int32_t* p = fp8_status_word();
   if (!p) return cudaErrorInvalidSymbol;
+  // (cleared only when it is reported: a product of another stream may give up meanwhile, which
+  // a clean answer must not hide. It sets the one bit that there is.)
   cudaError_t e = cudaMemcpyAsync(out, p, sizeof(*p), cudaMemcpyDeviceToHost, stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, sizeof(*p), stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
+  if (e != cudaSuccess || *out == 0) return e;
+  e = cudaMemsetAsync(p, 0, sizeof(*p), stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   return e;
 }

@@ -119,3 +119,15 @@ def test_plan_refusals(lib):
         args[at] = value
         assert lib.moe_w4a16_fp8_plan_debug(*args) == rc
     assert lib.moe_w4a16_fp8_plan_debug(1, None, BUF, BF16, 4, 100, 256, plan) == -2
+
+
+def test_status_clears_what_it_reports_and_nothing_else(lib):
+    value = ctypes.c_int32(-1)
+    lib.fake_status(0)
+    assert lib.moe_w4a16_fp8_status(ctypes.byref(value), None) == 0 and value.value == 0
+    # (clean: a product that gives up on another stream right now must still be seen)
+    assert lib.fake_calls(b"cudaMemcpyAsync") == 1 and lib.fake_calls(b"cudaMemsetAsync") == 0
+    lib.fake_status(2)
+    assert lib.moe_w4a16_fp8_status(ctypes.byref(value), None) == 0 and value.value == 2
+    assert lib.fake_calls(b"cudaMemsetAsync") == 1
+    assert lib.moe_w4a16_fp8_status(ctypes.byref(value), None) == 0 and value.value == 0
