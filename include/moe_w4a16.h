@@ -275,7 +275,8 @@ int moe_w4a16_route_scored(const void* logits, int logits_type, long long row_st
  * (computed in fp32): q [M, N], s [M, ceil(N / 128)].
  * quantize_weight: one scale for each block of 128 rows x 128 columns of w [N, K]:
  * s [ceil(N / 128), ceil(K / 128)].
- * M == 0 (N == 0) is a no-op. One launch on `stream`, no host synchronisation. */
+ * At most 2^30 rows (2^22 of a weight) and 2^22 columns; M == 0 (N == 0) is a no-op. One
+ * launch on `stream` (one for each 2^30 blocks), no host synchronisation. */
 int moe_w4a16_fp8_quantize(const void* x, int x_type, long long row_stride, int M, int K, uint8_t* q, float* s,
                            void* stream);
 int moe_w4a16_fp8_swiglu_quantize(const void* gate_up, int x_type, long long row_stride, int M, int N, uint8_t* q,
@@ -290,7 +291,9 @@ int moe_w4a16_fp8_quantize_weight(const void* w, int w_type, long long row_strid
  *   b    [N, K] bytes, rows ldb bytes apart;  b_s fp32 [ceil(N / 128), ceil(K / 128)]
  *   add  bf16 [M, N] or NULL; may be `out` itself when out_type is bf16
  *   out  bf16 or fp32 (out_type) [M, N]
- * Any M, N >= 0 and K >= 1, contiguous scales, add and out. M == 0 or N == 0 is a
+ * 0 <= M <= 2^30, 0 <= N <= 2^22, 1 <= K <= 2^22; contiguous scales, add and out. K that
+ * is no multiple of 16, or operands whose addresses or row strides are not, run on the CUDA
+ * cores, a hundred times slower at thousands of rows. M == 0 or N == 0 is a
  * no-op. One launch on `stream`, no workspace, no host synchronisation, and the same
  * result in every run (no atomics). */
 int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, const uint8_t* b, long long ldb,
