@@ -224,8 +224,8 @@ int moe_w4a16_finalize(const float* acc, uint16_t* out, long long n, void* strea
  * They launch on the current device: every pointer is that device's, and `stream` too
  * (the Python calls check it). */
 
-/* Element types of the floating inputs and outputs below. */
-enum { MOE_W4A16_F32 = 0, MOE_W4A16_BF16 = 1 };
+/* Element types of the inputs and outputs below (E4M3: bytes, moved and not computed with). */
+enum { MOE_W4A16_F32 = 0, MOE_W4A16_BF16 = 1, MOE_W4A16_E4M3 = 2 };
 
 /* Scores of moe_w4a16_route_scored. */
 enum { MOE_W4A16_SCORE_SOFTMAX = 0, MOE_W4A16_SCORE_SIGMOID = 1 };
@@ -240,10 +240,6 @@ enum { MOE_W4A16_SCORE_SOFTMAX = 0, MOE_W4A16_SCORE_SIGMOID = 1 };
  *   the experts of the topk_group best groups stay
  *   topk_ids = the topk largest c that stay, in descending order
  *   topk_weights = s of those, divided by their sum if `renormalize`, times `scale`
- * Without a bias the logits are ranked themselves (group_top 1: the groups by their largest),
- * so that scores which 32 bits would round to the same number keep their order; a softmax's
- * more than 104 below the row's largest logit are 0, and equal. With a bias values closer
- * than a few 2^-22 of the score may rank either way.
  * Without a bias the logits are ranked themselves (group_top 1: the groups by their largest),
  * so that scores which 32 bits would round to the same number keep their order; a softmax's
  * more than 104 below the row's largest logit are 0, and equal. With a bias values closer
@@ -341,6 +337,99 @@ size_t moe_w4a16_shared_expert_workspace_size(int M, int K, int N);
 int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const float* w1_s, const uint8_t* w2,
                             const float* w2_s, const uint16_t* add, uint16_t* out, int M, int K, int N,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Tokens sorted by expert, for expert products of the caller's own, and back.
+ *
+ * The order of the experts' rows. Slot i = t * topk + j is token t's j-th choice, its
+ * expert topk_ids[i] - expert_begin; ids outside [expert_begin, expert_begin + E) are
+ * nobody's here (another part's experts, or -1 for a dropped choice). The rows are the
+ * slots by expert, then by slot, each expert's rows filled up to a multiple of `block`:
+ *   rows      moe_w4a16_dispatch_rows(M, topk, E, block) = n + min(E, n) (block - 1) with
+ *             n = M topk: as many as there can be (-1: sizes that are not supported)
+ *   offsets   int32 [E + 1]   out: where each expert's rows begin, and the end of the last's
+ *   slots     int32 [rows]    out: the slot of a row; -1 in rows that fill up and behind the last
+ *   position  int32 [M, topk] out: the row of a slot; -1 for nobody's
+ * The same expert may stand twice among a token's choices. 1 <= E <= 1024, topk <= 32, at
+ * most 2^30 rows. M == 0 gives offsets of 0. One launch, no host synchronisation; the same
+ * result in every run.
+ *
+ * gather: out[position[t, j]] = x[t]; 0 in rows that fill up an expert's; rows behind
+ * offsets[E] are left as they were.
+ *   x    fp32, bf16 or bytes (type) [M, K], rows row_stride elements apart
+ *   out  [rows, K] of the same type
+ * K <= 2^22. Its gradient is moe_w4a16_combine without weights. One launch.
+ *
+ * sort_gather: both, at most two launches.
+ *
+ * combine: out[t] = sum_j weights[t, j] y[position[t, j]] (+ add[t]), summed in fp32 in the
+ * order of j, the addend last, rounded once. Positions outside [0, rows) count nothing: a
+ * token of which no choice is left gives 0 (or add).
+ *   y        fp32 or bf16 (y_type) [rows, K]
+ *   weights  fp32 [M, topk], or NULL for weights of 1
+ *   add      [M, K] of out's type, or NULL; may be out
+ *   out      fp32 or bf16 (out_type) [M, K]
+ * One launch.
+ *
+ * combine_backward: the gradient of combine (with weights) for grad = dL/dout:
+ *   dy[position[t, j]] = weights[t, j] grad[t]   (0 in rows that fill up; rows behind
+ *                                                 offsets[E] are left as they were)
+ *   dweights[t, j] = <grad[t], y[position[t, j]]>   in fp32; 0 where there is no row
+ *   grad  fp32 or bf16 (grad_type) [M, K];  y, dy  fp32 or bf16 (y_type) [rows, K], not the
+ *   same array;  dweights fp32 [M, topk]
+ * (The gradient of add is grad itself.) One launch. */
+long long moe_w4a16_dispatch_rows(int M, int topk, int E, int block);
+int moe_w4a16_dispatch_sort(const int32_t* topk_ids, int M, int topk, int expert_begin, int E, int block,
+                            int32_t* offsets, int32_t* slots, int32_t* position, void* stream);
+int moe_w4a16_dispatch_gather(const void* x, int type, long long row_stride, const int32_t* offsets,
+                              const int32_t* slots, const int32_t* position, void* out, int M, int K, int topk, int E,
+                              int block, void* stream);
+int moe_w4a16_dispatch_sort_gather(const void* x, int type, long long row_stride, const int32_t* topk_ids, int M, int K,
+                                   int topk, int expert_begin, int E, int block, int32_t* offsets, int32_t* slots,
+                                   int32_t* position, void* out, void* stream);
+int moe_w4a16_combine(const void* y, int y_type, const float* weights, const int32_t* position, const void* add,
+                      void* out, int out_type, int M, int K, int topk, int rows, void* stream);
+int moe_w4a16_combine_backward(const void* grad, int grad_type, const void* y, int y_type, const float* weights,
+                               const int32_t* offsets, const int32_t* slots, const int32_t* position, void* dy,
+                               float* dweights, int M, int K, int topk, int E, int block, void* stream);
+
+/* Gradient of moe_w4a16_route_scored's weights with regard to its logits (the selection is
+ * taken as it is, the bias has no part in the weights). With s the scores of the chosen
+ * experts, T their sum, g = dweights:
+ *   u = scale (g - sum g s / T) / T if `renormalize`, else scale g
+ *   sigmoid: dlogits = u s (1 - s) at the chosen experts, 0 elsewhere
+ *   softmax: dlogits_e = s_e (u_e - sum u s), u_e = 0 where e is not chosen
+ * in fp32, rounded once. A logit of -infinity or NaN gets 0 and counts nothing, +infinity
+ * counts as the largest number; an id outside [0, E) counts nothing; of an expert that
+ * stands twice the gradients add up. Renormalised, the quotients s / T are those of the
+ * scores however small they are (of chosen logits far below 0, or far below the row's
+ * largest), also where 32 bits round the scores themselves to 0.
+ *   dweights fp32 [M, topk], topk_ids int32 [M, topk]
+ *   logits   fp32 or bf16 (logits_type) [M, E], rows row_stride elements apart
+ *   dlogits  [M, E] of the same type, not the logits themselves    out
+ * One launch on `stream`, no host synchronisation. */
+int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, int logits_type, long long row_stride,
+                                    const int32_t* topk_ids, int M, int E, int topk, int scoring, int renormalize,
+                                    float scale, void* dlogits, void* stream);
+
+/* Low-rank adapters of many requests beside a projection (whose output is the addend):
+ *   out[m] = add[m] + scale[l] b[l] (a[l] x[m]),  l = index[m]
+ * and out[m] = add[m] where index[m] lies outside [0, L): a row without an adapter.
+ *   x      bf16 [M, K], rows ldx elements apart;  index int32 [M]
+ *   a      bf16 [L, r, K];  b bf16 [L, N, r];  scale fp32 [L], or NULL for 1. Adapters of
+ *          smaller rank are filled up with zeros
+ *   add    fp32 or bf16 (add_type) [M, N], or NULL for 0; may be out where the types are
+ *          the same (rows without an adapter are then not touched)
+ *   out    fp32 or bf16 (out_type) [M, N], rounded once
+ *   workspace  >= moe_w4a16_lora_workspace_size(M, K, N, r, L) bytes (0 for sizes that are
+ *          not supported, and where none is needed), 256-byte aligned; holds nothing between
+ *          calls. NULL: as in moe_w4a16_shared_expert
+ * 1 <= r <= 128 (a larger rank is two adapters, one call after the other), 1 <= L <= 1023, M
+ * up to 2^29, K and N up to 2^22. M == 0 is a no-op. No host synchronisation; the same
+ * result in every run. */
+size_t moe_w4a16_lora_workspace_size(int M, int K, int N, int r, int L);
+int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const uint16_t* b, const float* scale,
+                   const int32_t* index, const void* add, int add_type, void* out, int out_type, int M, int K, int N,
+                   int r, int L, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Read the device status word of the last forward that used `workspace`
  * (bits MOE_W4A16_STATUS_*; 0 = clean). Synchronises `stream`. */

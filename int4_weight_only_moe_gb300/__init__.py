@@ -26,6 +26,9 @@ __all__ = [
     "moe_w4a16_route_scored", "moe_w4a16_fp8_quantize", "moe_w4a16_fp8_swiglu_quantize",
     "moe_w4a16_fp8_quantize_weight", "moe_w4a16_fp8_matmul", "moe_w4a16_shared_expert_workspace_size",
     "moe_w4a16_shared_expert", "moe_w4a16_fp8_status", "moe_w4a16_fp8_set_option", "moe_w4a16_fp8_plan_debug",
+    "moe_w4a16_dispatch_rows", "moe_w4a16_dispatch_sort", "moe_w4a16_dispatch_gather",
+    "moe_w4a16_dispatch_sort_gather", "moe_w4a16_combine", "moe_w4a16_combine_backward",
+    "moe_w4a16_route_scored_backward", "moe_w4a16_lora", "moe_w4a16_lora_workspace_size", "E4M3",
     "FP8_OPT_WAIT_LIMIT_US", "FP8_OPT_TEST_WAIT_NEVER_COMPLETES", "F32", "BF16", "SCORE_SOFTMAX", "SCORE_SIGMOID",
 ]
 
@@ -42,7 +45,7 @@ OPT_FUSED_SMALL_BATCH = 8
 OPT_GEMV_SMALL_BATCH = 9
 OPT_GEMV_ONE_LAUNCH = 10
 NOALLOC_WORKSPACE_BYTES = 48 << 20
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 FP8_OPT_WAIT_LIMIT_US, FP8_OPT_TEST_WAIT_NEVER_COMPLETES = 1, 2
 
@@ -87,6 +90,16 @@ _SIGNATURES = {
     "moe_w4a16_fp8_set_option": (_c_int, [_c_int, _c_int]),
     "moe_w4a16_fp8_status": (_c_int, [ctypes.POINTER(ctypes.c_int32), _vp]),
     "moe_w4a16_shared_expert_workspace_size": (_c_size, [_c_int, _c_int, _c_int]),
+    "moe_w4a16_dispatch_rows": (_c_ll, [_c_int] * 4),
+    "moe_w4a16_dispatch_sort": (_c_int, [_vp] + [_c_int] * 5 + [_vp] * 4),
+    "moe_w4a16_dispatch_gather": (_c_int, [_vp, _c_int, _c_ll, _vp, _vp, _vp, _vp] + [_c_int] * 5 + [_vp]),
+    "moe_w4a16_dispatch_sort_gather": (_c_int, [_vp, _c_int, _c_ll, _vp] + [_c_int] * 6 + [_vp] * 5),
+    "moe_w4a16_combine": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp] + [_c_int] * 5 + [_vp]),
+    "moe_w4a16_combine_backward": (_c_int, [_vp, _c_int, _vp, _c_int] + [_vp] * 6 + [_c_int] * 5 + [_vp]),
+    "moe_w4a16_route_scored_backward": (_c_int, [_vp, _vp, _c_int, _c_ll, _vp] + [_c_int] * 5 +
+                                        [ctypes.c_float, _vp, _vp]),
+    "moe_w4a16_lora_workspace_size": (_c_size, [_c_int] * 5),
+    "moe_w4a16_lora": (_c_int, [_vp, _c_ll] + [_vp] * 5 + [_c_int, _vp] + [_c_int] * 6 + [_vp, _c_size, _vp]),
     "moe_w4a16_shared_expert": (_c_int, [_vp] * 7 + [_c_int, _c_int, _c_int, _vp, _c_size, _vp]),
 }
 
@@ -377,6 +390,57 @@ def moe_w4a16_shared_expert(hidden, w1, w1_s, w2, w2_s, add, out, M, K, N, works
                                          _ptr(out), M, K, N, _ptr(workspace),
                                          0 if workspace is None else workspace.numel() * workspace.element_size(),
                                          _stream(stream)))
+
+
+def moe_w4a16_dispatch_rows(M: int, topk: int, E: int, block: int) -> int:
+    return int(lib().moe_w4a16_dispatch_rows(M, topk, E, block))
+
+
+def moe_w4a16_dispatch_sort(topk_ids, M, topk, expert_begin, E, block, offsets, slots, position, stream=None):
+    _check(lib().moe_w4a16_dispatch_sort(_ptr(topk_ids), M, topk, expert_begin, E, block, _ptr(offsets), _ptr(slots),
+                                         _ptr(position), _stream(stream)))
+
+
+def moe_w4a16_dispatch_gather(x, type_, row_stride, offsets, slots, position, out, M, K, topk, E, block, stream=None):
+    _check(lib().moe_w4a16_dispatch_gather(_ptr(x), type_, row_stride, _ptr(offsets), _ptr(slots), _ptr(position),
+                                           _ptr(out), M, K, topk, E, block, _stream(stream)))
+
+
+def moe_w4a16_dispatch_sort_gather(x, type_, row_stride, topk_ids, M, K, topk, expert_begin, E, block, offsets, slots,
+                                   position, out, stream=None):
+    _check(lib().moe_w4a16_dispatch_sort_gather(_ptr(x), type_, row_stride, _ptr(topk_ids), M, K, topk, expert_begin,
+                                                E, block, _ptr(offsets), _ptr(slots), _ptr(position), _ptr(out),
+                                                _stream(stream)))
+
+
+def moe_w4a16_combine(y, y_type, weights, position, add, out, out_type, M, K, topk, rows, stream=None):
+    _check(lib().moe_w4a16_combine(_ptr(y), y_type, _ptr(weights), _ptr(position), _ptr(add), _ptr(out), out_type, M, K,
+                                   topk, rows, _stream(stream)))
+
+
+def moe_w4a16_combine_backward(grad, grad_type, y, y_type, weights, offsets, slots, position, dy, dweights, M, K, topk,
+                               E, block, stream=None):
+    _check(lib().moe_w4a16_combine_backward(_ptr(grad), grad_type, _ptr(y), y_type, _ptr(weights), _ptr(offsets),
+                                            _ptr(slots), _ptr(position), _ptr(dy), _ptr(dweights), M, K, topk, E, block,
+                                            _stream(stream)))
+
+
+def moe_w4a16_route_scored_backward(dweights, logits, logits_type, row_stride, topk_ids, M, E, topk, scoring,
+                                    renormalize, scale, dlogits, stream=None):
+    _check(lib().moe_w4a16_route_scored_backward(_ptr(dweights), _ptr(logits), logits_type, row_stride, _ptr(topk_ids),
+                                                 M, E, topk, scoring, renormalize, scale, _ptr(dlogits),
+                                                 _stream(stream)))
+
+
+def moe_w4a16_lora_workspace_size(M: int, K: int, N: int, r: int, L: int) -> int:
+    return int(lib().moe_w4a16_lora_workspace_size(M, K, N, r, L))
+
+
+def moe_w4a16_lora(x, ldx, a, b, scale, index, add, add_type, out, out_type, M, K, N, r, L, workspace, stream=None):
+    _check(lib().moe_w4a16_lora(_ptr(x), ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(index), _ptr(add), add_type,
+                                _ptr(out), out_type, M, K, N, r, L, _ptr(workspace),
+                                0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                _stream(stream)))
 
 
 class MoEW4A16:

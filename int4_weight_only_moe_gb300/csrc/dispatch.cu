@@ -1,0 +1,455 @@
+// Tokens sorted by expert and back: the order of the experts' rows, the gather of the
+// tokens into it, the weighted sum of the experts' rows for each token, and its gradient.
+//
+//   slot i = t * topk + j: token t's j-th choice. Rows: by expert, then by slot, an
+//   expert's rows filled up to a multiple of `block`.
+//   gather             out[position[t, j]] = x[t]
+//   combine            out[t] = sum_j w[t, j] y[position[t, j]] (+ add[t])
+//   combine backward   dy[position[t, j]] = w[t, j] g[t],  dw[t, j] = <g[t], y[position[t, j]]>
+//   (the gather's gradient is the combine with weights of 1)
+//
+// All of it moves memory and computes next to nothing, so each kernel goes by token: it
+// reads a token's row once and its topk rows in the sorted order once. Sums are fp32 in the
+// order of j: the same bits in every run (no atomics on values).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "fp8_tma.cuh"
+#include "ops.cuh"
+
+namespace moe {
+namespace {
+
+// ------------------------------------------------------------------------------ the order
+
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kMaxBuckets = 1024;  // one to a thread
+
+// Bucket of an expert id: the expert's, one more for all other ids (`rest`), or none.
+__device__ __forceinline__ int bucket_of(const SortArgs& a, int id) {
+  const uint32_t l = static_cast<uint32_t>(id) - static_cast<uint32_t>(a.begin);
+  return l < static_cast<uint32_t>(a.E) ? static_cast<int>(l) : (a.rest ? a.E : -1);
+}
+
+// Exclusive prefix sum over the block; *total gets the sum.
+__device__ int block_scan(int v, int* warp_sum, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) warp_sum[w] = x;
+  __syncthreads();
+  if (w == 0) {
+    int s = lane < warps ? warp_sum[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += y;
+    }
+    warp_sum[lane] = s;
+  }
+  __syncthreads();
+  const int before = (w > 0 ? warp_sum[w - 1] : 0) + x - v;
+  *total = warp_sum[warps - 1];
+  __syncthreads();
+  return before;
+}
+
+__device__ __forceinline__ int ld_shared_rank(const int* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_rank(smem_u32(p), rank)) : "memory");
+  return static_cast<int>(v);
+}
+
+// Stable counting sort by one cluster. Each warp owns a run of consecutive slots and
+// counts it by itself; prefix sums over the warps, the CTAs of the cluster and the buckets
+// give every warp the first row of its own slots of each bucket, and a second pass over the
+// run hands the rows out in order.
+__global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs a, int ctas) {
+  extern __shared__ int sm[];
+  const int B = a.E + (a.rest ? 1 : 0);
+  int* hist = sm;                     // [warps][B]: counts, then slots of the bucket already placed by this CTA
+  int* mine = hist + kSortWarps * B;  // [B]: this CTA's counts, read by the whole cluster
+  int* base = mine + B;               // [B]: row of this CTA's first slot
+  int* ends = base + B;               // [B]: row behind the last slot
+  __shared__ int warp_sum[32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
+  for (int i = tid; i < kSortWarps * B; i += kSortThreads) hist[i] = 0;
+  __syncthreads();
+  pdl_wait();
+  const int run = (a.n + kSortWarps * ctas - 1) / (kSortWarps * ctas);
+  const long long first = static_cast<long long>(rank * kSortWarps + w) * run;
+  const int lo = static_cast<int>(min(first, static_cast<long long>(a.n)));
+  const int hi = static_cast<int>(min(first + run, static_cast<long long>(a.n)));
+  for (int i = lo + lane; i < hi; i += 32) {
+    const int b = bucket_of(a, a.ids[i]);
+    if (b >= 0) atomicAdd(&hist[w * B + b], 1);
+  }
+  __syncthreads();
+  int own = 0;
+  if (tid < B) {
+    for (int v = 0; v < kSortWarps; ++v) {
+      const int c = hist[v * B + tid];
+      hist[v * B + tid] = own;
+      own += c;
+    }
+    mine[tid] = own;
+  }
+  int count = own, before = 0;
+  if (ctas > 1) {
+    cluster_sync();
+    count = 0;
+    if (tid < B)
+      for (int r = 0; r < ctas; ++r) {
+        const int c = ld_shared_rank(mine + tid, r);
+        if (r < rank) before += c;
+        count += c;
+      }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  }
+  int total;
+  const int start = block_scan((count + a.block - 1) / a.block * a.block, warp_sum, &total);
+  if (tid < B) {
+    base[tid] = start + before;
+    ends[tid] = start + count;
+    if (rank == 0) a.offsets[tid] = start;
+  }
+  if (rank == 0 && tid == 0) a.offsets[B] = total;
+  __syncthreads();
+  // rows that fill up, and rows behind the last
+  if (a.block > 1)
+    for (int b = rank * kSortWarps + w; b < B; b += ctas * kSortWarps) {
+      const int e = ends[b], next = (e + a.block - 1) / a.block * a.block;  // (all starts are multiples of `block`)
+      for (int r = e + lane; r < next; r += 32) a.slots[r] = -1;
+    }
+  for (long long r = total + static_cast<long long>(rank) * kSortThreads + tid; r < a.capacity; r += ctas * kSortThreads)
+    a.slots[r] = -1;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const int i = i0 + lane;
+    const int b = i < hi ? bucket_of(a, a.ids[i]) : -1;
+    const unsigned peers = __match_any_sync(0xffffffffu, b);
+    int row = -1;
+    if (b >= 0) row = base[b] + hist[w * B + b] + __popc(peers & ((1u << lane) - 1u));
+    __syncwarp();
+    if (b >= 0 && lane == __ffs(peers) - 1) hist[w * B + b] += __popc(peers);
+    __syncwarp();
+    if (i < hi && a.position) a.position[i] = row;
+    if (b >= 0) a.slots[row] = i;
+  }
+  // (no CTA leaves while another may still read its counts)
+  if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------------------------- the rows
+
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+
+// 16-, 4-, 2- or 1-byte pieces, whichever the rows' lengths and addresses allow.
+template <int kBytes>
+struct Piece;
+template <>
+struct Piece<16> {
+  using T = uint4;
+};
+template <>
+struct Piece<4> {
+  using T = uint32_t;
+};
+template <>
+struct Piece<2> {
+  using T = uint16_t;
+};
+template <>
+struct Piece<1> {
+  using T = uint8_t;
+};
+
+// Zeros for the rows that fill up experts, by the CTAs behind those of the tokens: a warp
+// takes every (warps of these CTAs)-th row.
+template <int kBytes>
+__device__ __forceinline__ void zero_filling(const int32_t* slots, int rows, uint8_t* out, long long row_bytes, int cta,
+                                             int ctas) {
+  using T = typename Piece<kBytes>::T;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int r = cta * kRowWarps + w; r < rows; r += ctas * kRowWarps) {
+    if (slots[r] >= 0) continue;
+    T* to = reinterpret_cast<T*>(out + r * row_bytes);
+    for (int v = lane; v < row_bytes / kBytes; v += 32) to[v] = T{};
+  }
+}
+
+// Token t's row to its places; `parts` CTAs share a row.
+template <int kBytes>
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherRowsArgs a, int parts, int fill_ctas) {
+  using T = typename Piece<kBytes>::T;
+  __shared__ int row_of[kMaxTopk];
+  pdl_wait();
+  const long long cta = blockIdx.x;
+  if (cta >= static_cast<long long>(a.M) * parts) {
+    zero_filling<kBytes>(a.slots, min(a.offsets[a.E], a.capacity), static_cast<uint8_t*>(a.out), a.row_bytes,
+                         static_cast<int>(cta - static_cast<long long>(a.M) * parts), fill_ctas);
+    return;
+  }
+  const int t = static_cast<int>(cta / parts), part = static_cast<int>(cta % parts);
+  if (threadIdx.x < a.topk) row_of[threadIdx.x] = a.position[static_cast<long long>(t) * a.topk + threadIdx.x];
+  const int n = static_cast<int>(a.row_bytes / kBytes), per = (n + parts - 1) / parts;
+  const int lo = part * per, hi = min(n, lo + per);
+  const T* from = reinterpret_cast<const T*>(static_cast<const uint8_t*>(a.x) + t * a.stride_bytes);
+  uint8_t* out = static_cast<uint8_t*>(a.out);
+  constexpr int kOnce = 4;
+  __syncthreads();
+  for (int v0 = lo + threadIdx.x; v0 < hi; v0 += kOnce * kRowThreads) {
+    T x[kOnce];
+#pragma unroll
+    for (int i = 0; i < kOnce; ++i)
+      if (v0 + i * kRowThreads < hi) x[i] = from[v0 + i * kRowThreads];
+    for (int j = 0; j < a.topk; ++j) {
+      const int r = row_of[j];
+      if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.capacity)) continue;
+      T* to = reinterpret_cast<T*>(out + r * a.row_bytes);
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i)
+        if (v0 + i * kRowThreads < hi) to[v0 + i * kRowThreads] = x[i];
+    }
+  }
+}
+
+// n consecutive values of a row as fp32, and back.
+template <typename T, int n>
+struct Values;
+template <>
+struct Values<float, 1> {
+  static __device__ __forceinline__ void load(const void* p, float (&f)[1]) { f[0] = *static_cast<const float*>(p); }
+  static __device__ __forceinline__ void store(void* p, const float (&f)[1]) { *static_cast<float*>(p) = f[0]; }
+};
+template <>
+struct Values<uint16_t, 1> {
+  static __device__ __forceinline__ void load(const void* p, float (&f)[1]) {
+    f[0] = __uint_as_float(static_cast<uint32_t>(*static_cast<const uint16_t*>(p)) << 16);
+  }
+  static __device__ __forceinline__ void store(void* p, const float (&f)[1]) {
+    *static_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(f[0]);
+  }
+};
+template <>
+struct Values<float, 8> {
+  static __device__ __forceinline__ void load(const void* p, float (&f)[8]) {
+    const float4 u = static_cast<const float4*>(p)[0], v = static_cast<const float4*>(p)[1];
+    f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+  }
+  static __device__ __forceinline__ void store(void* p, const float (&f)[8]) {
+    static_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    static_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+template <>
+struct Values<uint16_t, 8> {
+  static __device__ __forceinline__ void load(const void* p, float (&f)[8]) {
+    const uint4 u = *static_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ void store(void* p, const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ T* at(void* p, long long row, long long K, int k) {
+  return static_cast<T*>(p) + row * K + k;
+}
+template <typename T>
+__device__ __forceinline__ const T* at(const void* p, long long row, long long K, int k) {
+  return static_cast<const T*>(p) + row * K + k;
+}
+
+// out[t] = sum_j w y[row of j] (+ add[t]); `parts` CTAs share a row, kOnce rows of y are
+// under way at a time.
+template <typename Ty, typename To, int n>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs a, int parts) {
+  constexpr int kOnce = 8;
+  __shared__ int row_of[kMaxTopk];
+  __shared__ float weight_of[kMaxTopk];
+  pdl_wait();
+  const int t = static_cast<int>(blockIdx.x / parts), part = static_cast<int>(blockIdx.x % parts);
+  if (threadIdx.x < a.topk) {
+    const long long i = static_cast<long long>(t) * a.topk + threadIdx.x;
+    const int r = a.position[i];
+    row_of[threadIdx.x] = static_cast<uint32_t>(r) < static_cast<uint32_t>(a.rows) ? r : -1;
+    weight_of[threadIdx.x] = a.weights ? a.weights[i] : 1.0f;
+  }
+  const int pieces = a.K / n, per = (pieces + parts - 1) / parts;
+  const int lo = part * per, hi = min(pieces, lo + per);
+  __syncthreads();
+  for (int v = lo + threadIdx.x; v < hi; v += kRowThreads) {
+    float acc[n];
+#pragma unroll
+    for (int i = 0; i < n; ++i) acc[i] = 0.f;
+    for (int j0 = 0; j0 < a.topk; j0 += kOnce) {
+      float y[kOnce][n];
+#pragma unroll
+      for (int j = 0; j < kOnce; ++j)
+        if (j0 + j < a.topk && row_of[j0 + j] >= 0) Values<Ty, n>::load(at<Ty>(a.y, row_of[j0 + j], a.K, v * n), y[j]);
+#pragma unroll
+      for (int j = 0; j < kOnce; ++j)
+        if (j0 + j < a.topk && row_of[j0 + j] >= 0) {
+#pragma unroll
+          for (int i = 0; i < n; ++i) acc[i] = fmaf(weight_of[j0 + j], y[j][i], acc[i]);
+        }
+    }
+    if (a.add) {
+      float d[n];
+      Values<To, n>::load(at<To>(a.add, t, a.K, v * n), d);
+#pragma unroll
+      for (int i = 0; i < n; ++i) acc[i] += d[i];
+    }
+    Values<To, n>::store(at<To>(a.out, t, a.K, v * n), acc);
+  }
+}
+
+// One CTA to a token: each thread keeps its own part of the topk sums of products, which
+// the CTA joins at the end.
+template <typename Tg, typename Ty, int n>
+__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const CombineBackwardArgs a, int fill_ctas) {
+  constexpr int kOnce = 8;
+  __shared__ int row_of[kMaxTopk];
+  __shared__ float weight_of[kMaxTopk];
+  __shared__ float part_of[kRowWarps][kOnce];
+  pdl_wait();
+  if (blockIdx.x >= static_cast<unsigned>(a.M)) {
+    zero_filling<n * sizeof(Ty) >= 16 ? 16 : n * static_cast<int>(sizeof(Ty))>(
+        a.slots, min(a.offsets[a.E], a.capacity), static_cast<uint8_t*>(a.dy), a.K * static_cast<long long>(sizeof(Ty)),
+        blockIdx.x - a.M, fill_ctas);
+    return;
+  }
+  const int t = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  if (threadIdx.x < a.topk) {
+    const long long i = static_cast<long long>(t) * a.topk + threadIdx.x;
+    const int r = a.position[i];
+    row_of[threadIdx.x] = static_cast<uint32_t>(r) < static_cast<uint32_t>(a.capacity) ? r : -1;
+    weight_of[threadIdx.x] = a.weights[i];
+  }
+  __syncthreads();
+  for (int j0 = 0; j0 < a.topk; j0 += kOnce) {
+    float dot[kOnce] = {};
+    for (int v = threadIdx.x; v < a.K / n; v += kRowThreads) {
+      float g[n];
+      Values<Tg, n>::load(at<Tg>(a.g, t, a.K, v * n), g);
+      float y[kOnce][n];
+#pragma unroll
+      for (int j = 0; j < kOnce; ++j)
+        if (j0 + j < a.topk && row_of[j0 + j] >= 0) Values<Ty, n>::load(at<Ty>(a.y, row_of[j0 + j], a.K, v * n), y[j]);
+#pragma unroll
+      for (int j = 0; j < kOnce; ++j)
+        if (j0 + j < a.topk && row_of[j0 + j] >= 0) {
+          float d[n];
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            dot[j] = fmaf(g[i], y[j][i], dot[j]);
+            d[i] = weight_of[j0 + j] * g[i];
+          }
+          Values<Ty, n>::store(at<Ty>(a.dy, row_of[j0 + j], a.K, v * n), d);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kOnce; ++j) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+      if (lane == 0) part_of[w][j] = dot[j];
+    }
+    __syncthreads();
+    if (threadIdx.x < kOnce && j0 + threadIdx.x < a.topk) {
+      float sum = 0.f;
+      for (int i = 0; i < kRowWarps; ++i) sum += part_of[i][threadIdx.x];
+      a.dweights[static_cast<long long>(t) * a.topk + j0 + threadIdx.x] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+// CTAs to a row of `pieces` pieces: one, unless the tokens alone leave SMs without work.
+int row_parts(long long M, int pieces, int num_sms) {
+  const int most = (pieces + kRowThreads - 1) / kRowThreads;
+  const long long want = (2LL * num_sms + M - 1) / std::max(1LL, M);
+  return static_cast<int>(std::max(1LL, std::min<long long>(most, want)));
+}
+
+}  // namespace
+
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
+  static PerDevice<int> ready;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* entry = ready.of(dev);
+  if (!entry || !entry->load()) {
+    e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kSortWarps + 3) * kMaxBuckets * 4);
+    if (e != cudaSuccess) return e;
+    if (entry) entry->store(1);
+  }
+  const int B = a.E + (a.rest ? 1 : 0);
+  const int ctas = a.n > 4 * kSortThreads ? 8 : 1;
+  return launch_cluster(sort_kernel, dim3(ctas), dim3(kSortThreads), (kSortWarps + 3) * B * sizeof(int), stream, ctas, a, ctas);
+}
+
+cudaError_t launch_gather(const GatherRowsArgs& a, int num_sms, cudaStream_t stream) {
+  const int fill = a.block > 1 ? 2 * num_sms : 0;
+  auto go = [&](auto bytes) {
+    constexpr int n = decltype(bytes)::value;
+    const int parts = row_parts(a.M, static_cast<int>(a.row_bytes / n), num_sms);
+    return launch_k(gather_kernel<n>, dim3(static_cast<unsigned>(static_cast<long long>(a.M) * parts + fill)), dim3(kRowThreads), 0,
+                    stream, true, a, parts, fill);
+  };
+  const uintptr_t all = static_cast<uintptr_t>(a.row_bytes) | static_cast<uintptr_t>(a.stride_bytes) |
+                        reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out);
+  if (all % 16 == 0) return go(std::integral_constant<int, 16>{});
+  if (all % 4 == 0) return go(std::integral_constant<int, 4>{});
+  if (all % 2 == 0) return go(std::integral_constant<int, 2>{});
+  return go(std::integral_constant<int, 1>{});
+}
+
+cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t stream) {
+  const bool wide = a.K % 8 == 0 && aligned(a.y, 16) && aligned(a.add, 16) && aligned(a.out, 16);
+  auto go = [&](auto ty, auto to) {
+    using Ty = decltype(ty);
+    using To = decltype(to);
+    auto with = [&](auto kernel, int n) {
+      const int parts = row_parts(a.M, a.K / n, num_sms);
+      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) * parts), dim3(kRowThreads), 0, stream, true, a, parts);
+    };
+    return wide ? with(combine_kernel<Ty, To, 8>, 8) : with(combine_kernel<Ty, To, 1>, 1);
+  };
+  if (a.y_type == kTypeF32) return a.out_type == kTypeF32 ? go(float{}, float{}) : go(float{}, uint16_t{});
+  return a.out_type == kTypeF32 ? go(uint16_t{}, float{}) : go(uint16_t{}, uint16_t{});
+}
+
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, cudaStream_t stream) {
+  const bool wide = a.K % 8 == 0 && aligned(a.y, 16) && aligned(a.g, 16) && aligned(a.dy, 16);
+  const int fill = a.block > 1 ? 2 * num_sms : 0;
+  auto go = [&](auto tg, auto ty) {
+    using Tg = decltype(tg);
+    using Ty = decltype(ty);
+    auto with = [&](auto kernel) {
+      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) + fill), dim3(kRowThreads), 0, stream, true, a, fill);
+    };
+    return wide ? with(combine_backward_kernel<Tg, Ty, 8>) : with(combine_backward_kernel<Tg, Ty, 1>);
+  };
+  if (a.g_type == kTypeF32) return a.y_type == kTypeF32 ? go(float{}, float{}) : go(float{}, uint16_t{});
+  return a.y_type == kTypeF32 ? go(uint16_t{}, float{}) : go(uint16_t{}, uint16_t{});
+}
+
+}  // namespace moe

@@ -87,6 +87,97 @@ struct Fp8Plan {
 };
 cudaError_t fp8_plan(const Fp8MatmulArgs& a, bool swiglu, int num_sms, Fp8Plan* plan);
 
+// The order of experts' rows (dispatch.cu). Buckets: E experts from id `begin` on, and with
+// `rest` one more that takes every other id (at most 1,024 in all).
+struct SortArgs {
+  const int32_t* ids;  // [n]
+  int n, begin, E;
+  int rest;
+  int block;           // rows of a bucket are filled up to a multiple
+  int32_t* offsets;    // [buckets + 1]
+  int32_t* slots;      // [capacity]
+  int capacity;
+  int32_t* position;   // [n] or null
+};
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream);
+
+constexpr int kMaxTopk = 32;
+// out[position[t, j]] = x[t], zeros in the rows that fill up.
+struct GatherRowsArgs {
+  const void* x;  // [M] rows stride_bytes apart
+  long long stride_bytes, row_bytes;
+  const int32_t* offsets;
+  const int32_t* slots;
+  const int32_t* position;
+  void* out;      // [capacity] rows
+  int M, topk, E, block, capacity;
+};
+cudaError_t launch_gather(const GatherRowsArgs& a, int num_sms, cudaStream_t stream);
+
+// out[t] = sum_j weights[t, j] y[position[t, j]] (+ add[t])
+struct CombineArgs {
+  const void* y;  // [rows, K]
+  int y_type;
+  const float* weights;  // [M, topk], or null: 1
+  const int32_t* position;
+  const void* add;       // [M, K] of the output's type, or null
+  void* out;             // [M, K]
+  int out_type;
+  int M, K, topk, rows;
+};
+cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t stream);
+
+struct CombineBackwardArgs {
+  const void* g;  // [M, K]
+  int g_type;
+  const void* y;  // [capacity, K], and dy
+  int y_type;
+  const float* weights;
+  const int32_t* offsets;
+  const int32_t* slots;
+  const int32_t* position;
+  void* dy;
+  float* dweights;  // [M, topk]
+  int M, K, topk, E, block, capacity;
+};
+cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, cudaStream_t stream);
+
+struct RouteBackwardArgs {
+  const float* dweights;  // [M, topk]
+  const void* logits;     // [M, E], rows row_stride elements apart
+  int logits_type;
+  long long row_stride;
+  const int32_t* ids;     // [M, topk]
+  int M, E, topk, softmax, renormalize;
+  float scale;
+  void* dlogits;          // [M, E], of the logits' type
+};
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t stream);
+
+// out[m] = add[m] + scale[l] b[l] (a[l] x[m]), l = index[m]; add[m] where that is no adapter.
+struct LoraArgs {
+  const uint16_t* x;  // [M, K], rows ldx apart
+  long long ldx;
+  const uint16_t* a;  // [L, r, K]
+  const uint16_t* b;  // [L, N, r]
+  const float* scale;  // [L] or null: 1
+  const int32_t* index;
+  const void* add;  // [M, N] or null
+  int add_type;
+  void* out;
+  int out_type;
+  int M, K, N, r, L;
+  void* workspace;  // lora_workspace_bytes()
+};
+constexpr int kMaxRank = 128;
+size_t lora_workspace_bytes(int M, int r, int L);
+cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream);
+
+// SM count of the current device, and a stream-ordered memory pool of the library's own on
+// it (ops_api.cu).
+int num_sms(cudaError_t* err);
+cudaMemPool_t scratch_pool(cudaError_t* err);
+
 // Settings of the products' pipeline waits (MOE_W4A16_FP8_OPT_*); false: no such option
 // or value.
 bool fp8_set_option(int option, int value);

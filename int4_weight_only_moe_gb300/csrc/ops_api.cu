@@ -21,6 +21,10 @@ bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 int blocks(int n) { return (n + kScaleBlock - 1) / kScaleBlock; }
 
+}  // namespace
+
+namespace moe {
+
 // SM count of the current device.
 int num_sms(cudaError_t* err) {
   static PerDevice<int> known;
@@ -71,6 +75,10 @@ cudaMemPool_t scratch_pool(cudaError_t* err) {
   if (*err == cudaSuccess) *err = back;
   return *err == cudaSuccess ? pool : nullptr;
 }
+
+}  // namespace moe
+
+namespace {
 
 int check_quant(const void* x, int x_type, long long row_stride, int M, int cols, int width, const void* q,
                 const void* s) {

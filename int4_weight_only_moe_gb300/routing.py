@@ -3,7 +3,8 @@
 ``route_scored`` turns the gate's logits into the ``topk_ids`` and ``topk_weights`` that
 ``MoEW4A16.forward`` takes (definition: ``moe_w4a16_route_scored`` in
 ``include/moe_w4a16.h``). ``MoEW4A16.route`` is the plain form, a softmax over the
-selected logits.
+selected logits. ``route_scored_backward`` takes the gradient of those weights back to the
+logits.
 """
 from __future__ import annotations
 
@@ -91,3 +92,25 @@ def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_gro
         renormalize, scale, _dense(ids, torch.int32, (M, topk), "ids", dev),
         _dense(weights, torch.float32, (M, topk), "weights", dev), _handle(stream, dev)))
     return ids, weights
+
+
+def route_scored_backward(dweights, logits, ids, scoring="sigmoid", renormalize=True, scale=1.0, out=None, stream=None):
+    """Gradient with regard to ``logits`` [M, E] (fp32 or bf16, and so is it) of the weights
+    of ``route_scored``, for their gradient ``dweights`` fp32 [M, topk] and the chosen ``ids``
+    int32 [M, topk]; ``scoring``, ``renormalize`` and ``scale`` as they were there."""
+    M, E, stride = _rows(logits, "logits", _TYPES)
+    dev = _device(logits, "logits")
+    score = _SCORES.get(scoring)
+    if score is None:
+        raise ValueError(f"scoring: {scoring!r}, expected one of {tuple(_SCORES)}")
+    if ids.dim() != 2:
+        raise ValueError(f"ids: shape {tuple(ids.shape)}, expected two dimensions")
+    topk = ids.shape[1]
+    i = _dense(ids, torch.int32, (M, topk), "ids", dev)
+    g = _dense(dweights, torch.float32, (M, topk), "dweights", dev)
+    if out is None:
+        out = _new((M, E), logits.dtype, logits.device, stream)
+    _check(lib().moe_w4a16_route_scored_backward(
+        g, logits.data_ptr(), _TYPES[logits.dtype], stride, i, M, E, topk, score, renormalize, scale,
+        _dense(out, logits.dtype, (M, E), "out", dev), _handle(stream, dev)))
+    return out
