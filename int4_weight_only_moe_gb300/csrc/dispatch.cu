@@ -169,30 +169,38 @@ struct Piece<1> {
   using T = uint8_t;
 };
 
-// Zeros for the rows that fill up experts, by the CTAs behind those of the tokens: a warp
-// takes every (warps of these CTAs)-th row.
+// Zeros for the rows that fill up the experts', by CTAs behind those of the tokens: each
+// takes kFillRows rows at a multiple of that from the end of an expert's. (Consecutive rows by
+// one CTA: 352 MB take 55 us; 94 with the rows dealt out to the warps of two CTAs an SM.)
+constexpr int kFillRows = 16;
+int fill_parts(int block) { return std::min(64, (block - 1 + kFillRows - 1) / kFillRows); }  // CTAs to an expert
 template <int kBytes>
-__device__ __forceinline__ void zero_filling(const int32_t* slots, int rows, uint8_t* out, long long row_bytes, int cta,
-                                             int ctas) {
+__device__ __forceinline__ void zero_filling(const int32_t* offsets, const int32_t* slots, int capacity, uint8_t* out,
+                                             long long row_bytes, int cta, int parts) {
   using T = typename Piece<kBytes>::T;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int r = cta * kRowWarps + w; r < rows; r += ctas * kRowWarps) {
-    if (slots[r] >= 0) continue;
-    T* to = reinterpret_cast<T*>(out + r * row_bytes);
-    for (int v = lane; v < row_bytes / kBytes; v += 32) to[v] = T{};
+  const int e = cta / parts, begin = max(offsets[e], 0), end = min(offsets[e + 1], capacity);
+  const int n = static_cast<int>(row_bytes / kBytes);
+  for (int last = end - (cta % parts) * kFillRows; last > begin; last -= parts * kFillRows) {
+    const int first = max(begin, last - kFillRows);
+    if (slots[last - 1] >= 0) return;  // (the tokens' rows stand in front)
+    for (int r = first; r < last; ++r) {
+      if (slots[r] >= 0) continue;
+      T* to = reinterpret_cast<T*>(out + r * row_bytes);
+      for (int v = threadIdx.x; v < n; v += kRowThreads) to[v] = T{};
+    }
   }
 }
 
-// Token t's row to its places; `parts` CTAs share a row.
+// Token t's row to its places; `parts` CTAs share a row, `fill` those that fill up an expert's.
 template <int kBytes>
-__global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherRowsArgs a, int parts, int fill_ctas) {
+__global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherRowsArgs a, int parts, int fill) {
   using T = typename Piece<kBytes>::T;
   __shared__ int row_of[kMaxTopk];
   pdl_wait();
   const long long cta = blockIdx.x;
   if (cta >= static_cast<long long>(a.M) * parts) {
-    zero_filling<kBytes>(a.slots, min(a.offsets[a.E], a.capacity), static_cast<uint8_t*>(a.out), a.row_bytes,
-                         static_cast<int>(cta - static_cast<long long>(a.M) * parts), fill_ctas);
+    zero_filling<kBytes>(a.offsets, a.slots, a.capacity, static_cast<uint8_t*>(a.out), a.row_bytes,
+                         static_cast<int>(cta - static_cast<long long>(a.M) * parts), fill);
     return;
   }
   const int t = static_cast<int>(cta / parts), part = static_cast<int>(cta % parts);
@@ -219,28 +227,34 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherRowsArg
   }
 }
 
-// n consecutive values of a row as fp32, and back.
+// n consecutive values of a row as they are in memory, as fp32, and back.
 template <typename T, int n>
 struct Values;
 template <>
 struct Values<float, 1> {
-  static __device__ __forceinline__ void load(const void* p, float (&f)[1]) { f[0] = *static_cast<const float*>(p); }
+  float raw;
+  __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const float*>(p); }
+  __device__ __forceinline__ float operator[](int) const { return raw; }
   static __device__ __forceinline__ void store(void* p, const float (&f)[1]) { *static_cast<float*>(p) = f[0]; }
 };
 template <>
 struct Values<uint16_t, 1> {
-  static __device__ __forceinline__ void load(const void* p, float (&f)[1]) {
-    f[0] = __uint_as_float(static_cast<uint32_t>(*static_cast<const uint16_t*>(p)) << 16);
-  }
+  uint16_t raw;
+  __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const uint16_t*>(p); }
+  __device__ __forceinline__ float operator[](int) const { return __uint_as_float(static_cast<uint32_t>(raw) << 16); }
   static __device__ __forceinline__ void store(void* p, const float (&f)[1]) {
     *static_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(f[0]);
   }
 };
 template <>
 struct Values<float, 8> {
-  static __device__ __forceinline__ void load(const void* p, float (&f)[8]) {
-    const float4 u = static_cast<const float4*>(p)[0], v = static_cast<const float4*>(p)[1];
-    f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w, f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
+  float4 raw[2];
+  __device__ __forceinline__ void load(const void* p) {
+    raw[0] = static_cast<const float4*>(p)[0], raw[1] = static_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    const float4 v = raw[i >> 2];
+    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
   }
   static __device__ __forceinline__ void store(void* p, const float (&f)[8]) {
     static_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -249,11 +263,11 @@ struct Values<float, 8> {
 };
 template <>
 struct Values<uint16_t, 8> {
-  static __device__ __forceinline__ void load(const void* p, float (&f)[8]) {
-    const uint4 u = *static_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  uint4 raw;
+  __device__ __forceinline__ void load(const void* p) { raw = *static_cast<const uint4*>(p); }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = (i >> 1) == 0 ? raw.x : (i >> 1) == 1 ? raw.y : (i >> 1) == 2 ? raw.z : raw.w;
+    return __uint_as_float(i & 1 ? w & 0xFFFF0000u : w << 16);
   }
   static __device__ __forceinline__ void store(void* p, const float (&f)[8]) {
     uint32_t w[4];
@@ -275,11 +289,23 @@ __device__ __forceinline__ const T* at(const void* p, long long row, long long K
   return static_cast<const T*>(p) + row * K + k;
 }
 
-// out[t] = sum_j w y[row of j] (+ add[t]); `parts` CTAs share a row, kOnce rows of y are
-// under way at a time.
+// `f` with the choices j0 .. j0 + C - 1 of a token, in groups of 8, 4, 2 and 1: a group's
+// loads are all under way at once, none behind a condition. (8,192 tokens of 8 choices,
+// 7,168 wide: 152 us; 501 with a condition to each load, behind which the conversion of its
+// values waited before the next load began.)
+template <typename F>
+__device__ __forceinline__ void by_groups(int topk, F&& f) {
+  int j = 0;
+  for (; j + 8 <= topk; j += 8) f(std::integral_constant<int, 8>{}, j);
+  if (topk & 4) f(std::integral_constant<int, 4>{}, j), j += 4;
+  if (topk & 2) f(std::integral_constant<int, 2>{}, j), j += 2;
+  if (topk & 1) f(std::integral_constant<int, 1>{}, j);
+}
+
+// out[t] = sum_j w y[row of j] (+ add[t]); `parts` CTAs share a row. A choice without a row
+// reads row 0 in its place, which counts nothing.
 template <typename Ty, typename To, int n>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs a, int parts) {
-  constexpr int kOnce = 8;
   __shared__ int row_of[kMaxTopk];
   __shared__ float weight_of[kMaxTopk];
   pdl_wait();
@@ -297,21 +323,22 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs 
     float acc[n];
 #pragma unroll
     for (int i = 0; i < n; ++i) acc[i] = 0.f;
-    for (int j0 = 0; j0 < a.topk; j0 += kOnce) {
-      float y[kOnce][n];
+    by_groups(a.topk, [&](auto count, int j0) {
+      constexpr int C = decltype(count)::value;
+      Values<Ty, n> y[C];
 #pragma unroll
-      for (int j = 0; j < kOnce; ++j)
-        if (j0 + j < a.topk && row_of[j0 + j] >= 0) Values<Ty, n>::load(at<Ty>(a.y, row_of[j0 + j], a.K, v * n), y[j]);
+      for (int j = 0; j < C; ++j) y[j].load(at<Ty>(a.y, max(row_of[j0 + j], 0), a.K, v * n));
 #pragma unroll
-      for (int j = 0; j < kOnce; ++j)
-        if (j0 + j < a.topk && row_of[j0 + j] >= 0) {
+      for (int j = 0; j < C; ++j) {
+        const bool has = row_of[j0 + j] >= 0;
+        const float w = weight_of[j0 + j];
 #pragma unroll
-          for (int i = 0; i < n; ++i) acc[i] = fmaf(weight_of[j0 + j], y[j][i], acc[i]);
-        }
-    }
+        for (int i = 0; i < n; ++i) acc[i] = has ? fmaf(w, y[j][i], acc[i]) : acc[i];
+      }
+    });
     if (a.add) {
-      float d[n];
-      Values<To, n>::load(at<To>(a.add, t, a.K, v * n), d);
+      Values<To, n> d;
+      d.load(at<To>(a.add, t, a.K, v * n));
 #pragma unroll
       for (int i = 0; i < n; ++i) acc[i] += d[i];
     }
@@ -320,18 +347,17 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs 
 }
 
 // One CTA to a token: each thread keeps its own part of the topk sums of products, which
-// the CTA joins at the end.
+// the CTA joins at the end. Behind the tokens' CTAs those of the rows that fill up.
 template <typename Tg, typename Ty, int n>
-__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const CombineBackwardArgs a, int fill_ctas) {
-  constexpr int kOnce = 8;
+__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const CombineBackwardArgs a, int fill) {
   __shared__ int row_of[kMaxTopk];
   __shared__ float weight_of[kMaxTopk];
-  __shared__ float part_of[kRowWarps][kOnce];
+  __shared__ float part_of[kRowWarps][kMaxTopk];
   pdl_wait();
   if (blockIdx.x >= static_cast<unsigned>(a.M)) {
     zero_filling<n * sizeof(Ty) >= 16 ? 16 : n * static_cast<int>(sizeof(Ty))>(
-        a.slots, min(a.offsets[a.E], a.capacity), static_cast<uint8_t*>(a.dy), a.K * static_cast<long long>(sizeof(Ty)),
-        blockIdx.x - a.M, fill_ctas);
+        a.offsets, a.slots, a.capacity, static_cast<uint8_t*>(a.dy), a.K * static_cast<long long>(sizeof(Ty)),
+        blockIdx.x - a.M, fill);
     return;
   }
   const int t = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -342,40 +368,39 @@ __global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const Com
     weight_of[threadIdx.x] = a.weights[i];
   }
   __syncthreads();
-  for (int j0 = 0; j0 < a.topk; j0 += kOnce) {
-    float dot[kOnce] = {};
+  by_groups(a.topk, [&](auto count, int j0) {
+    constexpr int C = decltype(count)::value;
+    float dot[C] = {};
     for (int v = threadIdx.x; v < a.K / n; v += kRowThreads) {
-      float g[n];
-      Values<Tg, n>::load(at<Tg>(a.g, t, a.K, v * n), g);
-      float y[kOnce][n];
+      Values<Tg, n> g;
+      Values<Ty, n> y[C];
+      g.load(at<Tg>(a.g, t, a.K, v * n));
 #pragma unroll
-      for (int j = 0; j < kOnce; ++j)
-        if (j0 + j < a.topk && row_of[j0 + j] >= 0) Values<Ty, n>::load(at<Ty>(a.y, row_of[j0 + j], a.K, v * n), y[j]);
+      for (int j = 0; j < C; ++j) y[j].load(at<Ty>(a.y, max(row_of[j0 + j], 0), a.K, v * n));
 #pragma unroll
-      for (int j = 0; j < kOnce; ++j)
-        if (j0 + j < a.topk && row_of[j0 + j] >= 0) {
-          float d[n];
+      for (int j = 0; j < C; ++j) {
+        if (row_of[j0 + j] < 0) continue;
+        float d[n];
 #pragma unroll
-          for (int i = 0; i < n; ++i) {
-            dot[j] = fmaf(g[i], y[j][i], dot[j]);
-            d[i] = weight_of[j0 + j] * g[i];
-          }
-          Values<Ty, n>::store(at<Ty>(a.dy, row_of[j0 + j], a.K, v * n), d);
+        for (int i = 0; i < n; ++i) {
+          dot[j] = fmaf(g[i], y[j][i], dot[j]);
+          d[i] = weight_of[j0 + j] * g[i];
         }
+        Values<Ty, n>::store(at<Ty>(a.dy, row_of[j0 + j], a.K, v * n), d);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kOnce; ++j) {
+    for (int j = 0; j < C; ++j) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-      if (lane == 0) part_of[w][j] = dot[j];
+      if (lane == 0) part_of[w][j0 + j] = dot[j];
     }
-    __syncthreads();
-    if (threadIdx.x < kOnce && j0 + threadIdx.x < a.topk) {
-      float sum = 0.f;
-      for (int i = 0; i < kRowWarps; ++i) sum += part_of[i][threadIdx.x];
-      a.dweights[static_cast<long long>(t) * a.topk + j0 + threadIdx.x] = sum;
-    }
-    __syncthreads();
+  });
+  __syncthreads();
+  if (threadIdx.x < a.topk) {
+    float sum = 0.f;
+    for (int i = 0; i < kRowWarps; ++i) sum += part_of[i][threadIdx.x];
+    a.dweights[static_cast<long long>(t) * a.topk + threadIdx.x] = sum;
   }
 }
 
@@ -407,11 +432,11 @@ cudaError_t launch_sort(const SortArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_gather(const GatherRowsArgs& a, int num_sms, cudaStream_t stream) {
-  const int fill = a.block > 1 ? 2 * num_sms : 0;
+  const int fill = fill_parts(a.block);
   auto go = [&](auto bytes) {
     constexpr int n = decltype(bytes)::value;
     const int parts = row_parts(a.M, static_cast<int>(a.row_bytes / n), num_sms);
-    return launch_k(gather_kernel<n>, dim3(static_cast<unsigned>(static_cast<long long>(a.M) * parts + fill)), dim3(kRowThreads), 0,
+    return launch_k(gather_kernel<n>, dim3(static_cast<unsigned>(static_cast<long long>(a.M) * parts + a.E * fill)), dim3(kRowThreads), 0,
                     stream, true, a, parts, fill);
   };
   const uintptr_t all = static_cast<uintptr_t>(a.row_bytes) | static_cast<uintptr_t>(a.stride_bytes) |
@@ -422,7 +447,9 @@ cudaError_t launch_gather(const GatherRowsArgs& a, int num_sms, cudaStream_t str
   return go(std::integral_constant<int, 1>{});
 }
 
-cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_combine(const CombineArgs& args, int num_sms, cudaStream_t stream) {
+  CombineArgs a = args;
+  if (a.rows == 0) a.y = a.out, a.y_type = a.out_type;  // (no row counts; what is read in its place is out's)
   const bool wide = a.K % 8 == 0 && aligned(a.y, 16) && aligned(a.add, 16) && aligned(a.out, 16);
   auto go = [&](auto ty, auto to) {
     using Ty = decltype(ty);
@@ -439,12 +466,12 @@ cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t strea
 
 cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, cudaStream_t stream) {
   const bool wide = a.K % 8 == 0 && aligned(a.y, 16) && aligned(a.g, 16) && aligned(a.dy, 16);
-  const int fill = a.block > 1 ? 2 * num_sms : 0;
+  const int fill = fill_parts(a.block);
   auto go = [&](auto tg, auto ty) {
     using Tg = decltype(tg);
     using Ty = decltype(ty);
     auto with = [&](auto kernel) {
-      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) + fill), dim3(kRowThreads), 0, stream, true, a, fill);
+      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) + a.E * fill), dim3(kRowThreads), 0, stream, true, a, fill);
     };
     return wide ? with(combine_backward_kernel<Tg, Ty, 8>) : with(combine_backward_kernel<Tg, Ty, 1>);
   };
