@@ -20,7 +20,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libmoe_w4a16.so")
 SOURCES = ["pack.cu", "align.cu", "route.cu", "gemm.cu", "gemv.cu", "api.cu", "noalloc.cu",
            "route_scored.cu", "fp8_quant.cu", "fp8_matmul.cu", "fp8_many.cu", "ops_api.cu",
-           "dispatch.cu", "route_backward.cu", "lora.cu", "dispatch_api.cu"]
+           "dispatch.cu", "route_backward.cu", "lora.cu", "lora_many.cu", "dispatch_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I", INCLUDE, "-I", CSRC]

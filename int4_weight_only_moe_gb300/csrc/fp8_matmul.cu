@@ -666,6 +666,11 @@ bool fp8_set_option(int option, int value) {
   return true;
 }
 
+void fp8_wait_settings(uint32_t* kcycles, int* test_never_wait) {
+  *kcycles = wait_limit_kcycles(static_cast<unsigned long long>(g_wait_us.load(std::memory_order_relaxed)));
+  *test_never_wait = g_test_never_wait.load(std::memory_order_relaxed);
+}
+
 int32_t* fp8_status_word() {
   // (one context per device in a process)
   static PerDevice<int32_t*> known;

@@ -134,8 +134,10 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
 // pieces (else it is transposed and written value by value).
 bool fp8_whole_pieces(const Fp8MatmulArgs& a);
 cudaError_t launch_fp8_many(const Fp8MatmulArgs& a, bool swiglu, int32_t* status, int num_sms, cudaStream_t stream);
-// Device address of the products' status word, null on failure.
+// Device address of the products' status word, null on failure; the settings of their waits
+// (the low-rank adapters' kernel shares both).
 int32_t* fp8_status_word();
+void fp8_wait_settings(uint32_t* kcycles, int* test_never_wait);
 
 // Tensor map of row-major bytes [rows, cols], rows `stride` bytes apart, read in boxes
 // of 128 columns x box_rows rows laid out as 128-byte swizzled rows. False when the

@@ -3,26 +3,29 @@
 //   out[m] = add[m] + scale[l] b[l] (a[l] x[m]),  l = index[m]
 //
 // and out[m] = add[m] for a row without an adapter.
+//
+// Few rows (a decode step): one launch, in which a cluster of eight CTAs takes up to 16 rows
+// of one adapter. Each CTA sums an eighth of a[l] x's products, hands its part to all
+// eight, and computes an eighth of the outputs; nothing goes through memory in between.
+// The rows of an adapter are found by each cluster itself: row m's counts the rows in front
+// of m that have the same adapter, and goes on where that is a multiple of 16.
+// What bounds it is latency (index, then x and a, then the exchange, then b and the
+// addends, which are asked into L2 ahead) and from about 32 adapters on the reading of a and
+// b. The sums run on mma.sync: 16 rows fill its tile, and 2 r (K + N) operations a row are
+// far below what it can do.
+//
+// The first product's sums stay 32 bits: they enter the second product as two bf16 parts
+// (of 16 bits together; three, of 24, for an fp32 output), so that what is lost stays below
+// the rounding of the output. All sums have a fixed order: the same bits in every run.
 #include <cuda_bf16.h>
 
-#include "ops.cuh"
+#include "fp8_tma.cuh"
+#include "lora.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
-__device__ __forceinline__ float addend(const LoraArgs& a, long long at) {
-  if (!a.add) return 0.f;
-  return a.add_type == kTypeF32 ? static_cast<const float*>(a.add)[at] : bf16_value(static_cast<const uint16_t*>(a.add)[at]);
-}
-__device__ __forceinline__ void put(const LoraArgs& a, long long at, float v) {
-  if (a.out_type == kTypeF32)
-    static_cast<float*>(a.out)[at] = v;
-  else
-    static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-}
 
 // Any shape and alignment: one CTA to a row, everything in fp32 on the CUDA cores.
 __global__ void __launch_bounds__(kThreads) lora_plain_kernel(const LoraArgs a) {
@@ -55,15 +58,235 @@ __global__ void __launch_bounds__(kThreads) lora_plain_kernel(const LoraArgs a) 
   }
 }
 
-}  // namespace
+// -------------------------------------------------------------------------------- few rows
 
-size_t lora_workspace_bytes(int M, int r, int L) {
-  (void)M, (void)r, (void)L;
-  return 0;
+constexpr int kCluster = 8, kWarps = kThreads / 32;
+constexpr int kGroup = 16;      // rows of a cluster
+constexpr int kFewRows = 512;   // rows of a call
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
+// Shared memory of the few-row kernel for ranks up to 8 * kTiles: the warps' sums, the
+// CTAs' sums as they arrive from the cluster, and the parts of the sum, rows padded by 8
+// values against bank conflicts.
+template <int kTiles>
+struct Few {
+  static constexpr int kRank = 8 * kTiles;               // a multiple of 16
+  static constexpr int kSums = kGroup * kRank;           // fp32
+  static constexpr int kRow = kRank + 8;                 // bf16 of a row of parts
+  static constexpr int kSmem = (kWarps + kCluster) * kSums * 4 + 3 * kGroup * kRow * 2;
+};
+
+// Sums of 16 rows and up to 8 kTiles ranks. The order of the reduction's elements is free
+// as long as both operands share it: a lane takes 16 consecutive bytes of a row, of which
+// the words 0, 1 make one MMA's elements (2t, 2t + 1, 2t + 8, 2t + 9) and 2, 3 the next's.
+template <int kTiles>
+__global__ void __launch_bounds__(kThreads) lora_few_kernel(const LoraArgs a, int parts) {
+  using F = Few<kTiles>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* warp_sums = reinterpret_cast<float*>(smem);                                       // [warps][16][kRank]
+  float* arrived = warp_sums + kWarps * F::kSums;                                          // [CTAs][16][kRank]
+  uint16_t* part_of = reinterpret_cast<uint16_t*>(arrived + kCluster * F::kSums);          // [parts][16][kRow]
+  __shared__ int index_of[kFewRows];
+  __shared__ int row_of[kGroup];
+  __shared__ int rows_in;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank());
+  const int m = blockIdx.x / kCluster;
+  pdl_wait();
+  for (int i = tid; i < a.M; i += kThreads) index_of[i] = a.index[i];
+  __syncthreads();
+  const int l = index_of[m];
+  // columns of the output that are this CTA's, in blocks of 32
+  const int blocks = (a.N + 31) / 32, per = (blocks + kCluster - 1) / kCluster;
+  const int block0 = rank * per, block1 = min(blocks, block0 + per);
+  if (static_cast<uint32_t>(l) >= static_cast<uint32_t>(a.L)) {  // (the same in the whole cluster, as all that returns here)
+    if (a.add != a.out)
+      for (int n = block0 * 32 + tid; n < min(a.N, block1 * 32); n += kThreads) {
+        const long long at = static_cast<long long>(m) * a.N + n;
+        put(a, at, addend(a, at));
+      }
+    return;
+  }
+  if (w == 0) {
+    int before = 0;
+    for (int i0 = 0; i0 < m; i0 += 32) before += __popc(__ballot_sync(0xffffffffu, i0 + lane < m && index_of[i0 + lane] == l));
+    int found = 0;
+    if (before % kGroup == 0)
+      for (int i0 = m; i0 < a.M && found < kGroup; i0 += 32) {
+        const unsigned same = __ballot_sync(0xffffffffu, i0 + lane < a.M && index_of[i0 + lane] == l);
+        const int at = found + __popc(same & ((1u << lane) - 1u));
+        if ((same >> lane & 1) && at < kGroup) row_of[at] = i0 + lane;
+        found += __popc(same);
+      }
+    if (lane == 0) rows_in = min(found, kGroup);
+  }
+  __syncthreads();
+  const int rows = rows_in;
+  if (rows == 0) return;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (every CTA runs before another writes to it)
+
+  const int g = lane >> 2, t = lane & 3;
+  const uint16_t* A = a.a + static_cast<long long>(l) * a.r * a.K;
+  const uint16_t* B = a.b + static_cast<long long>(l) * a.N * a.r;
+  // what comes after the exchange is asked into L2: lines of b, lines of the addends
+  {
+    const int n0 = block0 * 32, n1 = min(a.N, block1 * 32);
+    const char* from = reinterpret_cast<const char*>(B + static_cast<long long>(n0) * a.r);
+    for (int i = tid * 128; i < (n1 - n0) * a.r * 2; i += kThreads * 128) prefetch_l2(from + i);
+    if (a.add && n1 > n0) {
+      const int item = a.add_type == kTypeF32 ? 4 : 2, lines = ((n1 - n0) * item + 127) / 128;
+      for (int i = tid; i < rows * lines; i += kThreads)
+        prefetch_l2(static_cast<const char*>(a.add) + (static_cast<long long>(row_of[i / lines]) * a.N + n0) * item + i % lines * 128);
+    }
+  }
+  // ---- a[l] x: this CTA's part of the K columns in units of 32, dealt out to its warps
+  float sum[kTiles][4] = {};
+  {
+    const int units = (a.K + 31) / 32, each = (units + kCluster - 1) / kCluster;
+    const int u0 = rank * each, u1 = min(units, u0 + each);
+    const uint16_t* x0 = a.x + static_cast<long long>(row_of[min(g, rows - 1)]) * a.ldx + 8 * t;
+    const uint16_t* x1 = a.x + static_cast<long long>(row_of[min(g + 8, rows - 1)]) * a.ldx + 8 * t;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    constexpr int kOnce = kTiles <= 4 ? 4 : 2;  // units under way
+    for (int u = u0 + w; u < u1; u += kOnce * kWarps) {
+      uint4 xa[kOnce], xb[kOnce], y[kOnce][kTiles];
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i) {
+        const int k = (u + i * kWarps) * 32;
+        const bool in = u + i * kWarps < u1 && k + 8 * t < a.K;
+        xa[i] = in && g < rows ? *reinterpret_cast<const uint4*>(x0 + k) : none;
+        xb[i] = in && g + 8 < rows ? *reinterpret_cast<const uint4*>(x1 + k) : none;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j)
+          y[i][j] = in && 8 * j + g < a.r ? *reinterpret_cast<const uint4*>(A + static_cast<long long>(8 * j + g) * a.K + k + 8 * t) : none;
+      }
+#pragma unroll
+      for (int i = 0; i < kOnce; ++i)
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          mma_bf16(sum[j], xa[i].x, xb[i].x, xa[i].y, xb[i].y, y[i][j].x, y[i][j].y);
+          mma_bf16(sum[j], xa[i].z, xb[i].z, xa[i].w, xb[i].w, y[i][j].z, y[i][j].w);
+        }
+    }
+  }
+  {
+    float* mine = warp_sums + w * F::kSums;
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+      *reinterpret_cast<float2*>(mine + g * F::kRank + 8 * j + 2 * t) = make_float2(sum[j][0], sum[j][1]);
+      *reinterpret_cast<float2*>(mine + (g + 8) * F::kRank + 8 * j + 2 * t) = make_float2(sum[j][2], sum[j][3]);
+    }
+  }
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  for (int i = tid; i < F::kSums / 4; i += kThreads) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) {
+      const float4 p = reinterpret_cast<const float4*>(warp_sums + v * F::kSums)[i];
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    const uint32_t at = smem_u32(arrived + rank * F::kSums) + 16 * i;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) st_cluster_v4(map_rank(at, c), s);
+  }
+  cluster_sync();  // (the only one: afterwards a CTA reads its own shared memory alone)
+  const float scale = a.scale ? a.scale[l] : 1.f;
+  for (int i = tid; i < F::kSums; i += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) s += arrived[c * F::kSums + i];
+    s *= scale;
+    const int at = i / F::kRank * F::kRow + i % F::kRank;
+    for (int p = 0; p < parts; ++p) {
+      const uint16_t h = bf16_part(s);
+      part_of[p * kGroup * F::kRow + at] = h;
+      s = isfinite(s) ? s - bf16_value(h) : 0.f;
+    }
+  }
+  __syncthreads();
+  // ---- b[l] of that: 16 rows x 32 columns at a time, a lane's outputs 8 consecutive columns
+  for (int bl = block0 + w; bl < block1; bl += kWarps) {
+    const int n0 = bl * 32, n = n0 + 8 * t;
+    const bool live = n < a.N;
+    float d0[8], d1[8];  // addends of rows g and g + 8
+    const long long at0 = static_cast<long long>(row_of[min(g, rows - 1)]) * a.N + n;
+    const long long at1 = static_cast<long long>(row_of[min(g + 8, rows - 1)]) * a.N + n;
+    load8(a, live ? at0 : 0, d0);
+    load8(a, live ? at1 : 0, d1);
+    float acc[4][4] = {};
+    uint2 y[4][kTiles / 2];
+#pragma unroll
+    for (int s = 0; s < kTiles / 2; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = n0 + 8 * (g >> 1) + 2 * j + (g & 1), i = 16 * s + 4 * t;
+        y[j][s] = row < a.N && i < a.r ? *reinterpret_cast<const uint2*>(B + static_cast<long long>(row) * a.r + i) : make_uint2(0, 0);
+      }
+    for (int p = parts - 1; p >= 0; --p) {  // (the small parts first)
+      const uint16_t* v = part_of + p * kGroup * F::kRow;
+#pragma unroll
+      for (int s = 0; s < kTiles / 2; ++s) {
+        const uint2 v0 = *reinterpret_cast<const uint2*>(v + g * F::kRow + 16 * s + 4 * t);
+        const uint2 v1 = *reinterpret_cast<const uint2*>(v + (g + 8) * F::kRow + 16 * s + 4 * t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_bf16(acc[j], v0.x, v1.x, v0.y, v1.y, y[j][s].x, y[j][s].y);
+      }
+    }
+    if (!live) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d0[2 * j] += acc[j][0], d0[2 * j + 1] += acc[j][1];
+      d1[2 * j] += acc[j][2], d1[2 * j + 1] += acc[j][3];
+    }
+    if (g < rows) store8(a, at0, d0);
+    if (g + 8 < rows) store8(a, at1, d1);
+  }
+}
+
+template <int kTiles>
+cudaError_t launch_few(const LoraArgs& a, cudaStream_t stream) {
+  static PerDevice<int> ready;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* entry = ready.of(dev);
+  if (!entry || !entry->load()) {
+    e = cudaFuncSetAttribute(lora_few_kernel<kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<kTiles>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (entry) entry->store(1);
+  }
+  return launch_cluster(lora_few_kernel<kTiles>, dim3(static_cast<unsigned>(a.M) * kCluster), dim3(kThreads), Few<kTiles>::kSmem,
+                        stream, kCluster, a, a.out_type == kTypeF32 ? 3 : 2);
+}
+
+bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
+
+}  // namespace
+
+size_t lora_workspace_bytes(int M, int L) { return M > kFewRows ? lora_many_workspace(M, L) : 0; }
+
 cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
+  // 16-byte pieces of every row
+  const bool whole = a.K % 8 == 0 && a.N % 8 == 0 && a.r % 8 == 0 && (a.M == 1 || a.ldx % 8 == 0) && aligned(a.x, 16) &&
+                     aligned(a.a, 16) && aligned(a.b, 16) && aligned(a.add, 16) && aligned(a.out, 16);
+  if (whole && a.M > kFewRows && static_cast<long long>(a.L) * a.N < (1LL << 31) - kFewRows) return launch_lora_many(a, num_sms, stream);
+  if (whole && a.M <= kFewRows) {
+    if (a.r <= 16) return launch_few<2>(a, stream);
+    if (a.r <= 32) return launch_few<4>(a, stream);
+    if (a.r <= 64) return launch_few<8>(a, stream);
+    return launch_few<16>(a, stream);
+  }
   return launch_k(lora_plain_kernel, dim3(static_cast<unsigned>(a.M)), dim3(kThreads), 0, stream, true, a);
 }
 

@@ -170,8 +170,12 @@ struct LoraArgs {
   void* workspace;  // lora_workspace_bytes()
 };
 constexpr int kMaxRank = 128;
-size_t lora_workspace_bytes(int M, int r, int L);
+size_t lora_workspace_bytes(int M, int L);
 cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream);
+
+// Its kernel for many rows (lora_many.cu): rows of whole, aligned 16-byte pieces.
+size_t lora_many_workspace(int M, int L);
+cudaError_t launch_lora_many(const LoraArgs& a, int num_sms, cudaStream_t stream);
 
 // SM count of the current device, and a stream-ordered memory pool of the library's own on
 // it (ops_api.cu).

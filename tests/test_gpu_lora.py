@@ -209,3 +209,20 @@ def test_no_rows_and_refusals():
     with pytest.raises(MoeW4A16Error):
         lora.apply(x, torch.zeros(3, 136, 64, device="cuda", dtype=BF16),
                    torch.zeros(3, 40, 136, device="cuda", dtype=BF16), index)
+
+
+def test_a_wait_that_gives_up_is_reported():
+    import int4_weight_only_moe_gb300 as pkg
+    x, a, b, index = problem(1000, 1024, 640, 32, 3)
+    add = normal(1000, 640, seed=1)
+    want = lora.apply(x, a, b, dev(index), add=add)
+    assert fp8.status() == 0
+    pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, 1000)
+    pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_TEST_WAIT_NEVER_COMPLETES, 1)
+    try:
+        lora.apply(x, a, b, dev(index), add=add)
+        assert fp8.status() == pkg.STATUS_TIMEOUT
+    finally:
+        pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, 0)
+        pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_TEST_WAIT_NEVER_COMPLETES, 0)
+    assert torch.equal(lora.apply(x, a, b, dev(index), add=add), want) and fp8.status() == 0
