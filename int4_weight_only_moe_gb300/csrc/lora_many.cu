@@ -2,20 +2,24 @@
 //
 // The rows are sorted by adapter (the order of dispatch.cu, filled up to tiles of 128 rows;
 // rows without an adapter are the last bucket's). A cluster of CTAs takes a tile. Each CTA
-//   1. sums its share of a[l] x's columns: tcgen05 MMAs of 128 rows x r, whose x rows the
-//      copy engine gathers from wherever they lie;
+//   1. sums its share of a[l] x's columns: tcgen05 MMAs of 128 rows x r, whose x rows 16
+//      warps copy from wherever they lie, a stage's copies under way beside the next ones'
+//      (the copy engine's gathers of four rows take 18 cycles a row of 128 bytes here, five
+//      times as long);
 //   2. joins the sums with the cluster's other CTAs: each sends its sums of a row to the
 //      row's CTA, which adds them in the order of the ranks, scales them, splits them into
 //      bf16 parts (two, three for an fp32 output: 16 and 24 bits of the sum) and hands them
 //      to all CTAs, straight into the second product's operand;
 //   3. computes its share of the N columns: MMAs of 128 rows x 128 columns over the parts,
 //      one after another against the same tile of b[l], two accumulators in turn, taken out
-//      of tensor memory by eight warps that add the addends and write the output.
+//      of tensor memory by 16 warps that add the addends, which they have loaded one tile
+//      ahead, and write the output.
 // Nothing but x, a, b, the addends and the output goes through memory, and each once (a and
 // b once for each tile, from L2). The operations are few, r of them for a byte at most: what
 // bounds it is memory.
 //
-// Warps: 0..7 joining and output, 8 copies, 9 the MMAs. All sums have a fixed order.
+// Warps: 0..15 rows of x, joining and output, 16 the copies of a and b, 17 the MMAs. All
+// sums have a fixed order.
 #include <algorithm>
 
 #include "fp8_tma.cuh"
@@ -27,7 +31,8 @@ namespace {
 constexpr int kTile = 128;         // rows of a tile, columns of an accumulator
 constexpr int kChunk = 64;         // columns of x to a stage: 128 bytes
 constexpr int kBox = kTile * 128;  // bytes of 128 rows of 128 bytes
-constexpr int kEpiWarps = 8, kWarpCopy = 8, kWarpMma = 9, kThreads = 10 * 32;
+constexpr int kEpiWarps = 16, kEpiThreads = kEpiWarps * 32, kWarpCopy = 16, kWarpMma = 17, kThreads = 18 * 32;
+constexpr int kCols = kTile * 4 / kEpiWarps;  // of an accumulator, to a warp
 constexpr int kMaxStages = 6;
 constexpr int kHead = 2048;        // barriers, the tile's rows
 constexpr int kSmemMost = 227 * 1024;
@@ -56,13 +61,20 @@ __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, ui
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// Four rows of a tensor map whose box is one row: 128 bytes from byte x on.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int4 rows, uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(bar), "l"(policy)
-      : "memory");
+// 16 bytes of global memory to shared memory, zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// All but the last `left` groups of this thread's copies have landed.
+__device__ __forceinline__ void copies_left(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+  }
 }
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
@@ -75,10 +87,88 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
+struct Words8 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Words8 ld32(const void* p) {
+  Words8 v;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// kCols consecutive addends of a row as they are in memory: pieces of 32 bytes where rows
+// and addresses are multiples of that, else of 16. Those from column `left` on are not read.
+template <int kAdd>
+struct Addends {
+  static constexpr int kItem = kAdd == kTypeF32 ? 4 : 2, kWords = kCols * kItem / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const LoraArgs& a, long long at, int left, bool pieces32) {
+    const char* p = static_cast<const char*>(a.add) + at * kItem;
+    if (pieces32) {
+#pragma unroll
+      for (int i = 0; i < kWords / 8; ++i)
+        if (i * 32 / kItem < left) {
+          const Words8 v = ld32(p + 32 * i);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[8 * i + j] = v.w[j];
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i)
+        if (i * 16 / kItem < left) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * i);
+          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    return __uint_as_float(kItem == 4 ? w[i] : i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
+template <>
+struct Addends<-1> {
+  __device__ __forceinline__ void load(const LoraArgs&, long long, int, bool) {}
+  __device__ __forceinline__ float operator[](int) const { return 0.f; }
+};
+template <int kOut>
+__device__ __forceinline__ void store_cols(const LoraArgs& a, long long at, int left, bool pieces32, const float (&y)[kCols]) {
+  constexpr int kItem = kOut == kTypeF32 ? 4 : 2, kWords = kCols * kItem / 4;
+  uint32_t w[kWords];
+  if constexpr (kOut == kTypeF32) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) w[i] = __float_as_uint(y[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCols / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  char* p = static_cast<char*>(a.out) + at * kItem;
+  if (pieces32) {
+#pragma unroll
+    for (int i = 0; i < kWords / 8; ++i)
+      if (i * 32 / kItem < left) st32(p + 32 * i, w + 8 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+      if (i * 16 / kItem < left) *reinterpret_cast<uint4*>(p + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+}
+
+// kAdd: the addends' type, -1 without; kOut: the output's.
+template <int kAdd, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
-    lora_many_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap amap,
-                     const __grid_constant__ CUtensorMap bmap, const __grid_constant__ LoraArgs a, const Order order,
-                     const ManyPlan plan, uint32_t limit, int test_never_wait, int32_t* status) {
+    lora_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ LoraArgs a, const Order order,
+                     const ManyPlan plan, bool pieces32, uint32_t limit, int test_never_wait, int32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -99,25 +189,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = plan.ctas, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = blockIdx.x / C;
+  int* bucket = reinterpret_cast<int*>(gbase + 264);
+  if (threadIdx.x == 0) *bucket = -1;
+  __syncthreads();
   pdl_wait();
-  if (tile >= order.offsets[a.L + 1] / kTile) return;  // (the whole cluster)
-  int lo = 0, hi = a.L;  // the tile's bucket: the last that begins at or in front of it and is not empty
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (order.offsets[mid] <= tile * kTile)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  const int l = lo;
+  const int32_t* slots = order.slots + static_cast<long long>(tile) * kTile;
+  const int my_row = threadIdx.x < kTile ? slots[threadIdx.x] : -1;
+  for (int e = threadIdx.x; e <= a.L; e += kThreads)  // the tile's bucket, if it has one
+    if (order.offsets[e] <= tile * kTile && tile * kTile < order.offsets[e + 1]) *bucket = e;
+  if (threadIdx.x < kTile) row_of[threadIdx.x] = my_row;
+  __syncthreads();
+  const int l = *bucket;
+  if (l < 0) return;  // (the whole cluster)
   const int nt = (a.N + kTile - 1) / kTile, nper = (nt + C - 1) / C;
   const int nt0 = min(nt, rank * nper), nt1 = min(nt, nt0 + nper);
-  const int32_t* slots = order.slots + static_cast<long long>(tile) * kTile;
   if (l == a.L) {  // rows without an adapter
     if (a.add == a.out) return;
     const int n0 = nt0 * kTile, pieces = (min(a.N, nt1 * kTile) - n0) / 8;
     for (int i = warp; i < kTile; i += kThreads / 32) {
-      const int m = slots[i];
+      const int m = row_of[i];
       if (m < 0) break;
       for (int v = lane; v < pieces; v += 32) {
         const long long at = static_cast<long long>(m) * a.N + n0 + 8 * v;
@@ -128,12 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  if (threadIdx.x < kTile) row_of[threadIdx.x] = slots[threadIdx.x];
   if (threadIdx.x == 0) {
-    tma_prefetch_map(&xmap);
     tma_prefetch_map(&amap);
     tma_prefetch_map(&bmap);
-    for (int i = 0; i < S; ++i) mbar_init(full(i), 1), mbar_init(empty(i), 1);
+    for (int i = 0; i < S; ++i) mbar_init(full(i), 1 + kEpiWarps), mbar_init(empty(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), kEpiWarps);
     mbar_init(summed, 1);
     mbar_init(drain, 1);
@@ -158,39 +246,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ahead = min(nn, S);            // column tiles copied before the join
   const int wide = plan.rank16 > kChunk ? 2 : 1;  // boxes of a row of b
   auto slot_of = [&](int i) { return ring + (i % S) * plan.stage_bytes; };
-  // what the copying lanes issue as item i: a stage of x and a, or a tile of b
+  // what the copying lane issues as item i: a stage of a, or a tile of b (and then the warps'
+  // arrivals too, which copy no x into it)
   bool copying = true;
   int issued = 0;
-  const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
-  auto copy = [&](int i, int4 rows) {
-    if (!__all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit)))
-      return false;
+  const uint64_t keep = l2_policy_evict_last();
+  auto copy = [&](int i) {
+    if (!mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit)) return false;
     if (i < kn) {
-      if (lane == 0) mbar_arrive_expect_tx(full(i % S), kBox + plan.rank16 * 128);
-      __syncwarp();
-      tma_gather4(slot_of(i) + lane * 512, &xmap, (c0 + i) * 128, rows, full(i % S), once);
-      if (lane == 0) tma_load_2d(slot_of(i) + kBox, &amap, (c0 + i) * 128, l * a.r, full(i % S), keep);
-    } else if (lane == 0) {
+      mbar_arrive_expect_tx(full(i % S), plan.rank16 * 128);
+      tma_load_2d(slot_of(i) + kBox, &amap, (c0 + i) * 128, l * a.r, full(i % S), keep);
+    } else {
       const int n0 = (nt0 + i - kn) * kTile;
+      mbar_arrive_cnt(full(i % S), kEpiWarps);
       mbar_arrive_expect_tx(full(i % S), wide * kBox);
       for (int b = 0; b < wide; ++b) tma_load_2d(slot_of(i) + b * kBox, &bmap, b * 128, l * a.N + n0, full(i % S), keep);
     }
-    __syncwarp();
     return true;
   };
 
   // ---- 1. this CTA's columns of a[l] x
   bool ok = true;
   if (warp == kWarpCopy) {
-    int4 rows;
-    {
-      // (rows behind the last read the first: their sums are not used)
-      const int first = row_of[0], q = 4 * lane;
-      rows = make_int4(row_of[q] < 0 ? first : row_of[q], row_of[q + 1] < 0 ? first : row_of[q + 1],
-                       row_of[q + 2] < 0 ? first : row_of[q + 2], row_of[q + 3] < 0 ? first : row_of[q + 3]);
-    }
-    for (; issued < kn + ahead && copying; ++issued) copying = copy(issued, rows);
-    if (!copying) --issued;
+    if (lane == 0)
+      for (; issued < kn + ahead; ++issued)
+        if (!(copying = copy(issued))) break;
+    __syncwarp();
   } else if (warp == kWarpMma) {
     const uint32_t idesc = idesc_bf16_f32(kTile, plan.rank16);
     const bool leader = elect_one();
@@ -209,12 +290,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader) tc_commit(summed);
     __syncwarp();
   } else {
-    // the first column tiles' addends are asked into L2 meanwhile
-    const int item = a.add_type == kTypeF32 ? 4 : 2;
-    const int n0 = nt0 * kTile, lines = a.add ? (min(a.N, (nt0 + min(nn, 2)) * kTile) - n0) * item / 128 : 0;
-    for (int i = threadIdx.x; i < kTile * lines; i += kEpiWarps * 32) {
-      const int m = row_of[i / lines];
-      if (m >= 0) prefetch_l2(static_cast<const char*>(a.add) + (static_cast<long long>(m) * a.N + n0) * item + i % lines * 128);
+    // a thread copies the same 16 bytes of each stage's 128 of two rows; the rows' 16-byte
+    // pieces are swizzled as the MMA reads them
+    {
+      const int piece = threadIdx.x & 7, row = threadIdx.x >> 3;
+      const int m0 = row_of[row], m1 = row_of[row + kTile / 2];
+      const uint16_t* x0 = a.x + max(m0, 0) * a.ldx + 8 * piece;
+      const uint16_t* x1 = a.x + max(m1, 0) * a.ldx + 8 * piece;
+      const uint32_t at = row * 128 + ((piece ^ (row & 7)) << 4);
+      for (int i = 0; i < kn + S - 1; ++i) {
+        if (i < kn) {
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
+          if (!ok) break;
+          const int k = (c0 + i) * kChunk;
+          const bool in = k + 8 * piece < a.K;
+          copy16(slot_of(i) + at, in ? x0 + k : x0, in && m0 >= 0 ? 16 : 0);
+          copy16(slot_of(i) + at + kBox / 2, in ? x1 + k : x1, in && m1 >= 0 ? 16 : 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (i >= S - 1) {
+          copies_left(S - 1);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full((i - S + 1) % S));
+        }
+      }
+      copies_left(0);
     }
     if (test_never_wait) ok = __all_sync(0xffffffffu, mbar_wait(never, 0, abort_flag, status, kStatusTimeout, limit));
     ok = ok && __all_sync(0xffffffffu, mbar_wait(summed, 0, abort_flag, status, kStatusTimeout, limit));
@@ -222,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---- 2. to the row's CTA
     const int row = (warp & 3) * 32 + lane, share = kTile / C;
     const uint32_t to = map_rank(sums_at + (rank * (plan.rank16 / 4) * share + row % share) * 16, row / share);
-    for (int c = warp >> 2; c < plan.rank16 / 16; c += 2) {
+    for (int c = warp >> 2; c < plan.rank16 / 16; c += kEpiWarps / 4) {
       uint32_t v[16] = {};
       if (ok && kn > 0) {
         tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 16 * c, v);
@@ -271,16 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- 3. this CTA's columns of the output
   if (warp == kWarpCopy) {
-    for (; issued < kn + nn && copying; ++issued) {
-      copying = copy(issued, make_int4(0, 0, 0, 0));
-      if (!copying) break;
+    if (lane == 0) {
+      for (; issued < kn + nn && copying; ++issued)
+        if (!(copying = copy(issued))) break;
+      // the last copies have landed, and the MMAs' last signals, before shared memory is given up
+      for (int i = max(0, issued - S); i < issued; ++i)
+        if (!mbar_wait(empty(i % S), (i / S) & 1, abort_flag, status, kStatusTimeout, limit)) break;
     }
-    // the last copies have landed, and the MMAs' last signals, before shared memory is given up
-    for (int i = max(0, issued - S); i < issued; ++i) {
-      mbar_drain(full(i % S), (i / S) & 1);
-      if (!__all_sync(0xffffffffu, mbar_wait(empty(i % S), (i / S) & 1, abort_flag, status, kStatusTimeout, limit))) break;
-    }
-    if (*abort_flag) {  // (what nobody waited for gets 2 ms)
+    __syncwarp();
+    if (*abort_flag) {  // (copies and signals that nobody waited for get 2 ms)
       const long long t0 = clock64();
       while (clock64() - t0 < 4000000) {
       }
@@ -316,44 +416,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int half = warp >> 2, m = row_of[(warp & 3) * 32 + lane];
-    const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + half * (kTile / 2);
+    const int col = (warp >> 2) * kCols, m = row_of[(warp & 3) * 32 + lane];
+    const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col;
+    const long long row_at = static_cast<long long>(max(m, 0)) * a.N;
+    Addends<kAdd> next;
+    auto load = [&](int j) {
+      const int n = (nt0 + j) * kTile + col;
+      next.load(a, row_at + n, m >= 0 && j < nn ? a.N - n : 0, pieces32);
+    };
+    load(0);
     for (int j = 0; j < nn; ++j) {
-      const int n0 = (nt0 + j) * kTile + half * (kTile / 2), buf = j & 1;
-      const long long at = static_cast<long long>(max(m, 0)) * a.N + n0;
-      // (the next but one tile's addends)
-      if (a.add && m >= 0 && j + 2 < nn) {
-        const int item = a.add_type == kTypeF32 ? 4 : 2;
-        for (int i = 0; i < kTile / 2 && n0 + 2 * kTile + i < a.N; i += 128 / item)
-          prefetch_l2(static_cast<const char*>(a.add) + (at + 2 * kTile + i) * item);
-      }
+      const int n = (nt0 + j) * kTile + col, buf = j & 1;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(buf), (j >> 1) & 1, abort_flag, status, kStatusTimeout, limit));
       if (!ok) break;
       tc_fence_after();
+      uint32_t v[kCols];
+      tmem_ld32(src + buf * kTile, v);
+      const Addends<kAdd> now = next;
+      load(j + 1);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty(buf));
+      float y[kCols];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float d[4][8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = 32 * c + 8 * i;
-          load8(a, m >= 0 && n0 + n < a.N ? at + n : 0, d[i]);
-        }
-        uint32_t v[32];
-        tmem_ld32(src + buf * kTile + 32 * c, v);
-        tmem_ld_wait();
-        if (c == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tempty(buf));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int n = 32 * c + 8 * i;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) d[i][k] += __uint_as_float(v[8 * i + k]);
-          if (m >= 0 && n0 + n < a.N) store8(a, at + n, d[i]);
-        }
-      }
+      for (int i = 0; i < kCols; ++i) y[i] = __uint_as_float(v[i]) + now[i];
+      if (m >= 0) store_cols<kOut>(a, row_at + n, a.N - n, pieces32, y);
     }
   }
   __syncwarp();
@@ -399,34 +487,50 @@ size_t lora_many_workspace(int M, int L) {
   return align_up(sizeof(int32_t) * (L + 2)) + align_up(sizeof(int32_t) * static_cast<size_t>(order_rows(M, L)));
 }
 
-cudaError_t launch_lora_many(const LoraArgs& a, int num_sms, cudaStream_t stream) {
+namespace {
+template <int kAdd, int kOut>
+cudaError_t launch(const LoraArgs& a, const CUtensorMap& amap, const CUtensorMap& bmap, const Order& order, const ManyPlan& p,
+                   cudaStream_t stream) {
   static PerDevice<int> ready;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::atomic<int>* entry = ready.of(dev);
   if (!entry || !entry->load()) {
-    e = cudaFuncSetAttribute(lora_many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    e = cudaFuncSetAttribute(lora_many_kernel<kAdd, kOut>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     if (e != cudaSuccess) return e;
     if (entry) entry->store(1);
   }
   int32_t* status = fp8_status_word();
   if (!status) return cudaErrorInvalidSymbol;
-  auto* offsets = static_cast<int32_t*>(a.workspace);
-  auto* slots = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + align_up(sizeof(int32_t) * (a.L + 2)));
-  CUtensorMap xmap, amap, bmap;
-  if (!make_bf16_map(&xmap, a.x, a.M, a.K, a.ldx, 1) ||
-      !make_bf16_map(&amap, a.a, static_cast<long long>(a.L) * a.r, a.K, a.K, (a.r + 15) / 16 * 16) ||
-      !make_bf16_map(&bmap, a.b, static_cast<long long>(a.L) * a.N, a.r, a.r, kTile))
-    return cudaErrorInvalidValue;
-  e = launch_sort(SortArgs{a.index, a.M, 0, a.L, 1, kTile, offsets, slots, order_rows(a.M, a.L), nullptr}, stream);
-  if (e != cudaSuccess) return e;
-  const ManyPlan p = plan_many(a, num_sms);
   uint32_t limit;
   int never;
   fp8_wait_settings(&limit, &never);
-  return launch_cluster(lora_many_kernel, dim3(static_cast<unsigned>(p.tiles) * p.ctas), dim3(kThreads), p.smem, stream, p.ctas, xmap,
-                        amap, bmap, a, Order{offsets, slots}, p, limit, never, status);
+  const uintptr_t where = reinterpret_cast<uintptr_t>(a.add) | reinterpret_cast<uintptr_t>(a.out);
+  const bool pieces32 = where % 32 == 0 && a.N % 16 == 0;
+  return launch_cluster(lora_many_kernel<kAdd, kOut>, dim3(static_cast<unsigned>(p.tiles) * p.ctas), dim3(kThreads), p.smem, stream,
+                        p.ctas, amap, bmap, a, order, p, pieces32, limit, never, status);
+}
+}  // namespace
+
+cudaError_t launch_lora_many(const LoraArgs& a, int num_sms, cudaStream_t stream) {
+  auto* offsets = static_cast<int32_t*>(a.workspace);
+  auto* slots = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + align_up(sizeof(int32_t) * (a.L + 2)));
+  CUtensorMap amap, bmap;
+  if (!make_bf16_map(&amap, a.a, static_cast<long long>(a.L) * a.r, a.K, a.K, (a.r + 15) / 16 * 16) ||
+      !make_bf16_map(&bmap, a.b, static_cast<long long>(a.L) * a.N, a.r, a.r, kTile))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = launch_sort(SortArgs{a.index, a.M, 0, a.L, 1, kTile, offsets, slots, order_rows(a.M, a.L), nullptr}, stream);
+  if (e != cudaSuccess) return e;
+  const ManyPlan p = plan_many(a, num_sms);
+  const Order order{offsets, slots};
+  auto go = [&](auto out) {
+    constexpr int kOut = decltype(out)::value;
+    if (!a.add) return launch<-1, kOut>(a, amap, bmap, order, p, stream);
+    return a.add_type == kTypeF32 ? launch<kTypeF32, kOut>(a, amap, bmap, order, p, stream)
+                                  : launch<kTypeBf16, kOut>(a, amap, bmap, order, p, stream);
+  };
+  return a.out_type == kTypeF32 ? go(std::integral_constant<int, kTypeF32>{}) : go(std::integral_constant<int, kTypeBf16>{});
 }
 
 }  // namespace moe
