@@ -13,7 +13,7 @@
 //   3. computes its share of the N columns: MMAs of 128 rows x 128 columns over the parts,
 //      one after another against the same tile of b[l], two accumulators in turn, taken out
 //      of tensor memory by 16 warps that add the addends, which they have loaded one tile
-//      ahead, and write the output.
+//      ahead, and write the output, eight columns to a lane.
 // Nothing but x, a, b, the addends and the output goes through memory, and each once (a and
 // b once for each tile, from L2). The operations are few, r of them for a byte at most: what
 // bounds it is memory.
@@ -33,6 +33,7 @@ constexpr int kChunk = 64;         // columns of x to a stage: 128 bytes
 constexpr int kBox = kTile * 128;  // bytes of 128 rows of 128 bytes
 constexpr int kEpiWarps = 16, kEpiThreads = kEpiWarps * 32, kWarpCopy = 16, kWarpMma = 17, kThreads = 18 * 32;
 constexpr int kCols = kTile * 4 / kEpiWarps;  // of an accumulator, to a warp
+constexpr int kAhead = 4;          // column tiles whose addends are asked into L2 ahead
 constexpr int kMaxStages = 6;
 constexpr int kHead = 2048;        // barriers, the tile's rows
 constexpr int kSmemMost = 227 * 1024;
@@ -65,16 +66,37 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// All but the last `left` groups of this thread's copies have landed.
-__device__ __forceinline__ void copies_left(int left) {
-  switch (left) {
-    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
-    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
-    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-  }
+// Arrive on the barrier when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// 16 rows x 32 columns of fp32 sums: lane 4 g + t gets of row g (v[4 i], v[4 i + 1]) and of row
+// g + 8 (v[4 i + 2], v[4 i + 3]) the columns 8 i + 2 t, 8 i + 2 t + 1.
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+// Of the four lanes of a row, each with pairs of every eighth column, lane t gets the eight
+// columns from 8 t on: a transpose of 4 x 4 pairs in two rounds. v: pairs 0..3 of this lane.
+__device__ __forceinline__ void row_pieces(float (&v)[8], int t) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit *= 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & bit))
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& a = v[2 * i + e];
+          float& b = v[2 * (i + bit) + e];
+          const bool up = t & bit;
+          const float got = __shfl_xor_sync(0xffffffffu, up ? a : b, bit);
+          (up ? a : b) = got;
+        }
 }
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
@@ -87,80 +109,45 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-struct Words8 {
-  uint32_t w[8];
-};
-__device__ __forceinline__ Words8 ld32(const void* p) {
-  Words8 v;
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]), "=r"(v.w[7])
-               : "l"(p)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void st32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
-// kCols consecutive addends of a row as they are in memory: pieces of 32 bytes where rows
-// and addresses are multiples of that, else of 16. Those from column `left` on are not read.
+// Eight consecutive addends of a row as they are in memory; the output's of eight sums.
 template <int kAdd>
 struct Addends {
-  static constexpr int kItem = kAdd == kTypeF32 ? 4 : 2, kWords = kCols * kItem / 4;
-  uint32_t w[kWords];
-  __device__ __forceinline__ void load(const LoraArgs& a, long long at, int left, bool pieces32) {
-    const char* p = static_cast<const char*>(a.add) + at * kItem;
-    if (pieces32) {
-#pragma unroll
-      for (int i = 0; i < kWords / 8; ++i)
-        if (i * 32 / kItem < left) {
-          const Words8 v = ld32(p + 32 * i);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) w[8 * i + j] = v.w[j];
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kWords / 4; ++i)
-        if (i * 16 / kItem < left) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p + 16 * i);
-          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-        }
-    }
+  uint4 w[kAdd == kTypeF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const LoraArgs& a, long long at) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.add) + at * (kAdd == kTypeF32 ? 4 : 2));
+    w[0] = p[0];
+    if constexpr (kAdd == kTypeF32) w[1] = p[1];
   }
   __device__ __forceinline__ float operator[](int i) const {
-    return __uint_as_float(kItem == 4 ? w[i] : i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+    if constexpr (kAdd == kTypeF32) {
+      const uint4 v = w[i >> 2];
+      return __uint_as_float((i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w);
+    } else {
+      const uint32_t v = (i >> 1) == 0 ? w[0].x : (i >> 1) == 1 ? w[0].y : (i >> 1) == 2 ? w[0].z : w[0].w;
+      return __uint_as_float(i & 1 ? v & 0xFFFF0000u : v << 16);
+    }
   }
 };
 template <>
 struct Addends<-1> {
-  __device__ __forceinline__ void load(const LoraArgs&, long long, int, bool) {}
+  __device__ __forceinline__ void load(const LoraArgs&, long long) {}
   __device__ __forceinline__ float operator[](int) const { return 0.f; }
 };
+
 template <int kOut>
-__device__ __forceinline__ void store_cols(const LoraArgs& a, long long at, int left, bool pieces32, const float (&y)[kCols]) {
-  constexpr int kItem = kOut == kTypeF32 ? 4 : 2, kWords = kCols * kItem / 4;
-  uint32_t w[kWords];
+__device__ __forceinline__ void store_cols(const LoraArgs& a, long long at, const float (&y)[8]) {
   if constexpr (kOut == kTypeF32) {
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) w[i] = __float_as_uint(y[i]);
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+    p[0] = make_float4(y[0], y[1], y[2], y[3]);
+    p[1] = make_float4(y[4], y[5], y[6], y[7]);
   } else {
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < kCols / 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-  }
-  char* p = static_cast<char*>(a.out) + at * kItem;
-  if (pieces32) {
-#pragma unroll
-    for (int i = 0; i < kWords / 8; ++i)
-      if (i * 32 / kItem < left) st32(p + 32 * i, w + 8 * i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kWords / 4; ++i)
-      if (i * 16 / kItem < left) *reinterpret_cast<uint4*>(p + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -168,7 +155,7 @@ __device__ __forceinline__ void store_cols(const LoraArgs& a, long long at, int 
 template <int kAdd, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     lora_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ LoraArgs a, const Order order,
-                     const ManyPlan plan, bool pieces32, uint32_t limit, int test_never_wait, int32_t* status) {
+                     const ManyPlan plan, uint32_t limit, int test_never_wait, int32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -221,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     tma_prefetch_map(&amap);
     tma_prefetch_map(&bmap);
-    for (int i = 0; i < S; ++i) mbar_init(full(i), 1 + kEpiWarps), mbar_init(empty(i), 1);
+    for (int i = 0; i < S; ++i) mbar_init(full(i), 1 + kEpiThreads), mbar_init(empty(i), 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), kEpiWarps);
     mbar_init(summed, 1);
     mbar_init(drain, 1);
@@ -246,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ahead = min(nn, S);            // column tiles copied before the join
   const int wide = plan.rank16 > kChunk ? 2 : 1;  // boxes of a row of b
   auto slot_of = [&](int i) { return ring + (i % S) * plan.stage_bytes; };
-  // what the copying lane issues as item i: a stage of a, or a tile of b (and then the warps'
-  // arrivals too, which copy no x into it)
+  // what the copying lane issues as item i: a stage of a, or a tile of b (and then the arrivals
+  // of the threads too, which copy no x into it)
   bool copying = true;
   int issued = 0;
   const uint64_t keep = l2_policy_evict_last();
@@ -258,11 +245,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_load_2d(slot_of(i) + kBox, &amap, (c0 + i) * 128, l * a.r, full(i % S), keep);
     } else {
       const int n0 = (nt0 + i - kn) * kTile;
-      mbar_arrive_cnt(full(i % S), kEpiWarps);
+      mbar_arrive_cnt(full(i % S), kEpiThreads);
       mbar_arrive_expect_tx(full(i % S), wide * kBox);
       for (int b = 0; b < wide; ++b) tma_load_2d(slot_of(i) + b * kBox, &bmap, b * 128, l * a.N + n0, full(i % S), keep);
     }
     return true;
+  };
+
+  // the output of a joining lane: of each tile eight columns of four rows
+  const int col = (warp >> 2) * kCols + 8 * (lane & 3);
+  int m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = row_of[(warp & 3) * 32 + 8 * i + (lane >> 2)];
+  auto at_of = [&](int i, int j) { return static_cast<long long>(m[i]) * a.N + (nt0 + j) * kTile + col; };
+  auto has = [&](int i, int j) { return m[i] >= 0 && j < nn && (nt0 + j) * kTile + col < a.N; };
+  auto ask_addends = [&](int j) {
+    if (kAdd >= 0)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (has(i, j)) prefetch_l2(static_cast<const char*>(a.add) + at_of(i, j) * (kAdd == kTypeF32 ? 4 : 2));
   };
 
   // ---- 1. this CTA's columns of a[l] x
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kn; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait(full(i % S), (i / S) & 1, abort_flag, status, kStatusTimeout, limit));
       if (!ok) break;
+      fence_proxy_async_smem();  // (x came by ordinary copies, which the threads do not wait for themselves)
       tc_fence_after();
       if (leader) {
         const uint64_t ad = sw128_kmajor_desc(slot_of(i)), bd = sw128_kmajor_desc(slot_of(i) + kBox);
@@ -290,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (leader) tc_commit(summed);
     __syncwarp();
   } else {
+    // the first column tiles' addends are asked into L2 meanwhile
+    for (int j = 0; j < min(kAhead, nn); ++j) ask_addends(j);
     // a thread copies the same 16 bytes of each stage's 128 of two rows; the rows' 16-byte
     // pieces are swizzled as the MMA reads them
     {
@@ -298,24 +302,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint16_t* x0 = a.x + max(m0, 0) * a.ldx + 8 * piece;
       const uint16_t* x1 = a.x + max(m1, 0) * a.ldx + 8 * piece;
       const uint32_t at = row * 128 + ((piece ^ (row & 7)) << 4);
-      for (int i = 0; i < kn + S - 1; ++i) {
-        if (i < kn) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
-          if (!ok) break;
-          const int k = (c0 + i) * kChunk;
-          const bool in = k + 8 * piece < a.K;
-          copy16(slot_of(i) + at, in ? x0 + k : x0, in && m0 >= 0 ? 16 : 0);
-          copy16(slot_of(i) + at + kBox / 2, in ? x1 + k : x1, in && m1 >= 0 ? 16 : 0);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (i >= S - 1) {
-          copies_left(S - 1);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(full((i - S + 1) % S));
-        }
+      for (int i = 0; i < kn; ++i) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
+        if (!ok) break;
+        const int k = (c0 + i) * kChunk;
+        const bool in = k + 8 * piece < a.K;
+        copy16(slot_of(i) + at, in ? x0 + k : x0, in && m0 >= 0 ? 16 : 0);
+        copy16(slot_of(i) + at + kBox / 2, in ? x1 + k : x1, in && m1 >= 0 ? 16 : 0);
+        copies_arrive(full(i % S));
       }
-      copies_left(0);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
     if (test_never_wait) ok = __all_sync(0xffffffffu, mbar_wait(never, 0, abort_flag, status, kStatusTimeout, limit));
     ok = ok && __all_sync(0xffffffffu, mbar_wait(summed, 0, abort_flag, status, kStatusTimeout, limit));
@@ -416,32 +412,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int col = (warp >> 2) * kCols, m = row_of[(warp & 3) * 32 + lane];
-    const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col;
-    const long long row_at = static_cast<long long>(max(m, 0)) * a.N;
-    Addends<kAdd> next;
+    const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (warp >> 2) * kCols;
+    Addends<kAdd> next[4];
     auto load = [&](int j) {
-      const int n = (nt0 + j) * kTile + col;
-      next.load(a, row_at + n, m >= 0 && j < nn ? a.N - n : 0, pieces32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (has(i, j)) next[i].load(a, at_of(i, j));
     };
     load(0);
     for (int j = 0; j < nn; ++j) {
-      const int n = (nt0 + j) * kTile + col, buf = j & 1;
+      const int buf = j & 1;
       ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(buf), (j >> 1) & 1, abort_flag, status, kStatusTimeout, limit));
       if (!ok) break;
       tc_fence_after();
-      uint32_t v[kCols];
-      tmem_ld32(src + buf * kTile, v);
-      const Addends<kAdd> now = next;
+      uint32_t v[2][16];
+      tmem_ld_16x32(src + buf * kTile, v[0]);
+      tmem_ld_16x32(src + buf * kTile + (16u << 16), v[1]);
+      if (j + kAhead < nn) ask_addends(j + kAhead);
+      Addends<kAdd> now[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) now[i] = next[i];
       load(j + 1);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty(buf));
-      float y[kCols];
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) y[i] = __uint_as_float(v[i]) + now[i];
-      if (m >= 0) store_cols<kOut>(a, row_at + n, a.N - n, pieces32, y);
+      for (int i = 0; i < 4; ++i) {  // rows 8 i + lane / 4
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) y[2 * k + e] = __uint_as_float(v[i >> 1][4 * k + 2 * (i & 1) + e]);
+        row_pieces(y, lane & 3);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] += now[i][k];
+        if (has(i, j)) store_cols<kOut>(a, at_of(i, j), y);
+      }
     }
   }
   __syncwarp();
@@ -506,10 +513,8 @@ cudaError_t launch(const LoraArgs& a, const CUtensorMap& amap, const CUtensorMap
   uint32_t limit;
   int never;
   fp8_wait_settings(&limit, &never);
-  const uintptr_t where = reinterpret_cast<uintptr_t>(a.add) | reinterpret_cast<uintptr_t>(a.out);
-  const bool pieces32 = where % 32 == 0 && a.N % 16 == 0;
   return launch_cluster(lora_many_kernel<kAdd, kOut>, dim3(static_cast<unsigned>(p.tiles) * p.ctas), dim3(kThreads), p.smem, stream,
-                        p.ctas, amap, bmap, a, order, p, pieces32, limit, never, status);
+                        p.ctas, amap, bmap, a, order, p, limit, never, status);
 }
 }  // namespace
 
