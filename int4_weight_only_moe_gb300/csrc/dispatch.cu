@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) sort_kernel(const SortArgs a,
   const int rank = ctas > 1 ? static_cast<int>(cluster_rank()) : 0;
   for (int i = tid; i < kSortWarps * B; i += kSortThreads) hist[i] = 0;
   __syncthreads();
+  pdl_launch_dependents();  // (they wait for this kernel's end, and set up meanwhile)
   pdl_wait();
   const int run = (a.n + kSortWarps * ctas - 1) / (kSortWarps * ctas);
   const long long first = static_cast<long long>(rank * kSortWarps + w) * run;

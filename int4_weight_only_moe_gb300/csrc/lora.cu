@@ -280,7 +280,7 @@ cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
   // 16-byte pieces of every row
   const bool whole = a.K % 8 == 0 && a.N % 8 == 0 && a.r % 8 == 0 && (a.M == 1 || a.ldx % 8 == 0) && aligned(a.x, 16) &&
                      aligned(a.a, 16) && aligned(a.b, 16) && aligned(a.add, 16) && aligned(a.out, 16);
-  if (whole && a.M > kFewRows && static_cast<long long>(a.L) * a.N < (1LL << 31) - kFewRows) return launch_lora_many(a, num_sms, stream);
+  if (whole && a.M > kFewRows) return launch_lora_many(a, num_sms, stream);
   if (whole && a.M <= kFewRows) {
     if (a.r <= 16) return launch_few<2>(a, stream);
     if (a.r <= 32) return launch_few<4>(a, stream);

@@ -2,24 +2,33 @@
 //
 // The rows are sorted by adapter (the order of dispatch.cu, filled up to tiles of 128 rows;
 // rows without an adapter are the last bucket's). A cluster of CTAs takes a tile. Each CTA
-//   1. sums its share of a[l] x's columns: tcgen05 MMAs of 128 rows x r, whose x rows 16
-//      warps copy from wherever they lie, a stage's copies under way beside the next ones'
-//      (the copy engine's gathers of four rows take 18 cycles a row of 128 bytes here, five
-//      times as long);
+//   1. sums its share of a[l] x's columns: tcgen05 MMAs of 128 rows x r, whose x rows are
+//      copied from wherever they lie;
 //   2. joins the sums with the cluster's other CTAs: each sends its sums of a row to the
 //      row's CTA, which adds them in the order of the ranks, scales them, splits them into
 //      bf16 parts (two, three for an fp32 output: 16 and 24 bits of the sum) and hands them
 //      to all CTAs, straight into the second product's operand;
 //   3. computes its share of the N columns: MMAs of 128 rows x 128 columns over the parts,
 //      one after another against the same tile of b[l], two accumulators in turn, taken out
-//      of tensor memory by 16 warps that add the addends, which they have loaded one tile
-//      ahead, and write the output, eight columns to a lane.
-// Nothing but x, a, b, the addends and the output goes through memory, and each once (a and
-// b once for each tile, from L2). The operations are few, r of them for a byte at most: what
-// bounds it is memory.
+//      of tensor memory by eight warps that add the addends, which they have loaded half a
+//      tile ahead, and write the output.
+// Two CTAs share an SM where the rank allows, so that one reads x while the other joins or
+// writes. Nothing but x, a, b, the addends and the output goes through memory, and each once
+// (a and b once for each tile, from L2). The operations are few, r of them for a byte at
+// most: what bounds it is memory, if the copies and the output take few instructions:
+//   - Operands come by 16-byte copies of single threads, zeros where there is no row or
+//     column. (The copy engine's gathers of four rows of 128 bytes take 18 cycles a row
+//     here: 2,370 cycles for a stage of x, which these bring in 500.) 64 threads copy a
+//     stage of x: each arrives at the stage's barrier by itself, and 256 arrivals took as
+//     long as the copies.
+//   - b's rows are copied in such an order that the four lanes that get a row's sums out of
+//     tensor memory get eight consecutive columns each, not pairs of columns: the addends
+//     and the output move in 16- and 32-byte pieces, 64 or 128 bytes of a row to four
+//     lanes, without an exchange. (A row to a lane, 32 lines to an access: 4,000 cycles a
+//     tile; exchanges: 3,300.)
 //
-// Warps: 0..15 rows of x, joining and output, 16 the copies of a and b, 17 the MMAs. All
-// sums have a fixed order.
+// Warps: 0..7 x, joining and output, 8 the copies of a and b, 9 the MMAs. All sums have a
+// fixed order.
 #include <algorithm>
 
 #include "fp8_tma.cuh"
@@ -31,18 +40,27 @@ namespace {
 constexpr int kTile = 128;         // rows of a tile, columns of an accumulator
 constexpr int kChunk = 64;         // columns of x to a stage: 128 bytes
 constexpr int kBox = kTile * 128;  // bytes of 128 rows of 128 bytes
-constexpr int kEpiWarps = 16, kEpiThreads = kEpiWarps * 32, kWarpCopy = 16, kWarpMma = 17, kThreads = 18 * 32;
-constexpr int kCols = kTile * 4 / kEpiWarps;  // of an accumulator, to a warp
-constexpr int kAhead = 4;          // column tiles whose addends are asked into L2 ahead
+constexpr int kEpiWarps = 8, kEpiThreads = kEpiWarps * 32, kWarpCopy = 8, kWarpMma = 9, kThreads = 10 * 32;
+constexpr int kCols = kTile * 4 / kEpiWarps;  // of an accumulator, to a warp, 32 at a time
+constexpr int kTeam = 64, kTeams = 2;  // threads that copy a stage of x, by turns
+// A team asks a stage's barrier for a phase by its parity, which two phases share, and only
+// every kTeams-th stage. Its last answer says that the MMAs of kTeams + S stages ago are done;
+// that those of 2 S ago are, whose phase has the same parity, follows if kTeams <= S. (Four
+// teams and three stages overwrote stages in use, until waits ran out.)
+constexpr int kLeastStages = 3;
+static_assert(kTeams <= kLeastStages, "a parity is answered by the phase before the last");
+constexpr int kAhead = 6;          // halves of column tiles whose addends are asked into L2 ahead
 constexpr int kMaxStages = 6;
 constexpr int kHead = 2048;        // barriers, the tile's rows
-constexpr int kSmemMost = 227 * 1024;
+constexpr int kSmemMost = 227 * 1024, kSmemHalf = 113 * 1024;
+constexpr int kSmemLeast = 77 * 1024;  // (two CTAs to an SM at most: they share its tensor memory)
 
 struct ManyPlan {
   int ctas;         // to a tile
   int parts;        // bf16 parts of a sum
   int rank16;       // r, up to a multiple of 16
   int stages, stage_bytes, smem;
+  int b_stages;     // tiles of b under way
   int tiles;        // at most
 };
 struct Order {
@@ -81,23 +99,9 @@ __device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&v)[16])
       : "r"(taddr)
       : "memory");
 }
-// Of the four lanes of a row, each with pairs of every eighth column, lane t gets the eight
-// columns from 8 t on: a transpose of 4 x 4 pairs in two rounds. v: pairs 0..3 of this lane.
-__device__ __forceinline__ void row_pieces(float (&v)[8], int t) {
-#pragma unroll
-  for (int bit = 1; bit <= 2; bit *= 2)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (!(i & bit))
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& a = v[2 * i + e];
-          float& b = v[2 * (i + bit) + e];
-          const bool up = t & bit;
-          const float got = __shfl_xor_sync(0xffffffffu, up ? a : b, bit);
-          (up ? a : b) = got;
-        }
-}
+// Column of a block of 32 whose b row stands in the operand's row c: columns 8 i + 2 t + e
+// of the sums, those of lane 4 g + t above, are its columns 8 t + 2 i + e.
+__device__ __forceinline__ int column_at(int c) { return 8 * ((c >> 1) & 3) + 2 * (c >> 3) + (c & 1); }
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
@@ -153,9 +157,8 @@ __device__ __forceinline__ void store_cols(const LoraArgs& a, long long at, cons
 
 // kAdd: the addends' type, -1 without; kOut: the output's.
 template <int kAdd, int kOut>
-__global__ void __launch_bounds__(kThreads, 1)
-    lora_many_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap, const __grid_constant__ LoraArgs a, const Order order,
-                     const ManyPlan plan, uint32_t limit, int test_never_wait, int32_t* status) {
+__global__ void __launch_bounds__(kThreads, 2)
+    lora_many_kernel(const __grid_constant__ LoraArgs a, const Order order, const ManyPlan plan, uint32_t limit, int test_never_wait, int32_t* status) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - smem_u32(smem_raw));
@@ -164,20 +167,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto empty = [&](int i) { return base + 8 * (kMaxStages + i); };
   auto tfull = [&](int i) { return base + 8 * (2 * kMaxStages + i); };
   auto tempty = [&](int i) { return base + 8 * (2 * kMaxStages + 2 + i); };
+  auto bfull = [&](int i) { return base + 8 * (2 * kMaxStages + 8 + i); };
+  auto bempty = [&](int i) { return base + 8 * (2 * kMaxStages + 10 + i); };
   const uint32_t summed = base + 8 * (2 * kMaxStages + 4), drain = summed + 8, never = summed + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + 256);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + 260);
   int* row_of = reinterpret_cast<int*>(gbase + 1024);  // [128] the tile's rows, -1 behind the last
-  const uint32_t parts_at = base + kHead;              // second product's operand: blocks of 128 rows x 64 columns
-  const int part_blocks = (plan.parts * plan.rank16 + kChunk - 1) / kChunk;
-  const uint32_t sums_at = parts_at + part_blocks * kBox;  // arriving sums: [CTA][r / 4][row] of four
-  const uint32_t ring = sums_at + kTile * plan.rank16 * 4;
+  // arriving sums: [CTA][r / 4][row] of four; then the stages of x and a, and when those are
+  // done in their place the second product's operand (blocks of 128 rows x 64 columns) and
+  // tiles of b
+  const uint32_t sums_at = base + kHead, ring = sums_at + kTile * plan.rank16 * 4, parts_at = ring;
+  const int wide = plan.rank16 > kChunk ? 2 : 1;  // boxes of a row of b
+  const uint32_t b_ring = parts_at + (plan.parts * plan.rank16 + kChunk - 1) / kChunk * kBox;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = plan.ctas, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = blockIdx.x / C;
   int* bucket = reinterpret_cast<int*>(gbase + 264);
-  if (threadIdx.x == 0) *bucket = -1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(full(i), kTeam + 32), mbar_init(empty(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bfull(i), 32), mbar_init(bempty(i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), kEpiWarps);
+    mbar_init(summed, 1);
+    mbar_init(drain, 1);
+    mbar_init(never, 1);
+    *abort_flag = 0;
+    *bucket = -1;
+    fence_mbar_init();
+  }
   __syncthreads();
   pdl_wait();
   const int32_t* slots = order.slots + static_cast<long long>(tile) * kTile;
@@ -205,17 +222,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  if (threadIdx.x == 0) {
-    tma_prefetch_map(&amap);
-    tma_prefetch_map(&bmap);
-    for (int i = 0; i < S; ++i) mbar_init(full(i), 1 + kEpiThreads), mbar_init(empty(i), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(tfull(i), 1), mbar_init(tempty(i), kEpiWarps);
-    mbar_init(summed, 1);
-    mbar_init(drain, 1);
-    mbar_init(never, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
   if (warp == kWarpMma) {
     __syncwarp();
     tmem_alloc(smem_u32(tmem_slot), 2 * kTile);
@@ -230,49 +236,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int chunks = (a.K + kChunk - 1) / kChunk, cper = (chunks + C - 1) / C;
   const int c0 = min(chunks, rank * cper), c1 = min(chunks, c0 + cper);
   const int kn = c1 - c0, nn = nt1 - nt0;  // this CTA's stages of x, its column tiles
-  const int ahead = min(nn, S);            // column tiles copied before the join
-  const int wide = plan.rank16 > kChunk ? 2 : 1;  // boxes of a row of b
   auto slot_of = [&](int i) { return ring + (i % S) * plan.stage_bytes; };
-  // what the copying lane issues as item i: a stage of a, or a tile of b (and then the arrivals
-  // of the threads too, which copy no x into it)
-  bool copying = true;
-  int issued = 0;
-  const uint64_t keep = l2_policy_evict_last();
-  auto copy = [&](int i) {
-    if (!mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit)) return false;
-    if (i < kn) {
-      mbar_arrive_expect_tx(full(i % S), plan.rank16 * 128);
-      tma_load_2d(slot_of(i) + kBox, &amap, (c0 + i) * 128, l * a.r, full(i % S), keep);
-    } else {
-      const int n0 = (nt0 + i - kn) * kTile;
-      mbar_arrive_cnt(full(i % S), kEpiThreads);
-      mbar_arrive_expect_tx(full(i % S), wide * kBox);
-      for (int b = 0; b < wide; ++b) tma_load_2d(slot_of(i) + b * kBox, &bmap, b * 128, l * a.N + n0, full(i % S), keep);
+  const int SB = plan.b_stages;
+  auto b_slot_of = [&](int j) { return b_ring + (j % SB) * wide * kBox; };
+  const int piece = lane & 7;  // the 16 bytes of a 128-byte row that this lane copies
+  // the copying warp's part of tile j of b: 32 columns at a time, rows in their order
+  const uint16_t* b_from = a.b + static_cast<long long>(l) * a.N * a.r;
+  auto copy_b = [&](int j) {
+    if (!__all_sync(0xffffffffu, mbar_wait(bempty(j % SB), ((j / SB) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit))) return false;
+    const int n0 = (nt0 + j) * kTile;
+    for (int c = lane >> 3; c < kTile; c += 4) {
+      const int n = n0 + (c & ~31) + column_at(c & 31);
+      for (int h = 0; h < wide; ++h) {
+        const int k = h * kChunk + 8 * piece;
+        const bool in = n < a.N && k < a.r;
+        copy16(b_slot_of(j) + h * kBox + c * 128 + ((piece ^ (c & 7)) << 4), b_from + (in ? static_cast<long long>(n) * a.r + k : 0), in ? 16 : 0);
+      }
     }
+    copies_arrive(bfull(j % SB));
     return true;
   };
+  int issued = 0;  // tiles of b
 
-  // the output of a joining lane: of each tile eight columns of four rows
-  const int col = (warp >> 2) * kCols + 8 * (lane & 3);
-  int m[4];
+  // the output of a joining lane: eight columns of four rows, of each half q of its warp's
+  // columns of a tile
+  long long row_at[4];  // -1: no row
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m[i] = row_of[(warp & 3) * 32 + 8 * i + (lane >> 2)];
-  auto at_of = [&](int i, int j) { return static_cast<long long>(m[i]) * a.N + (nt0 + j) * kTile + col; };
-  auto has = [&](int i, int j) { return m[i] >= 0 && j < nn && (nt0 + j) * kTile + col < a.N; };
-  auto ask_addends = [&](int j) {
-    if (kAdd >= 0)
+  for (int i = 0; i < 4; ++i) {
+    const int m = row_of[(warp & 3) * 32 + 8 * i + (lane >> 2)];
+    row_at[i] = m < 0 ? -1 : static_cast<long long>(m) * a.N;
+  }
+  const int col0 = nt0 * kTile + (warp >> 2) * kCols + 8 * (lane & 3);
+  auto col_of = [&](int q) { return col0 + (q >> 1) * kTile + (q & 1) * 32; };
+  auto ask_addends = [&](int q) {
+    const int n = col_of(q);
+    if (kAdd >= 0 && q < 2 * nn && n < a.N)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (has(i, j)) prefetch_l2(static_cast<const char*>(a.add) + at_of(i, j) * (kAdd == kTypeF32 ? 4 : 2));
+        if (row_at[i] >= 0) prefetch_l2(static_cast<const char*>(a.add) + (row_at[i] + n) * (kAdd == kTypeF32 ? 4 : 2));
   };
 
   // ---- 1. this CTA's columns of a[l] x
   bool ok = true;
   if (warp == kWarpCopy) {
-    if (lane == 0)
-      for (; issued < kn + ahead; ++issued)
-        if (!(copying = copy(issued))) break;
-    __syncwarp();
+    const uint16_t* from = a.a + static_cast<long long>(l) * a.r * a.K + 8 * piece;
+    for (int i = 0; i < kn && ok; ++i) {
+      ok = __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
+      if (!ok) break;
+      const int k = (c0 + i) * kChunk;
+      for (int row = lane >> 3; row < plan.rank16; row += 4) {
+        const bool in = row < a.r && k + 8 * piece < a.K;
+        copy16(slot_of(i) + kBox + row * 128 + ((piece ^ (row & 7)) << 4), in ? from + static_cast<long long>(row) * a.K + k : a.a, in ? 16 : 0);
+      }
+      copies_arrive(full(i % S));
+    }
+    // (the stages' place is free when all of their MMAs are done)
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(summed, 0, abort_flag, status, kStatusTimeout, limit));
+    for (; ok && issued < min(nn, SB); ++issued) ok = copy_b(issued);
   } else if (warp == kWarpMma) {
     const uint32_t idesc = idesc_bf16_f32(kTile, plan.rank16);
     const bool leader = elect_one();
@@ -293,26 +313,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // the first column tiles' addends are asked into L2 meanwhile
-    for (int j = 0; j < min(kAhead, nn); ++j) ask_addends(j);
-    // a thread copies the same 16 bytes of each stage's 128 of two rows; the rows' 16-byte
-    // pieces are swizzled as the MMA reads them
-    {
-      const int piece = threadIdx.x & 7, row = threadIdx.x >> 3;
-      const int m0 = row_of[row], m1 = row_of[row + kTile / 2];
-      const uint16_t* x0 = a.x + max(m0, 0) * a.ldx + 8 * piece;
-      const uint16_t* x1 = a.x + max(m1, 0) * a.ldx + 8 * piece;
-      const uint32_t at = row * 128 + ((piece ^ (row & 7)) << 4);
-      for (int i = 0; i < kn; ++i) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
-        if (!ok) break;
-        const int k = (c0 + i) * kChunk;
-        const bool in = k + 8 * piece < a.K;
-        copy16(slot_of(i) + at, in ? x0 + k : x0, in && m0 >= 0 ? 16 : 0);
-        copy16(slot_of(i) + at + kBox / 2, in ? x1 + k : x1, in && m1 >= 0 ? 16 : 0);
-        copies_arrive(full(i % S));
+    for (int q = 0; q < kAhead; ++q) ask_addends(q);
+    // the rows' 16-byte pieces are swizzled as the MMA reads them
+    const int team = threadIdx.x / kTeam, first = threadIdx.x % kTeam >> 3;
+    for (int i = team; i < kn && team < kTeams; i += kTeams) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
+      if (!ok) break;
+      const int k = (c0 + i) * kChunk + 8 * piece;
+#pragma unroll
+      for (int row = first, j = 0; j < kTile * 8 / kTeam; ++j, row += kTeam / 8) {
+        const int m = row_of[row];
+        const bool in = m >= 0 && k < a.K;
+        copy16(slot_of(i) + row * 128 + ((piece ^ (row & 7)) << 4), a.x + (in ? m * a.ldx + k : 0), in ? 16 : 0);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      copies_arrive(full(i % S));
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (test_never_wait) ok = __all_sync(0xffffffffu, mbar_wait(never, 0, abort_flag, status, kStatusTimeout, limit));
     ok = ok && __all_sync(0xffffffffu, mbar_wait(summed, 0, abort_flag, status, kStatusTimeout, limit));
     tc_fence_after();
@@ -345,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = 4 * q + j < a.r ? s[j] * scale : 0.f;  // (behind r stand the next adapter's)
+      for (int j = 0; j < 4; ++j) s[j] *= scale;
       for (int p = 0; p < plan.parts; ++p) {
         uint16_t h[4];
 #pragma unroll
@@ -368,14 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- 3. this CTA's columns of the output
   if (warp == kWarpCopy) {
-    if (lane == 0) {
-      for (; issued < kn + nn && copying; ++issued)
-        if (!(copying = copy(issued))) break;
-      // the last copies have landed, and the MMAs' last signals, before shared memory is given up
-      for (int i = max(0, issued - S); i < issued; ++i)
-        if (!mbar_wait(empty(i % S), (i / S) & 1, abort_flag, status, kStatusTimeout, limit)) break;
-    }
-    __syncwarp();
+    for (; ok && issued < nn; ++issued) ok = copy_b(issued);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    // the MMAs' last signals have arrived before shared memory is given up
+    for (int i = max(0, kn - S); i < kn && ok; ++i)
+      ok = __all_sync(0xffffffffu, mbar_wait(empty(i % S), (i / S) & 1, abort_flag, status, kStatusTimeout, limit));
+    for (int j = max(0, nn - SB); j < nn && ok; ++j)
+      ok = __all_sync(0xffffffffu, mbar_wait(bempty(j % SB), (j / SB) & 1, abort_flag, status, kStatusTimeout, limit));
     if (*abort_flag) {  // (copies and signals that nobody waited for get 2 ms)
       const long long t0 = clock64();
       while (clock64() - t0 < 4000000) {
@@ -385,10 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t idesc = idesc_bf16_f32(kTile, kTile);
     const bool leader = elect_one();
     for (int j = 0; j < nn && ok; ++j) {
-      const int i = kn + j, buf = j & 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(full(i % S), (i / S) & 1, abort_flag, status, kStatusTimeout, limit) &&
+      const int buf = j & 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bfull(j % SB), (j / SB) & 1, abort_flag, status, kStatusTimeout, limit) &&
                                        mbar_wait(tempty(buf), ((j >> 1) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
       if (!ok) break;
+      fence_proxy_async_smem();
       tc_fence_after();
       if (leader) {
         // (the small parts first)
@@ -397,11 +413,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < plan.rank16; k += 16) {
             const int at = p * plan.rank16 + k;
             const uint64_t ad = sw128_kmajor_desc(parts_at + at / kChunk * kBox) + (at % kChunk) / 8;
-            const uint64_t bd = sw128_kmajor_desc(slot_of(i) + k / kChunk * kBox) + (k % kChunk) / 8;
+            const uint64_t bd = sw128_kmajor_desc(b_slot_of(j) + k / kChunk * kBox) + (k % kChunk) / 8;
             tc_mma_bf16(tmem + buf * kTile, ad, bd, idesc, more);
             more = 1;
           }
-        tc_commit(empty(i % S));
+        tc_commit(bempty(j % SB));
         tc_commit(tfull(buf));
       }
       __syncwarp();
@@ -414,40 +430,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (warp >> 2) * kCols;
     Addends<kAdd> next[4];
-    auto load = [&](int j) {
+    auto load = [&](int q) {
+      const int n = col_of(q);
+      if (q < 2 * nn && n < a.N)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (has(i, j)) next[i].load(a, at_of(i, j));
+        for (int i = 0; i < 4; ++i)
+          if (row_at[i] >= 0) next[i].load(a, row_at[i] + n);
     };
     load(0);
-    for (int j = 0; j < nn; ++j) {
-      const int buf = j & 1;
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(buf), (j >> 1) & 1, abort_flag, status, kStatusTimeout, limit));
-      if (!ok) break;
-      tc_fence_after();
+    for (int q = 0; q < 2 * nn; ++q) {
+      const int j = q >> 1, buf = j & 1, n = col_of(q);
+      if (!(q & 1)) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(buf), (j >> 1) & 1, abort_flag, status, kStatusTimeout, limit));
+        if (!ok) break;
+        tc_fence_after();
+      }
       uint32_t v[2][16];
-      tmem_ld_16x32(src + buf * kTile, v[0]);
-      tmem_ld_16x32(src + buf * kTile + (16u << 16), v[1]);
-      if (j + kAhead < nn) ask_addends(j + kAhead);
+      tmem_ld_16x32(src + buf * kTile + (q & 1) * 32, v[0]);
+      tmem_ld_16x32(src + buf * kTile + (q & 1) * 32 + (16u << 16), v[1]);
+      ask_addends(q + kAhead);
       Addends<kAdd> now[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) now[i] = next[i];
-      load(j + 1);
+      load(q + 1);
       tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty(buf));
+      if (q & 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty(buf));
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // rows 8 i + lane / 4
         float y[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) y[2 * k + e] = __uint_as_float(v[i >> 1][4 * k + 2 * (i & 1) + e]);
-        row_pieces(y, lane & 3);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] += now[i][k];
-        if (has(i, j)) store_cols<kOut>(a, at_of(i, j), y);
+        for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v[i >> 1][4 * (k >> 1) + 2 * (i & 1) + (k & 1)]) + now[i][k];
+        if (row_at[i] >= 0 && n < a.N) store_cols<kOut>(a, row_at[i] + n, y);
       }
     }
   }
@@ -472,20 +489,23 @@ ManyPlan plan_many(const LoraArgs& a, int num_sms) {
   p.parts = a.out_type == kTypeF32 ? 3 : 2;
   p.rank16 = (a.r + 15) / 16 * 16;
   p.stage_bytes = kBox + (p.rank16 > kChunk ? kBox : p.rank16 * 128);
-  const int fixed = kHead + 1024 + (p.parts * p.rank16 + kChunk - 1) / kChunk * kBox + kTile * p.rank16 * 4;
-  p.stages = std::min(kMaxStages, (kSmemMost - fixed) / p.stage_bytes);
-  p.smem = fixed + p.stages * p.stage_bytes;
+  const int fixed = kHead + 1024 + kTile * p.rank16 * 4;
+  const int operand = (p.parts * p.rank16 + kChunk - 1) / kChunk * kBox, b_tile = p.rank16 > kChunk ? 2 * kBox : kBox;
+  // two CTAs to an SM if at least three stages, and the second product's operands in their
+  // place, fit a half
+  int room = kSmemHalf - fixed;
+  if (room < kLeastStages * p.stage_bytes || room < operand + b_tile) room = kSmemMost - fixed;
+  p.stages = std::min(kMaxStages, room / p.stage_bytes);  // (five at the least where one CTA has the SM)
+  p.b_stages = room >= operand + 2 * b_tile ? 2 : 1;
+  p.smem = std::max(kSmemLeast, fixed + std::max(p.stages * p.stage_bytes, operand + p.b_stages * b_tile));
+  const int per_sm = p.smem <= kSmemHalf ? 2 : 1;
   p.tiles = order_rows(a.M, a.L) / kTile;
   // CTAs to a tile: as many as leave the tiles that there will be about (half an extra one
   // for each adapter) in one wave
   const int about = (a.M + kTile - 1) / kTile + std::min(a.L, a.M / kTile) / 2;
   p.ctas = 8;
-  while (p.ctas > 1 && about * p.ctas > num_sms) p.ctas /= 2;
+  while (p.ctas > 1 && about * p.ctas > per_sm * num_sms) p.ctas /= 2;
   return p;
-}
-
-bool make_bf16_map(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride, int box_rows) {
-  return make_byte_map(map, base, rows, 2 * cols, 2 * stride, box_rows);
 }
 
 }  // namespace
@@ -496,8 +516,7 @@ size_t lora_many_workspace(int M, int L) {
 
 namespace {
 template <int kAdd, int kOut>
-cudaError_t launch(const LoraArgs& a, const CUtensorMap& amap, const CUtensorMap& bmap, const Order& order, const ManyPlan& p,
-                   cudaStream_t stream) {
+cudaError_t launch(const LoraArgs& a, const Order& order, const ManyPlan& p, cudaStream_t stream) {
   static PerDevice<int> ready;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -514,26 +533,22 @@ cudaError_t launch(const LoraArgs& a, const CUtensorMap& amap, const CUtensorMap
   int never;
   fp8_wait_settings(&limit, &never);
   return launch_cluster(lora_many_kernel<kAdd, kOut>, dim3(static_cast<unsigned>(p.tiles) * p.ctas), dim3(kThreads), p.smem, stream,
-                        p.ctas, amap, bmap, a, order, p, limit, never, status);
+                        p.ctas, a, order, p, limit, never, status);
 }
 }  // namespace
 
 cudaError_t launch_lora_many(const LoraArgs& a, int num_sms, cudaStream_t stream) {
   auto* offsets = static_cast<int32_t*>(a.workspace);
   auto* slots = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(a.workspace) + align_up(sizeof(int32_t) * (a.L + 2)));
-  CUtensorMap amap, bmap;
-  if (!make_bf16_map(&amap, a.a, static_cast<long long>(a.L) * a.r, a.K, a.K, (a.r + 15) / 16 * 16) ||
-      !make_bf16_map(&bmap, a.b, static_cast<long long>(a.L) * a.N, a.r, a.r, kTile))
-    return cudaErrorInvalidValue;
   const cudaError_t e = launch_sort(SortArgs{a.index, a.M, 0, a.L, 1, kTile, offsets, slots, order_rows(a.M, a.L), nullptr}, stream);
   if (e != cudaSuccess) return e;
   const ManyPlan p = plan_many(a, num_sms);
   const Order order{offsets, slots};
   auto go = [&](auto out) {
     constexpr int kOut = decltype(out)::value;
-    if (!a.add) return launch<-1, kOut>(a, amap, bmap, order, p, stream);
-    return a.add_type == kTypeF32 ? launch<kTypeF32, kOut>(a, amap, bmap, order, p, stream)
-                                  : launch<kTypeBf16, kOut>(a, amap, bmap, order, p, stream);
+    if (!a.add) return launch<-1, kOut>(a, order, p, stream);
+    return a.add_type == kTypeF32 ? launch<kTypeF32, kOut>(a, order, p, stream)
+                                  : launch<kTypeBf16, kOut>(a, order, p, stream);
   };
   return a.out_type == kTypeF32 ? go(std::integral_constant<int, kTypeF32>{}) : go(std::integral_constant<int, kTypeBf16>{});
 }
