@@ -10,8 +10,8 @@
 //      to all CTAs, straight into the second product's operand;
 //   3. computes its share of the N columns: MMAs of 128 rows x 128 columns over the parts,
 //      one after another against the same tile of b[l], two accumulators in turn, taken out
-//      of tensor memory by eight warps that add the addends, which they have loaded half a
-//      tile ahead, and write the output.
+//      of tensor memory by eight warps that add the addends, which each thread has copied
+//      for itself to shared memory some pieces ahead, and write the output.
 // Two CTAs share an SM where the rank allows, so that one reads x while the other joins or
 // writes. Nothing but x, a, b, the addends and the output goes through memory, and each once
 // (a and b once for each tile, from L2). The operations are few, r of them for a byte at
@@ -26,6 +26,8 @@
 //     and the output move in 16- and 32-byte pieces, 64 or 128 bytes of a row to four
 //     lanes, without an exchange. (A row to a lane, 32 lines to an access: 4,000 cycles a
 //     tile; exchanges: 3,300.)
+//   - Addends that wait in registers wait for one another: a warp tells its loads under way
+//     apart by few marks, and three halves of a tile ahead took twice as long as one.
 //
 // Warps: 0..7 x, joining and output, 8 the copies of a and b, 9 the MMAs. All sums have a
 // fixed order.
@@ -49,7 +51,6 @@ constexpr int kTeam = 64, kTeams = 2;  // threads that copy a stage of x, by tur
 // teams and three stages overwrote stages in use, until waits ran out.)
 constexpr int kLeastStages = 3;
 static_assert(kTeams <= kLeastStages, "a parity is answered by the phase before the last");
-constexpr int kAhead = 6;          // halves of column tiles whose addends are asked into L2 ahead
 constexpr int kMaxStages = 6;
 constexpr int kHead = 2048;        // barriers, the tile's rows
 constexpr int kSmemMost = 227 * 1024, kSmemHalf = 113 * 1024;
@@ -61,6 +62,7 @@ struct ManyPlan {
   int rank16;       // r, up to a multiple of 16
   int stages, stage_bytes, smem;
   int b_stages;     // tiles of b under way
+  int deep;         // pieces of addends under way
   int tiles;        // at most
 };
 struct Order {
@@ -105,39 +107,43 @@ __device__ __forceinline__ int column_at(int c) { return 8 * ((c >> 1) & 3) + 2 
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
-__device__ __forceinline__ void st_cluster_v2(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+__device__ __forceinline__ void st_cluster_b4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   const uint4 v = ld_shared_v4(addr);
   return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-// Eight consecutive addends of a row as they are in memory; the output's of eight sums.
+// All but the last `left` groups of this thread's copies have landed.
+constexpr int kMaxDeep = 6;
+__device__ __forceinline__ void copies_left(int left) {
+  switch (left) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+  }
+}
+static_assert(kMaxDeep - 1 <= 5, "cases above");
+// Eight consecutive addends of a row, as a thread copied them (a row's bytes of all threads:
+// kAddBytes), and eight values of the output.
 template <int kAdd>
-struct Addends {
-  uint4 w[kAdd == kTypeF32 ? 2 : 1];
-  __device__ __forceinline__ void load(const LoraArgs& a, long long at) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(a.add) + at * (kAdd == kTypeF32 ? 4 : 2));
-    w[0] = p[0];
-    if constexpr (kAdd == kTypeF32) w[1] = p[1];
+constexpr int kAddBytes = kEpiThreads * 16 * (kAdd == kTypeF32 ? 2 : 1);
+template <int kAdd>
+__device__ __forceinline__ void load_addends(uint32_t at, float (&y)[8]) {
+  if constexpr (kAdd == kTypeF32) {
+    const float4 u = ld_shared_f4(at), v = ld_shared_f4(at + kEpiThreads * 16);
+    y[0] = u.x, y[1] = u.y, y[2] = u.z, y[3] = u.w, y[4] = v.x, y[5] = v.y, y[6] = v.z, y[7] = v.w;
+  } else {
+    const uint4 u = ld_shared_v4(at);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[2 * i] = __uint_as_float(w[i] << 16), y[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  __device__ __forceinline__ float operator[](int i) const {
-    if constexpr (kAdd == kTypeF32) {
-      const uint4 v = w[i >> 2];
-      return __uint_as_float((i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w);
-    } else {
-      const uint32_t v = (i >> 1) == 0 ? w[0].x : (i >> 1) == 1 ? w[0].y : (i >> 1) == 2 ? w[0].z : w[0].w;
-      return __uint_as_float(i & 1 ? v & 0xFFFF0000u : v << 16);
-    }
-  }
-};
-template <>
-struct Addends<-1> {
-  __device__ __forceinline__ void load(const LoraArgs&, long long) {}
-  __device__ __forceinline__ float operator[](int) const { return 0.f; }
-};
-
+}
 template <int kOut>
 __device__ __forceinline__ void store_cols(const LoraArgs& a, long long at, const float (&y)[8]) {
   if constexpr (kOut == kTypeF32) {
@@ -173,12 +179,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + 256);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + 260);
   int* row_of = reinterpret_cast<int*>(gbase + 1024);  // [128] the tile's rows, -1 behind the last
-  // arriving sums: [CTA][r / 4][row] of four; then the stages of x and a, and when those are
-  // done in their place the second product's operand (blocks of 128 rows x 64 columns) and
-  // tiles of b
-  const uint32_t sums_at = base + kHead, ring = sums_at + kTile * plan.rank16 * 4, parts_at = ring;
+  // Arriving sums: [CTA][r / 4][row] of four; then the stages of x and a. When those are done,
+  // at the end of their place the second product's operand (blocks of 128 rows x 64 columns),
+  // in front of it tiles of b; and when the sums are joined, up to there addends.
+  const uint32_t sums_at = base + kHead, ring = sums_at + kTile * plan.rank16 * 4, adds_at = sums_at;
   const int wide = plan.rank16 > kChunk ? 2 : 1;  // boxes of a row of b
-  const uint32_t b_ring = parts_at + (plan.parts * plan.rank16 + kChunk - 1) / kChunk * kBox;
+  const uint32_t parts_at = base + plan.smem - 1024 - (plan.parts * plan.rank16 + kChunk - 1) / kChunk * kBox;
+  const uint32_t b_ring = parts_at - plan.b_stages * wide * kBox;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int C = plan.ctas, rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -205,16 +212,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   const int l = *bucket;
   if (l < 0) return;  // (the whole cluster)
-  const int nt = (a.N + kTile - 1) / kTile, nper = (nt + C - 1) / C;
-  const int nt0 = min(nt, rank * nper), nt1 = min(nt, nt0 + nper);
+  // A CTA's share of the columns, of x in stages and of the output in tiles: every C-th, so
+  // that a row's neighbouring pieces are read and written at about the same time.
+  const int nt = (a.N + kTile - 1) / kTile, chunks = (a.K + kChunk - 1) / kChunk;
+  const int nn = nt > rank ? (nt - rank - 1) / C + 1 : 0, kn = chunks > rank ? (chunks - rank - 1) / C + 1 : 0;
+  auto tile_col = [&](int j) { return (rank + j * C) * kTile; };
+  auto chunk_col = [&](int i) { return (rank + i * C) * kChunk; };
   if (l == a.L) {  // rows without an adapter
     if (a.add == a.out) return;
-    const int n0 = nt0 * kTile, pieces = (min(a.N, nt1 * kTile) - n0) / 8;
     for (int i = warp; i < kTile; i += kThreads / 32) {
       const int m = row_of[i];
       if (m < 0) break;
-      for (int v = lane; v < pieces; v += 32) {
-        const long long at = static_cast<long long>(m) * a.N + n0 + 8 * v;
+      for (int v = 32 * rank + lane; v < a.N / 8; v += 32 * C) {
+        const long long at = static_cast<long long>(m) * a.N + 8 * v;
         float d[8];
         load8(a, at, d);
         store8(a, at, d);
@@ -233,9 +243,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int chunks = (a.K + kChunk - 1) / kChunk, cper = (chunks + C - 1) / C;
-  const int c0 = min(chunks, rank * cper), c1 = min(chunks, c0 + cper);
-  const int kn = c1 - c0, nn = nt1 - nt0;  // this CTA's stages of x, its column tiles
   auto slot_of = [&](int i) { return ring + (i % S) * plan.stage_bytes; };
   const int SB = plan.b_stages;
   auto b_slot_of = [&](int j) { return b_ring + (j % SB) * wide * kBox; };
@@ -244,13 +251,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   const uint16_t* b_from = a.b + static_cast<long long>(l) * a.N * a.r;
   auto copy_b = [&](int j) {
     if (!__all_sync(0xffffffffu, mbar_wait(bempty(j % SB), ((j / SB) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit))) return false;
-    const int n0 = (nt0 + j) * kTile;
-    for (int c = lane >> 3; c < kTile; c += 4) {
-      const int n = n0 + (c & ~31) + column_at(c & 31);
-      for (int h = 0; h < wide; ++h) {
-        const int k = h * kChunk + 8 * piece;
-        const bool in = n < a.N && k < a.r;
-        copy16(b_slot_of(j) + h * kBox + c * 128 + ((piece ^ (c & 7)) << 4), b_from + (in ? static_cast<long long>(n) * a.r + k : 0), in ? 16 : 0);
+    // lanes of 8 copy a row; row c = lane / 8 + 4 i of the operand, whose column is the sum of
+    // those of lane / 8 and 4 i
+    const int n0 = tile_col(j) + column_at(lane >> 3);
+    const uint32_t to = b_slot_of(j) + (lane >> 3) * 128;
+    for (int h = 0; h < wide; ++h) {
+      const int k = h * kChunk + 8 * piece;
+      const bool whole = tile_col(j) + kTile <= a.N;
+      const uint16_t* from = b_from + static_cast<long long>(n0) * a.r + k;
+      const uint32_t bytes = k < a.r ? 16 : 0;
+      if (bytes == 0) from = a.b;
+      const long long one = bytes ? a.r : 0;
+#pragma unroll 8
+      for (int i = 0; i < kTile / 4; ++i) {
+        const int on = (i >> 3) * 32 + column_at((i & 7) * 4);
+        const bool in = whole || n0 + on < a.N;
+        copy16(to + h * kBox + i * 512 + ((piece ^ ((lane >> 3) + 4 * (i & 1))) << 4), in ? from : a.b, in ? bytes : 0);
+        from += one * ((i & 7) == 7 ? 32 - column_at(28) : column_at((i & 7) * 4 + 4) - column_at((i & 7) * 4));
       }
     }
     copies_arrive(bfull(j % SB));
@@ -258,35 +275,32 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   int issued = 0;  // tiles of b
 
-  // the output of a joining lane: eight columns of four rows, of each half q of its warp's
-  // columns of a tile
+  // The output of a joining lane: eight columns of four rows of each half of its warp's
+  // columns of a tile. Piece s: rows 2 (s & 1) and 2 (s & 1) + 1 of half s / 2.
   long long row_at[4];  // -1: no row
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int m = row_of[(warp & 3) * 32 + 8 * i + (lane >> 2)];
     row_at[i] = m < 0 ? -1 : static_cast<long long>(m) * a.N;
   }
-  const int col0 = nt0 * kTile + (warp >> 2) * kCols + 8 * (lane & 3);
-  auto col_of = [&](int q) { return col0 + (q >> 1) * kTile + (q & 1) * 32; };
-  auto ask_addends = [&](int q) {
-    const int n = col_of(q);
-    if (kAdd >= 0 && q < 2 * nn && n < a.N)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row_at[i] >= 0) prefetch_l2(static_cast<const char*>(a.add) + (row_at[i] + n) * (kAdd == kTypeF32 ? 4 : 2));
-  };
+  const int col0 = (warp >> 2) * kCols + 8 * (lane & 3), pieces = 4 * nn;
+  auto col_of = [&](int s) { return col0 + tile_col(s >> 2) + (s >> 1 & 1) * 32; };
 
   // ---- 1. this CTA's columns of a[l] x
   bool ok = true;
   if (warp == kWarpCopy) {
-    const uint16_t* from = a.a + static_cast<long long>(l) * a.r * a.K + 8 * piece;
+    const uint16_t* from = a.a + (static_cast<long long>(l) * a.r + (lane >> 3)) * a.K + 8 * piece;
     for (int i = 0; i < kn && ok; ++i) {
       ok = __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
       if (!ok) break;
-      const int k = (c0 + i) * kChunk;
-      for (int row = lane >> 3; row < plan.rank16; row += 4) {
-        const bool in = row < a.r && k + 8 * piece < a.K;
-        copy16(slot_of(i) + kBox + row * 128 + ((piece ^ (row & 7)) << 4), in ? from + static_cast<long long>(row) * a.K + k : a.a, in ? 16 : 0);
+      const int k = chunk_col(i);
+      const bool in_row = k + 8 * piece < a.K;
+      const uint32_t to = slot_of(i) + kBox + (lane >> 3) * 128;
+      const uint16_t* p = from + k;
+#pragma unroll 4
+      for (int j = 0; j < plan.rank16 / 4; ++j, p += 4 * static_cast<long long>(a.K)) {
+        const bool in = (lane >> 3) + 4 * j < a.r && in_row;
+        copy16(to + j * 512 + ((piece ^ ((lane >> 3) + 4 * (j & 1))) << 4), in ? p : a.a, in ? 16 : 0);
       }
       copies_arrive(full(i % S));
     }
@@ -312,21 +326,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (leader) tc_commit(summed);
     __syncwarp();
   } else {
-    // the first column tiles' addends are asked into L2 meanwhile
-    for (int q = 0; q < kAhead; ++q) ask_addends(q);
-    // the rows' 16-byte pieces are swizzled as the MMA reads them
-    const int team = threadIdx.x / kTeam, first = threadIdx.x % kTeam >> 3;
-    for (int i = team; i < kn && team < kTeams; i += kTeams) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
-      if (!ok) break;
-      const int k = (c0 + i) * kChunk + 8 * piece;
+    // the first addends are asked into L2 meanwhile
+    if (kAdd >= 0)
+      for (int s = 0; s < min(pieces, plan.deep); ++s)
 #pragma unroll
-      for (int row = first, j = 0; j < kTile * 8 / kTeam; ++j, row += kTeam / 8) {
-        const int m = row_of[row];
-        const bool in = m >= 0 && k < a.K;
-        copy16(slot_of(i) + row * 128 + ((piece ^ (row & 7)) << 4), a.x + (in ? m * a.ldx + k : 0), in ? 16 : 0);
+        for (int i = 0; i < 2; ++i) {
+          const long long at = s & 1 ? row_at[2 + i] : row_at[i];
+          if (at >= 0 && col_of(s) < a.N) prefetch_l2(static_cast<const char*>(a.add) + (at + col_of(s)) * (kAdd == kTypeF32 ? 4 : 2));
+        }
+    // the rows' 16-byte pieces are swizzled as the MMA reads them
+    const int team = threadIdx.x / kTeam;
+    if (team < kTeams) {
+      constexpr int kEach = kTile * 8 / kTeam, kStep = kTeam / 8;  // rows of a thread, and from one to the next
+      const int first = threadIdx.x % kTeam >> 3;
+      const uint16_t* from[kEach];  // (in registers: a look-up between two copies holds up the second)
+      uint32_t rows = 0;
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const int m = row_of[first + j * kStep];
+        rows |= (m >= 0 ? 1u : 0u) << j;
+        from[j] = a.x + max(m, 0) * a.ldx + 8 * piece;
       }
-      copies_arrive(full(i % S));
+      for (int i = team; i < kn; i += kTeams) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(empty(i % S), ((i / S) & 1) ^ 1, abort_flag, status, kStatusTimeout, limit));
+        if (!ok) break;
+        const int k = chunk_col(i);
+        const bool in_row = k + 8 * piece < a.K;
+        const uint32_t to = slot_of(i) + first * 128 + ((piece ^ (first & 7)) << 4);
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          copy16(to + j * kStep * 128, in_row ? from[j] + k : a.x, in_row && (rows >> j & 1) ? 16 : 0);
+        copies_arrive(full(i % S));
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (test_never_wait) ok = __all_sync(0xffffffffu, mbar_wait(never, 0, abort_flag, status, kStatusTimeout, limit));
@@ -351,28 +382,31 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncwarp();
   cluster_sync();
   {
+    // a thread: eight columns of a row of this CTA's share
     const int share = kTile / C, quads = plan.rank16 / 4;
     const float scale = a.scale ? a.scale[l] : 1.f;
-    for (int i = threadIdx.x; i < share * quads; i += kThreads) {
-      const int q = i / share, row = rank * share + i % share;
-      float s[4] = {};
+    for (int i = threadIdx.x; i < share * quads / 2; i += kThreads) {
+      const int q = i / share, mine = i % share, row = rank * share + mine;
+      float s[8] = {};
       for (int c = 0; c < C; ++c) {
-        const float4 v = ld_shared_f4(sums_at + ((c * quads + q) * share + i % share) * 16);
-        s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w;
+        const uint32_t from = sums_at + ((c * quads + 2 * q) * share + mine) * 16;
+        const float4 u = ld_shared_f4(from), v = ld_shared_f4(from + share * 16);
+        s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w, s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] *= scale;
+      for (int j = 0; j < 8; ++j) s[j] *= scale;
       for (int p = 0; p < plan.parts; ++p) {
-        uint16_t h[4];
+        uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          h[j] = bf16_part(s[j]);
-          s[j] = isfinite(s[j]) ? s[j] - bf16_value(h[j]) : 0.f;
+          const uint16_t lo = bf16_part(s[2 * j]), hi = bf16_part(s[2 * j + 1]);
+          s[2 * j] = isfinite(s[2 * j]) ? s[2 * j] - bf16_value(lo) : 0.f;
+          s[2 * j + 1] = isfinite(s[2 * j + 1]) ? s[2 * j + 1] - bf16_value(hi) : 0.f;
+          w[j] = lo | static_cast<uint32_t>(hi) << 16;
         }
-        const int k = p * plan.rank16 + 4 * q;  // column of the operand, 8 bytes within its 16
-        const uint32_t at = parts_at + k / kChunk * kBox + row * 128 + ((((k % kChunk) >> 3) ^ (row & 7)) << 4) + (k & 4) * 2;
-        for (int c = 0; c < C; ++c)
-          st_cluster_v2(map_rank(at, c), h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+        const int k = p * plan.rank16 + 8 * q;  // column of the operand
+        const uint32_t at = parts_at + k / kChunk * kBox + row * 128 + ((((k % kChunk) >> 3) ^ (row & 7)) << 4);
+        for (int c = 0; c < C; ++c) st_cluster_b4(map_rank(at, c), w);
       }
     }
   }
@@ -429,44 +463,63 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncwarp();
   } else {
     const uint32_t src = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (warp >> 2) * kCols;
-    Addends<kAdd> next[4];
-    auto load = [&](int q) {
-      const int n = col_of(q);
-      if (q < 2 * nn && n < a.N)
+    const uint32_t mine = adds_at + threadIdx.x * 16;  // [piece][row][16 bytes][thread] of 16
+    auto copy_addends = [&](int s, int slot) {
+      if constexpr (kAdd >= 0) {
+        constexpr int kItem = kAdd == kTypeF32 ? 4 : 2;
+        const int n = col_of(s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (row_at[i] >= 0) next[i].load(a, row_at[i] + n);
+        for (int i = 0; i < 2; ++i) {
+          const long long at = s & 1 ? row_at[2 + i] : row_at[i];
+          const bool in = s < pieces && at >= 0 && n < a.N;
+          const char* from = static_cast<const char*>(a.add) + (in ? (at + n) * kItem : 0);
+#pragma unroll
+          for (int h = 0; h < kItem / 2; ++h)
+            copy16(mine + ((slot * 2 + i) * (kItem / 2) + h) * kEpiThreads * 16, from + 16 * h, in ? 16 : 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      }
     };
-    load(0);
-    for (int q = 0; q < 2 * nn; ++q) {
-      const int j = q >> 1, buf = j & 1, n = col_of(q);
-      if (!(q & 1)) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(buf), (j >> 1) & 1, abort_flag, status, kStatusTimeout, limit));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      uint32_t v[2][16];
-      tmem_ld_16x32(src + buf * kTile + (q & 1) * 32, v[0]);
-      tmem_ld_16x32(src + buf * kTile + (q & 1) * 32 + (16u << 16), v[1]);
-      ask_addends(q + kAhead);
-      Addends<kAdd> now[4];
+    const int deep = plan.deep;
+    for (int s = 0; s < deep; ++s) copy_addends(s, s);
+    int slot = 0;
+    for (int s0 = 0; s0 < pieces; s0 += 4) {
+      const int j = s0 >> 2, buf = j & 1;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(tfull(buf), (j >> 1) & 1, abort_flag, status, kStatusTimeout, limit));
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) now[i] = next[i];
-      load(q + 1);
-      tmem_ld_wait();
-      if (q & 1) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty(buf));
-      }
+      for (int u = 0; u < 4; ++u) {
+        const int s = s0 + u, n = col_of(s);
+        uint32_t v[16];
+        tmem_ld_16x32(src + buf * kTile + (u >> 1) * 32 + (static_cast<uint32_t>(16 * (u & 1)) << 16), v);
+        float y[2][8];
+        if constexpr (kAdd >= 0) {
+          copies_left(deep - 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {  // rows 8 i + lane / 4
-        float y[8];
+          for (int i = 0; i < 2; ++i) load_addends<kAdd>(mine + slot * 2 * kAddBytes<kAdd> + i * kAddBytes<kAdd>, y[i]);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v[i >> 1][4 * (k >> 1) + 2 * (i & 1) + (k & 1)]) + now[i][k];
-        if (row_at[i] >= 0 && n < a.N) store_cols<kOut>(a, row_at[i] + n, y);
+          for (int i = 0; i < 16; ++i) y[i >> 3][i & 7] = 0.f;
+        }
+        tmem_ld_wait();
+        if (u == 3) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tempty(buf));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // rows 8 (2 (u & 1) + i) + lane / 4
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[i][k] += __uint_as_float(v[4 * (k >> 1) + 2 * i + (k & 1)]);
+          const long long at = row_at[2 * (u & 1) + i];
+          if (at >= 0 && n < a.N) store_cols<kOut>(a, at + n, y[i]);
+        }
+        copy_addends(s + deep, slot);
+        if (++slot == deep) slot = 0;
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   __syncwarp();
   tc_fence_before();
@@ -496,9 +549,14 @@ ManyPlan plan_many(const LoraArgs& a, int num_sms) {
   int room = kSmemHalf - fixed;
   if (room < kLeastStages * p.stage_bytes || room < operand + b_tile) room = kSmemMost - fixed;
   p.stages = std::min(kMaxStages, room / p.stage_bytes);  // (five at the least where one CTA has the SM)
-  p.b_stages = room >= operand + 2 * b_tile ? 2 : 1;
-  p.smem = std::max(kSmemLeast, fixed + std::max(p.stages * p.stage_bytes, operand + p.b_stages * b_tile));
-  const int per_sm = p.smem <= kSmemHalf ? 2 : 1;
+  const bool half = room <= kSmemHalf - fixed;
+  const int piece = kEpiThreads * 32 * (a.add_type == kTypeF32 ? 2 : 1);
+  p.b_stages = room >= operand + 2 * b_tile && room + kTile * p.rank16 * 4 >= operand + 2 * b_tile + 2 * piece ? 2 : 1;
+  const int ring = std::max(p.stages * p.stage_bytes, operand + p.b_stages * b_tile);
+  p.smem = std::max(kSmemLeast, fixed + ring);
+  // (the sums' place and what the ring has left are at least a piece of addends: 8 KB, fp32 16)
+  p.deep = std::max(1, std::min(kMaxDeep, (p.smem - kHead - 1024 - operand - p.b_stages * b_tile) / piece));
+  const int per_sm = half ? 2 : 1;
   p.tiles = order_rows(a.M, a.L) / kTile;
   // CTAs to a tile: as many as leave the tiles that there will be about (half an extra one
   // for each adapter) in one wave
