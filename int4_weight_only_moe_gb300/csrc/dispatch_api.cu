@@ -164,7 +164,7 @@ bool lora_shape_ok(int M, int K, int N, int r, int L) {
 }  // namespace
 
 size_t moe_w4a16_lora_workspace_size(int M, int K, int N, int r, int L) {
-  return lora_shape_ok(M, K, N, r, L) ? lora_workspace_bytes(M, L) : 0;
+  return lora_shape_ok(M, K, N, r, L) ? lora_workspace_bytes(M, r, L) : 0;
 }
 
 int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const uint16_t* b, const float* scale,
@@ -181,7 +181,7 @@ int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const ui
     return bad("a pointer is not aligned to its type");
   if (add == out && add_type != out_type) return bad("add may be out only where they are of one type");
   if (misaligned(workspace, 256)) return bad("workspace must be 256-byte aligned");
-  const size_t need = lora_workspace_bytes(M, L);
+  const size_t need = lora_workspace_bytes(M, r, L);
   if (workspace && workspace_bytes < need)
     return report_error(MOE_W4A16_WORKSPACE_TOO_SMALL, "workspace too small (moe_w4a16_lora_workspace_size)");
   cudaError_t e;

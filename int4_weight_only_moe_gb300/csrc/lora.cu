@@ -7,8 +7,9 @@
 // Few rows (a decode step): one launch, in which a cluster of eight CTAs takes up to 16 rows
 // of one adapter. Each CTA sums an eighth of a[l] x's products, hands its part to all
 // eight, and computes an eighth of the outputs; nothing goes through memory in between.
-// The rows of an adapter are found by each cluster itself: row m's counts the rows in front
-// of m that have the same adapter, and goes on where that is a multiple of 16.
+// Each cluster finds its rows itself: it counts the rows of every adapter (up to 32 rows by
+// comparing lanes), 16 of which are a group, and takes the group of its own number (rows without an adapter are the last
+// adapter's). There are no more groups than L + 1 + M / 16, or than rows.
 // What bounds it is latency (index, then x and a, then the exchange, then b and the
 // addends, which are asked into L2 ahead) and from about 32 adapters on the reading of a and
 // b. The sums run on mma.sync: 16 rows fill its tile, and 2 r (K + N) operations a row are
@@ -18,6 +19,8 @@
 // (of 16 bits together; three, of 24, for an fp32 output), so that what is lost stays below
 // the rounding of the output. All sums have a fixed order: the same bits in every run.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "fp8_tma.cuh"
 #include "lora.cuh"
@@ -62,7 +65,12 @@ __global__ void __launch_bounds__(kThreads) lora_plain_kernel(const LoraArgs a) 
 
 constexpr int kCluster = 8, kWarps = kThreads / 32;
 constexpr int kGroup = 16;      // rows of a cluster
-constexpr int kFewRows = 512;   // rows of a call
+// Rows of a call up to which this kernel takes less time than the one for many rows: 512 rows,
+// 7,168 to 4,096 wide, 4 adapters of rank 32 or 64 14 and 18 us (there 29 and 32), 1,024 of 4 or
+// 48 27 (29) and 53 (60), of 32 37 (33); of rank 128, 512 rows 45 (37).
+constexpr int kFewRows = 768, kFewRowsWide = 384;
+int few_rows(int r) { return r <= 64 ? kFewRows : kFewRowsWide; }
+constexpr int kMaxAdapters = 1023;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -90,49 +98,98 @@ struct Few {
 // as long as both operands share it: a lane takes 16 consecutive bytes of a row, of which
 // the words 0, 1 make one MMA's elements (2t, 2t + 1, 2t + 8, 2t + 9) and 2, 3 the next's.
 template <int kTiles>
-__global__ void __launch_bounds__(kThreads) lora_few_kernel(const LoraArgs a, int parts) {
+__global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 1) lora_few_kernel(const LoraArgs a, int parts) {
   using F = Few<kTiles>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* warp_sums = reinterpret_cast<float*>(smem);                                       // [warps][16][kRank]
   float* arrived = warp_sums + kWarps * F::kSums;                                          // [CTAs][16][kRank]
   uint16_t* part_of = reinterpret_cast<uint16_t*>(arrived + kCluster * F::kSums);          // [parts][16][kRow]
   __shared__ int index_of[kFewRows];
+  __shared__ int count_of[kMaxAdapters + 1];
   __shared__ int row_of[kGroup];
-  __shared__ int rows_in;
+  __shared__ int group[3];  // adapter, rows of it in front of the group, rows
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int rank = static_cast<int>(cluster_rank());
-  const int m = blockIdx.x / kCluster;
-  pdl_wait();
-  for (int i = tid; i < a.M; i += kThreads) index_of[i] = a.index[i];
-  __syncthreads();
-  const int l = index_of[m];
+  const int want = blockIdx.x / kCluster;
+  if (a.M <= 32) {
+    // one row to a lane: the first of an adapter's rows, and every 16th on, begins a group
+    pdl_wait();
+    if (w == 0) {
+      const int i = lane < a.M ? a.index[lane] : 0;
+      const int mine = lane >= a.M ? -1 : static_cast<uint32_t>(i) < static_cast<uint32_t>(a.L) ? i : a.L;
+      const unsigned peers = __match_any_sync(0xffffffffu, mine), below = (1u << lane) - 1u;
+      const int before = __popc(peers & below);
+      const unsigned first = __ballot_sync(0xffffffffu, mine >= 0 && before % kGroup == 0);
+      const int from = __ffs(__ballot_sync(0xffffffffu, (first >> lane & 1) && __popc(first & below) == want)) - 1;
+      if (from < 0) {
+        if (lane == 0) group[2] = 0;
+      } else {
+        const int skip = __shfl_sync(0xffffffffu, before, from);
+        const bool in = peers >> from & 1 && before >= skip && before < skip + kGroup;
+        if (in) row_of[before - skip] = lane;
+        const unsigned all = __ballot_sync(0xffffffffu, in);
+        if (lane == from) group[0] = mine, group[2] = __popc(all);
+      }
+    }
+    __syncthreads();
+  } else {
+    for (int i = tid; i <= a.L; i += kThreads) count_of[i] = 0;
+    if (tid < 3) group[tid] = 0;
+    __syncthreads();
+    pdl_wait();
+    for (int i = tid; i < a.M; i += kThreads) {
+      const int l = a.index[i];
+      const int b = static_cast<uint32_t>(l) < static_cast<uint32_t>(a.L) ? l : a.L;
+      index_of[i] = b;
+      atomicAdd(&count_of[b], 1);
+    }
+    __syncthreads();
+    if (w == 0) {
+      int before = 0;  // groups of the adapters so far
+      for (int b0 = 0; b0 <= a.L && before <= want; b0 += 32) {
+        const int n = b0 + lane <= a.L ? count_of[b0 + lane] : 0, groups = (n + kGroup - 1) / kGroup;
+        int upto = groups;
+  #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += v;
+        }
+        const int first = before + upto - groups;
+        if (first <= want && want < first + groups) {
+          group[0] = b0 + lane;
+          group[1] = (want - first) * kGroup;
+          group[2] = min(kGroup, n - group[1]);
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+      }
+      __syncwarp();
+      const int l = group[0], skip = group[1], rows = group[2];
+      int found = 0;
+      for (int i0 = 0; i0 < a.M && found < skip + rows; i0 += 32) {
+        const unsigned same = __ballot_sync(0xffffffffu, i0 + lane < a.M && index_of[i0 + lane] == l);
+        const int at = found + __popc(same & ((1u << lane) - 1u)) - skip;
+        if ((same >> lane & 1) && at >= 0 && at < rows) row_of[at] = i0 + lane;
+        found += __popc(same);
+      }
+    }
+    __syncthreads();
+  }
+  const int l = group[0], rows = group[2];
+  if (rows == 0) return;  // (the same in the whole cluster, as all that returns here)
   // columns of the output that are this CTA's, in blocks of 32
   const int blocks = (a.N + 31) / 32, per = (blocks + kCluster - 1) / kCluster;
   const int block0 = rank * per, block1 = min(blocks, block0 + per);
-  if (static_cast<uint32_t>(l) >= static_cast<uint32_t>(a.L)) {  // (the same in the whole cluster, as all that returns here)
-    if (a.add != a.out)
-      for (int n = block0 * 32 + tid; n < min(a.N, block1 * 32); n += kThreads) {
-        const long long at = static_cast<long long>(m) * a.N + n;
-        put(a, at, addend(a, at));
-      }
+  if (l == a.L) {  // rows without an adapter
+    if (a.add == a.out) return;
+    const int n0 = block0 * 32, pieces = (min(a.N, block1 * 32) - n0) / 8;
+    for (int i = tid; i < rows * pieces; i += kThreads) {
+      const long long at = static_cast<long long>(row_of[i / pieces]) * a.N + n0 + 8 * (i % pieces);
+      float d[8];
+      load8(a, at, d);
+      store8(a, at, d);
+    }
     return;
   }
-  if (w == 0) {
-    int before = 0;
-    for (int i0 = 0; i0 < m; i0 += 32) before += __popc(__ballot_sync(0xffffffffu, i0 + lane < m && index_of[i0 + lane] == l));
-    int found = 0;
-    if (before % kGroup == 0)
-      for (int i0 = m; i0 < a.M && found < kGroup; i0 += 32) {
-        const unsigned same = __ballot_sync(0xffffffffu, i0 + lane < a.M && index_of[i0 + lane] == l);
-        const int at = found + __popc(same & ((1u << lane) - 1u));
-        if ((same >> lane & 1) && at < kGroup) row_of[at] = i0 + lane;
-        found += __popc(same);
-      }
-    if (lane == 0) rows_in = min(found, kGroup);
-  }
-  __syncthreads();
-  const int rows = rows_in;
-  if (rows == 0) return;
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (every CTA runs before another writes to it)
 
   const int g = lane >> 2, t = lane & 3;
@@ -157,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) lora_few_kernel(const LoraArgs a, in
     const uint16_t* x0 = a.x + static_cast<long long>(row_of[min(g, rows - 1)]) * a.ldx + 8 * t;
     const uint16_t* x1 = a.x + static_cast<long long>(row_of[min(g + 8, rows - 1)]) * a.ldx + 8 * t;
     const uint4 none = make_uint4(0, 0, 0, 0);
-    constexpr int kOnce = kTiles <= 4 ? 4 : 2;  // units under way
+    constexpr int kOnce = kTiles <= 2 ? 4 : kTiles <= 4 ? 2 : 1;  // units under way (more of them would cost a CTA)
     for (int u = u0 + w; u < u1; u += kOnce * kWarps) {
       uint4 xa[kOnce], xb[kOnce], y[kOnce][kTiles];
 #pragma unroll
@@ -189,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) lora_few_kernel(const LoraArgs a, in
   }
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  for (int i = tid; i < F::kSums / 4; i += kThreads) {
+  for (int i = tid; i < rows * F::kRank / 4; i += kThreads) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) {
@@ -202,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) lora_few_kernel(const LoraArgs a, in
   }
   cluster_sync();  // (the only one: afterwards a CTA reads its own shared memory alone)
   const float scale = a.scale ? a.scale[l] : 1.f;
-  for (int i = tid; i < F::kSums; i += kThreads) {
+  for (int i = tid; i < rows * F::kRank; i += kThreads) {
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < kCluster; ++c) s += arrived[c * F::kSums + i];
@@ -266,7 +323,7 @@ cudaError_t launch_few(const LoraArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (entry) entry->store(1);
   }
-  return launch_cluster(lora_few_kernel<kTiles>, dim3(static_cast<unsigned>(a.M) * kCluster), dim3(kThreads), Few<kTiles>::kSmem,
+  return launch_cluster(lora_few_kernel<kTiles>, dim3(static_cast<unsigned>(std::min(a.M, a.L + 1 + (a.M + kGroup - 1) / kGroup)) * kCluster), dim3(kThreads), Few<kTiles>::kSmem,
                         stream, kCluster, a, a.out_type == kTypeF32 ? 3 : 2);
 }
 
@@ -274,14 +331,14 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 
 }  // namespace
 
-size_t lora_workspace_bytes(int M, int L) { return M > kFewRows ? lora_many_workspace(M, L) : 0; }
+size_t lora_workspace_bytes(int M, int r, int L) { return M > few_rows(r) ? lora_many_workspace(M, L) : 0; }
 
 cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
   // 16-byte pieces of every row
   const bool whole = a.K % 8 == 0 && a.N % 8 == 0 && a.r % 8 == 0 && (a.M == 1 || a.ldx % 8 == 0) && aligned(a.x, 16) &&
                      aligned(a.a, 16) && aligned(a.b, 16) && aligned(a.add, 16) && aligned(a.out, 16);
-  if (whole && a.M > kFewRows) return launch_lora_many(a, num_sms, stream);
-  if (whole && a.M <= kFewRows) {
+  if (whole && a.M > few_rows(a.r)) return launch_lora_many(a, num_sms, stream);
+  if (whole) {
     if (a.r <= 16) return launch_few<2>(a, stream);
     if (a.r <= 32) return launch_few<4>(a, stream);
     if (a.r <= 64) return launch_few<8>(a, stream);

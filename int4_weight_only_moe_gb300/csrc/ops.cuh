@@ -170,7 +170,7 @@ struct LoraArgs {
   void* workspace;  // lora_workspace_bytes()
 };
 constexpr int kMaxRank = 128;
-size_t lora_workspace_bytes(int M, int L);
+size_t lora_workspace_bytes(int M, int r, int L);
 cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream);
 
 // Its kernel for many rows (lora_many.cu): rows of whole, aligned 16-byte pieces.
