@@ -91,8 +91,18 @@ int moe_w4a16_dispatch_sort_gather(const void* x, int type, long long row_stride
                                    int32_t* position, void* out, void* stream) {
   if (int rc = check_order(M, topk, E, block)) return rc;
   if (int rc = check_rows(x, type, row_stride, M, K, out)) return rc;
-  if (int rc = moe_w4a16_dispatch_sort(topk_ids, M, topk, expert_begin, E, block, offsets, slots, position, stream)) return rc;
-  return moe_w4a16_dispatch_gather(x, type, row_stride, offsets, slots, position, out, M, K, topk, E, block, stream);
+  if (expert_begin < 0) return bad("need expert_begin >= 0");
+  if (M == 0) return moe_w4a16_dispatch_sort(topk_ids, M, topk, expert_begin, E, block, offsets, slots, position, stream);
+  if (int rc = check_order_out(offsets, slots, position)) return rc;
+  if (!topk_ids || misaligned(topk_ids, 4)) return bad("topk_ids is null or not aligned to its type");
+  cudaError_t e;
+  const int sms = num_sms(&e);
+  if (e != cudaSuccess) return done(e);
+  const int rows = static_cast<int>(rows_of(M, topk, E, block));
+  const SortArgs o{topk_ids, M * topk, expert_begin, E, 0, block, offsets, slots, rows, position};
+  const GatherRowsArgs g{x, M > 1 ? row_stride * item(type) : 0, static_cast<long long>(K) * item(type), offsets, slots,
+                         position, out, M, topk, E, block, rows};
+  return done(launch_sort_gather(o, g, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_w4a16_combine(const void* y, int y_type, const float* weights, const int32_t* position, const void* add,

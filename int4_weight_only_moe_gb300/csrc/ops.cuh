@@ -113,6 +113,8 @@ struct GatherRowsArgs {
   int M, topk, E, block, capacity;
 };
 cudaError_t launch_gather(const GatherRowsArgs& a, int num_sms, cudaStream_t stream);
+// Both, in one launch for few slots.
+cudaError_t launch_sort_gather(const SortArgs& o, const GatherRowsArgs& a, int num_sms, cudaStream_t stream);
 
 // out[t] = sum_j weights[t, j] y[position[t, j]] (+ add[t])
 struct CombineArgs {
