@@ -41,20 +41,43 @@ def rows(M: int, topk: int, E: int, block: int = 1) -> int:
     return n
 
 
+@functools.lru_cache(maxsize=1024)
+def _block_of(M, topk, E, cap):
+    """The block of an order of ``cap`` rows; 0 where there is none."""
+    n = M * topk
+    block = 1 if not n or not E else (cap - n) // min(E, n) + 1
+    return block if block > 0 and cap == _order_rows(M, topk, E, block) else 0
+
+
 def _parts(order, dev):
     """(addresses of the order's tensors, M, topk, E, rows, block)"""
     offsets, slots, position = order
-    if offsets.dim() != 1 or slots.dim() != 1 or position.dim() != 2 or not len(offsets):
-        raise ValueError("order: expected offsets [E + 1], slots [rows] and position [M, topk]")
-    M, topk = position.shape
-    E, n, cap = len(offsets) - 1, M * topk, len(slots)
-    block = 1 if not n or not E else (cap - n) // min(E, n) + 1
-    if cap != rows(M, topk, E, block):
+    try:
+        (E,), (cap,), (M, topk) = offsets.shape, slots.shape, position.shape
+    except ValueError:
+        raise ValueError("order: expected offsets [E + 1], slots [rows] and position [M, topk]") from None
+    E -= 1
+    block = _block_of(M, topk, E, cap)
+    if not block:
         raise ValueError(f"order: {cap} rows for {M} tokens of {topk} choices and {E} experts")
-    at = (_dense(offsets, torch.int32, (E + 1,), "order.offsets", dev),
-          _dense(slots, torch.int32, (cap,), "order.slots", dev),
-          _dense(position, torch.int32, (M, topk), "order.position", dev))
+    at = (_int32(offsets, "order.offsets", dev), _int32(slots, "order.slots", dev), _int32(position, "order.position", dev))
     return at, M, topk, E, cap, block
+
+
+def _int32(t, name, dev):
+    """Address of a contiguous int32 tensor of any shape on device ``dev``."""
+    if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous():
+        return _dense(t, torch.int32, t.shape, name, dev)
+    return t.data_ptr()
+
+
+def _matrix(t, name):
+    """(rows, columns, device) of a contiguous bf16 or fp32 matrix on the current device."""
+    if t.dtype not in _FLOATS or not t.is_contiguous() or t.dim() != 2:
+        _rows(t, name, _FLOATS)
+        raise ValueError(f"{name} must be contiguous")
+    rows, cols = t.shape
+    return rows, cols, _device(t, name)
 
 
 def _order_for(topk_ids, E, block, expert_range, order, dev, stream):
@@ -122,17 +145,14 @@ def sort_gather(x, topk_ids, E, block=1, expert_range=None, out=None, order=None
 
 
 def _combine(y, weights, order, add, out, out_dtype, stream):
-    R, K, stride = _rows(y, "y", _FLOATS)
-    if stride != K:
-        raise ValueError("y must be contiguous")
-    dev = _device(y, "y")
-    position = order[2]
+    R, K, dev = _matrix(y, "y")
+    _, slots, position = order
     if position.dim() != 2:
         raise ValueError(f"order.position: shape {tuple(position.shape)}, expected two dimensions")
     M, topk = position.shape
-    at = _dense(position, torch.int32, (M, topk), "order.position", dev)
-    if R != len(order[1]):
-        raise ValueError(f"y: {R} rows, expected the order's {len(order[1])}")
+    at = _int32(position, "order.position", dev)
+    if R != slots.shape[0]:
+        raise ValueError(f"y: {R} rows, expected the order's {slots.shape[0]}")
     w = 0 if weights is None else _dense(weights, torch.float32, (M, topk), "weights", dev)
     if out is None:
         out = _new((M, K), out_dtype or y.dtype, y.device, stream)
@@ -161,10 +181,7 @@ def combine_backward(dout, y, weights, order, dy=None, dweights=None, stream=Non
     """Gradient of ``combine`` for ``dout`` [M, K]: ``(dy [rows, K] of y's type, dweights fp32
     [M, topk])``. Rows of ``dy`` that fill up an expert's are 0, those behind the last
     expert's are left as they were. ``add`` has the gradient ``dout`` itself."""
-    M, K, stride = _rows(dout, "dout", _FLOATS)
-    if stride != K:
-        raise ValueError("dout must be contiguous")
-    dev = _device(dout, "dout")
+    M, K, dev = _matrix(dout, "dout")
     at, m, topk, E, cap, block = _parts(order, dev)
     if m != M:
         raise ValueError(f"order: of {m} tokens, dout has {M}")
