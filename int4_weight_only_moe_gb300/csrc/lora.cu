@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
     float s = 0.f;
 #pragma unroll
     for (int c = 0; c < kCluster; ++c) s += arrived[c * F::kSums + i];
-    s *= scale;
+    s = i % F::kRank < a.r ? s * scale : 0.f;  // (an infinite x times the zeros behind r)
     const int at = i / F::kRank * F::kRow + i % F::kRank;
     for (int p = 0; p < parts; ++p) {
       const uint16_t h = bf16_part(s);

@@ -54,7 +54,9 @@ static_assert(kTeams <= kLeastStages, "a parity is answered by the phase before 
 constexpr int kMaxStages = 6;
 constexpr int kHead = 2048;        // barriers, the tile's rows
 constexpr int kSmemMost = 227 * 1024, kSmemHalf = 113 * 1024;
-constexpr int kSmemLeast = 77 * 1024;  // (two CTAs to an SM at most: they share its tensor memory)
+// (Two CTAs to an SM at most, and beside them none of another kernel that takes tensor memory:
+// CTAs of a cluster wait for one another with their part of it in hand.)
+constexpr int kSmemLeast = 96 * 1024;
 
 struct ManyPlan {
   int ctas;         // to a tile
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w, s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] *= scale;
+      for (int j = 0; j < 8; ++j) s[j] = 8 * q < a.r ? s[j] * scale : 0.f;  // (infinite x times the zeros behind r)
       for (int p = 0; p < plan.parts; ++p) {
         uint32_t w[4];
 #pragma unroll

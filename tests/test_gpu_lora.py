@@ -226,3 +226,14 @@ def test_a_wait_that_gives_up_is_reported():
         pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_WAIT_LIMIT_US, 0)
         pkg.moe_w4a16_fp8_set_option(pkg.FP8_OPT_TEST_WAIT_NEVER_COMPLETES, 0)
     assert torch.equal(lora.apply(x, a, b, dev(index), add=add), want) and fp8.status() == 0
+
+
+@pytest.mark.parametrize("M", [5, 900])
+@pytest.mark.parametrize("r,K,N", [(8, 256, 128), (24, 264, 136), (16, 256, 128), (3, 33, 20)])
+def test_an_infinite_sum_is_infinite(M, r, K, N):
+    # positive factors: what the definition makes infinite is +infinity, not NaN
+    x, a, b, _ = problem(M, K, N, r, 2)
+    x, a, b = x.abs() + 0.25, a.abs() + 0.25, b.abs() + 0.25
+    x[1, K - 1] = float("inf")
+    got = lora.apply(x, a, b, torch.zeros(M, device="cuda", dtype=torch.int32), add=normal(M, N, seed=1))
+    assert (got[1] == float("inf")).all() and got[0].isfinite().all() and got[2:].isfinite().all()
