@@ -415,17 +415,23 @@ __device__ __forceinline__ const T* at(const void* p, long long row, long long K
   return static_cast<const T*>(p) + row * K + k;
 }
 
-// `f` with the choices j0 .. j0 + C - 1 of a token, in groups of 8, 4, 2 and 1: a group's
-// loads are all under way at once, none behind a condition. (8,192 tokens of 8 choices,
-// 7,168 wide: 152 us; 501 with a condition to each load, behind which the conversion of its
-// values waited before the next load began.)
+// `f` with the choices j0 .. j0 + C - 1 of a token, eight at a time and then what is left: a
+// group's loads are all under way at once, none behind a condition. (8,192 tokens of 8
+// choices, 7,168 wide: 152 us; 501 with a condition to each load, behind which the
+// conversion of its values waited before the next load began.)
 template <typename F>
 __device__ __forceinline__ void by_groups(int topk, F&& f) {
   int j = 0;
   for (; j + 8 <= topk; j += 8) f(std::integral_constant<int, 8>{}, j);
-  if (topk & 4) f(std::integral_constant<int, 4>{}, j), j += 4;
-  if (topk & 2) f(std::integral_constant<int, 2>{}, j), j += 2;
-  if (topk & 1) f(std::integral_constant<int, 1>{}, j);
+  switch (topk - j) {
+    case 7: f(std::integral_constant<int, 7>{}, j); break;
+    case 6: f(std::integral_constant<int, 6>{}, j); break;
+    case 5: f(std::integral_constant<int, 5>{}, j); break;
+    case 4: f(std::integral_constant<int, 4>{}, j); break;
+    case 3: f(std::integral_constant<int, 3>{}, j); break;
+    case 2: f(std::integral_constant<int, 2>{}, j); break;
+    case 1: f(std::integral_constant<int, 1>{}, j); break;
+  }
 }
 
 // out[t] = sum_j w y[row of j] (+ add[t]); `parts` CTAs share a row. A choice without a row
@@ -475,7 +481,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs 
 // One CTA to a token: each thread keeps its own part of the topk sums of products, which
 // the CTA joins at the end. Behind the tokens' CTAs those of the rows that fill up.
 template <typename Tg, typename Ty, int n>
-__global__ void __launch_bounds__(kRowThreads) combine_backward_kernel(const CombineBackwardArgs a, int fill) {
+__global__ void __launch_bounds__(kRowThreads, 2) combine_backward_kernel(const CombineBackwardArgs a, int fill) {
   __shared__ int row_of[kMaxTopk];
   __shared__ float weight_of[kMaxTopk];
   __shared__ float part_of[kRowWarps][kMaxTopk];
