@@ -130,6 +130,10 @@ __device__ __forceinline__ void copies_left(int left) {
   }
 }
 static_assert(kMaxDeep - 1 <= 5, "cases above");
+// The two halves of cluster_sync().
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Eight consecutive addends of a row, as a thread copied them (a row's bytes of all threads:
 // kAddBytes), and eight values of the output.
 template <int kAdd>
@@ -241,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // (every CTA runs before another writes to it)
   tc_fence_after();
+  cluster_arrive();  // (every CTA runs before another writes to it: waited for in front of that)
   const uint32_t tmem = *tmem_slot;
 
   auto slot_of = [&](int i) { return ring + (i % S) * plan.stage_bytes; };
@@ -308,6 +312,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // (the stages' place is free when all of their MMAs are done)
     ok = ok && __all_sync(0xffffffffu, mbar_wait(summed, 0, abort_flag, status, kStatusTimeout, limit));
+    cluster_wait();
+    cluster_arrive();  // (the join goes on without this warp, which has tiles of b to copy)
     for (; ok && issued < min(nn, SB); ++issued) ok = copy_b(issued);
   } else if (warp == kWarpMma) {
     const uint32_t idesc = idesc_bf16_f32(kTile, plan.rank16);
@@ -327,6 +333,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (leader) tc_commit(summed);
     __syncwarp();
+    cluster_wait();
+    cluster_arrive();
   } else {
     // the first addends are asked into L2 meanwhile
     if (kAdd >= 0)
@@ -365,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (test_never_wait) ok = __all_sync(0xffffffffu, mbar_wait(never, 0, abort_flag, status, kStatusTimeout, limit));
     ok = ok && __all_sync(0xffffffffu, mbar_wait(summed, 0, abort_flag, status, kStatusTimeout, limit));
     tc_fence_after();
+    cluster_wait();
     // ---- 2. to the row's CTA
     const int row = (warp & 3) * 32 + lane, share = kTile / C;
     const uint32_t to = map_rank(sums_at + (rank * (plan.rank16 / 4) * share + row % share) * 16, row / share);
@@ -380,14 +389,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                                 __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
     }
     tc_fence_before();
+    __syncwarp();
+    cluster_arrive();
   }
   __syncwarp();
-  cluster_sync();
-  {
+  cluster_wait();
+  if (warp < kEpiWarps) {
     // a thread: eight columns of a row of this CTA's share
     const int share = kTile / C, quads = plan.rank16 / 4;
     const float scale = a.scale ? a.scale[l] : 1.f;
-    for (int i = threadIdx.x; i < share * quads / 2; i += kThreads) {
+    for (int i = threadIdx.x; i < share * quads / 2; i += kEpiThreads) {
       const int q = i / share, mine = i % share, row = rank * share + mine;
       float s[8] = {};
       for (int c = 0; c < C; ++c) {
