@@ -296,13 +296,13 @@ int moe_w4a16_fp8_matmul(const uint8_t* a, long long lda, const float* a_s, cons
                          const float* b_s, const uint16_t* add, void* out, int out_type, int M, int N, int K,
                          void* stream);
 
-/* Status of the 8-bit products that ran on the current device since the last call of
- * this function: 0, or MOE_W4A16_STATUS_TIMEOUT when a pipeline wait gave up (the output
+/* Status of the 8-bit products and of the low-rank adapters (moe_w4a16_lora) that ran on the
+ * current device since the last call of this function: 0, or MOE_W4A16_STATUS_TIMEOUT when a pipeline wait gave up (the output
  * of that product is invalid). Clears it. Synchronises `stream`; products on other
  * streams count once they have finished. */
 int moe_w4a16_fp8_status(int32_t* status, void* stream);
 
-/* Settings of the 8-bit products' pipeline waits, for the whole process; they hold for
+/* Settings of the same kernels' pipeline waits, for the whole process; they hold for
  * calls that begin after this one returns.
  *   MOE_W4A16_FP8_OPT_WAIT_LIMIT_US             as MOE_W4A16_OPT_WAIT_LIMIT_US
  *   MOE_W4A16_FP8_OPT_TEST_WAIT_NEVER_COMPLETES as MOE_W4A16_OPT_TEST_WAIT_NEVER_COMPLETES */
@@ -359,7 +359,7 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
  *   out  [rows, K] of the same type
  * K <= 2^22. Its gradient is moe_w4a16_combine without weights. One launch.
  *
- * sort_gather: both, at most two launches.
+ * sort_gather: both, in one launch up to 1,024 choices, two above.
  *
  * combine: out[t] = sum_j weights[t, j] y[position[t, j]] (+ add[t]), summed in fp32 in the
  * order of j, the addend last, rounded once. Positions outside [0, rows) count nothing: a
@@ -423,9 +423,17 @@ int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, i
  *   workspace  >= moe_w4a16_lora_workspace_size(M, K, N, r, L) bytes (0 for sizes that are
  *          not supported, and where none is needed), 256-byte aligned; holds nothing between
  *          calls. NULL: as in moe_w4a16_shared_expert
+ * Both products' sums are fp32. Between them the first one's are split into bf16 parts of
+ * 16 bits together (24 for an fp32 output), so that an infinite or NaN value of b may make
+ * NaN where the formula gives infinity; rows of other adapters, and without one, are not
+ * affected by such values.
  * 1 <= r <= 128 (a larger rank is two adapters, one call after the other), 1 <= L <= 1023, M
- * up to 2^29, K and N up to 2^22. M == 0 is a no-op. No host synchronisation; the same
- * result in every run. */
+ * up to 2^29, K and N up to 2^22. One launch up to 768 rows (384 for r > 64), two above.
+ * Rows of x, a, add or out that are not whole 16-byte pieces (K, N or ldx no multiple of 8,
+ * other addresses), and r that is no multiple of 4 (of 8 above those rows), take a slower
+ * form, one launch for each 768 (384) rows. M == 0 is a no-op. No host synchronisation; the
+ * same result in every run. A pipeline wait that gives up is reported by
+ * moe_w4a16_fp8_status. */
 size_t moe_w4a16_lora_workspace_size(int M, int K, int N, int r, int L);
 int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const uint16_t* b, const float* scale,
                    const int32_t* index, const void* add, int add_type, void* out, int out_type, int M, int K, int N,

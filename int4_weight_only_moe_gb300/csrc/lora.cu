@@ -4,7 +4,7 @@
 //
 // and out[m] = add[m] for a row without an adapter.
 //
-// Few rows (a decode step): one launch, in which a cluster of eight CTAs takes up to 16 rows
+// Few rows (a decode step), and any shape and alignment: one launch, in which a cluster of eight CTAs takes up to 16 rows
 // of one adapter. Each CTA sums an eighth of a[l] x's products, hands its part to all
 // eight, and computes an eighth of the outputs; nothing goes through memory in between.
 // Each cluster finds its rows itself: it counts the rows of every adapter (up to 32 rows by
@@ -14,6 +14,10 @@
 // addends, which are asked into L2 ahead) and from about 32 adapters on the reading of a and
 // b. The sums run on mma.sync: 16 rows fill its tile, and 2 r (K + N) operations a row are
 // far below what it can do.
+//
+// Rows that are not whole, aligned pieces of 16 bytes (8 of b) are read and written value by
+// value, many of them 768 rows to a launch: 2,000 rows of 7,168 x 4,090 take 0.2 ms, where
+// 4,096 columns take 34 us.
 //
 // The first product's sums stay 32 bits: they enter the second product as two bf16 parts
 // (of 16 bits together; three, of 24, for an fp32 output), so that what is lost stays below
@@ -29,39 +33,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-
-// Any shape and alignment: one CTA to a row, everything in fp32 on the CUDA cores.
-__global__ void __launch_bounds__(kThreads) lora_plain_kernel(const LoraArgs a) {
-  __shared__ float v[kMaxRank];
-  pdl_wait();
-  const long long m = blockIdx.x;
-  const int l = a.index[m], lane = threadIdx.x & 31;
-  const bool has = static_cast<uint32_t>(l) < static_cast<uint32_t>(a.L);
-  if (!has && a.add == a.out) return;
-  if (has) {
-    const uint16_t* x = a.x + m * a.ldx;
-    const float scale = a.scale ? a.scale[l] : 1.f;
-    for (int i = threadIdx.x / 32; i < a.r; i += kThreads / 32) {
-      const uint16_t* w = a.a + (static_cast<long long>(l) * a.r + i) * a.K;
-      float sum = 0.f;
-      for (int k = lane; k < a.K; k += 32) sum = fmaf(bf16_value(x[k]), bf16_value(w[k]), sum);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) v[i] = sum * scale;
-    }
-    __syncthreads();
-  }
-  for (int n = threadIdx.x; n < a.N; n += kThreads) {
-    float sum = 0.f;
-    if (has) {
-      const uint16_t* w = a.b + (static_cast<long long>(l) * a.N + n) * a.r;
-      for (int i = 0; i < a.r; ++i) sum = fmaf(v[i], bf16_value(w[i]), sum);
-    }
-    put(a, m * a.N + n, sum + addend(a, m * a.N + n));
-  }
-}
-
-// -------------------------------------------------------------------------------- few rows
 
 constexpr int kCluster = 8, kWarps = kThreads / 32;
 constexpr int kGroup = 16;      // rows of a cluster
@@ -83,6 +54,53 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
 }
 
+// Eight (four) consecutive bf16 values of which `left` are in the row (a whole piece of them, or
+// none, where rows are whole pieces), zeros behind them.
+template <bool kWhole>
+__device__ __forceinline__ uint4 bf16x8(const uint16_t* p, int left) {
+  if constexpr (kWhole) {
+    return left > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = (2 * i < left ? p[2 * i] : 0u) | (2 * i + 1 < left ? static_cast<uint32_t>(p[2 * i + 1]) << 16 : 0u);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+template <bool kWhole>
+__device__ __forceinline__ uint2 bf16x4(const uint16_t* p, int left) {
+  if constexpr (kWhole) {
+    return left > 0 ? *reinterpret_cast<const uint2*>(p) : make_uint2(0, 0);
+  } else {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = (2 * i < left ? p[2 * i] : 0u) | (2 * i + 1 < left ? static_cast<uint32_t>(p[2 * i + 1]) << 16 : 0u);
+    return make_uint2(w[0], w[1]);
+  }
+}
+// Eight addends, and outputs, of which `left` are in the row.
+template <bool kWhole>
+__device__ __forceinline__ void load_eight(const LoraArgs& a, long long at, int left, float (&d)[8]) {
+  if constexpr (kWhole) {
+    load8(a, at, d);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = i < left ? addend(a, at + i) : 0.f;
+  }
+}
+template <bool kWhole>
+__device__ __forceinline__ void store_eight(const LoraArgs& a, long long at, int left, const float (&d)[8]) {
+  if constexpr (kWhole) {
+    store8(a, at, d);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) put(a, at + i, d[i]);
+  }
+}
+
 // Shared memory of the few-row kernel for ranks up to 8 * kTiles: the warps' sums, the
 // CTAs' sums as they arrive from the cluster, and the parts of the sum, rows padded by 8
 // values against bank conflicts.
@@ -97,7 +115,8 @@ struct Few {
 // Sums of 16 rows and up to 8 kTiles ranks. The order of the reduction's elements is free
 // as long as both operands share it: a lane takes 16 consecutive bytes of a row, of which
 // the words 0, 1 make one MMA's elements (2t, 2t + 1, 2t + 8, 2t + 9) and 2, 3 the next's.
-template <int kTiles>
+// kWhole: rows of whole, aligned pieces.
+template <int kTiles, bool kWhole>
 __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 1) lora_few_kernel(const LoraArgs a, int parts) {
   using F = Few<kTiles>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -181,12 +200,13 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
   const int block0 = rank * per, block1 = min(blocks, block0 + per);
   if (l == a.L) {  // rows without an adapter
     if (a.add == a.out) return;
-    const int n0 = block0 * 32, pieces = (min(a.N, block1 * 32) - n0) / 8;
+    const int n0 = block0 * 32, pieces = (min(a.N, block1 * 32) - n0 + 7) / 8;
     for (int i = tid; i < rows * pieces; i += kThreads) {
-      const long long at = static_cast<long long>(row_of[i / pieces]) * a.N + n0 + 8 * (i % pieces);
+      const int n = n0 + 8 * (i % pieces);
+      const long long at = static_cast<long long>(row_of[i / pieces]) * a.N + n;
       float d[8];
-      load8(a, at, d);
-      store8(a, at, d);
+      load_eight<kWhole>(a, at, a.N - n, d);
+      store_eight<kWhole>(a, at, a.N - n, d);
     }
     return;
   }
@@ -213,19 +233,18 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
     const int u0 = rank * each, u1 = min(units, u0 + each);
     const uint16_t* x0 = a.x + static_cast<long long>(row_of[min(g, rows - 1)]) * a.ldx + 8 * t;
     const uint16_t* x1 = a.x + static_cast<long long>(row_of[min(g + 8, rows - 1)]) * a.ldx + 8 * t;
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    constexpr int kOnce = kTiles <= 2 ? 4 : kTiles <= 4 ? 2 : 1;  // units under way (more of them would cost a CTA)
+    constexpr int kOnce = !kWhole ? 1 : kTiles <= 2 ? 4 : kTiles <= 4 ? 2 : 1;  // units under way (more of them would cost a CTA)
     for (int u = u0 + w; u < u1; u += kOnce * kWarps) {
       uint4 xa[kOnce], xb[kOnce], y[kOnce][kTiles];
 #pragma unroll
       for (int i = 0; i < kOnce; ++i) {
         const int k = (u + i * kWarps) * 32;
-        const bool in = u + i * kWarps < u1 && k + 8 * t < a.K;
-        xa[i] = in && g < rows ? *reinterpret_cast<const uint4*>(x0 + k) : none;
-        xb[i] = in && g + 8 < rows ? *reinterpret_cast<const uint4*>(x1 + k) : none;
+        const int left = u + i * kWarps < u1 ? a.K - k - 8 * t : 0;
+        xa[i] = bf16x8<kWhole>(x0 + k, g < rows ? left : 0);
+        xb[i] = bf16x8<kWhole>(x1 + k, g + 8 < rows ? left : 0);
 #pragma unroll
         for (int j = 0; j < kTiles; ++j)
-          y[i][j] = in && 8 * j + g < a.r ? *reinterpret_cast<const uint4*>(A + static_cast<long long>(8 * j + g) * a.K + k + 8 * t) : none;
+          y[i][j] = bf16x8<kWhole>(A + static_cast<long long>(8 * j + g) * a.K + k + 8 * t, 8 * j + g < a.r ? left : 0);
       }
 #pragma unroll
       for (int i = 0; i < kOnce; ++i)
@@ -279,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
     float d0[8], d1[8];  // addends of rows g and g + 8
     const long long at0 = static_cast<long long>(row_of[min(g, rows - 1)]) * a.N + n;
     const long long at1 = static_cast<long long>(row_of[min(g + 8, rows - 1)]) * a.N + n;
-    load8(a, live ? at0 : 0, d0);
-    load8(a, live ? at1 : 0, d1);
+    load_eight<kWhole>(a, live ? at0 : 0, live ? a.N - n : 0, d0);
+    load_eight<kWhole>(a, live ? at1 : 0, live ? a.N - n : 0, d1);
     float acc[4][4] = {};
     uint2 y[4][kTiles / 2];
 #pragma unroll
@@ -288,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int row = n0 + 8 * (g >> 1) + 2 * j + (g & 1), i = 16 * s + 4 * t;
-        y[j][s] = row < a.N && i < a.r ? *reinterpret_cast<const uint2*>(B + static_cast<long long>(row) * a.r + i) : make_uint2(0, 0);
+        y[j][s] = bf16x4<kWhole>(B + static_cast<long long>(row) * a.r + i, row < a.N ? a.r - i : 0);
       }
     for (int p = parts - 1; p >= 0; --p) {  // (the small parts first)
       const uint16_t* v = part_of + p * kGroup * F::kRow;
@@ -306,12 +325,12 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
       d0[2 * j] += acc[j][0], d0[2 * j + 1] += acc[j][1];
       d1[2 * j] += acc[j][2], d1[2 * j + 1] += acc[j][3];
     }
-    if (g < rows) store8(a, at0, d0);
-    if (g + 8 < rows) store8(a, at1, d1);
+    if (g < rows) store_eight<kWhole>(a, at0, a.N - n, d0);
+    if (g + 8 < rows) store_eight<kWhole>(a, at1, a.N - n, d1);
   }
 }
 
-template <int kTiles>
+template <int kTiles, bool kWhole>
 cudaError_t launch_few(const LoraArgs& a, cudaStream_t stream) {
   static PerDevice<int> ready;
   int dev = 0;
@@ -319,12 +338,21 @@ cudaError_t launch_few(const LoraArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   std::atomic<int>* entry = ready.of(dev);
   if (!entry || !entry->load()) {
-    e = cudaFuncSetAttribute(lora_few_kernel<kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<kTiles>::kSmem);
+    e = cudaFuncSetAttribute(lora_few_kernel<kTiles, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<kTiles>::kSmem);
     if (e != cudaSuccess) return e;
     if (entry) entry->store(1);
   }
-  return launch_cluster(lora_few_kernel<kTiles>, dim3(static_cast<unsigned>(std::min(a.M, a.L + 1 + (a.M + kGroup - 1) / kGroup)) * kCluster), dim3(kThreads), Few<kTiles>::kSmem,
-                        stream, kCluster, a, a.out_type == kTypeF32 ? 3 : 2);
+  const int groups = std::min(a.M, a.L + 1 + (a.M + kGroup - 1) / kGroup);
+  return launch_cluster(lora_few_kernel<kTiles, kWhole>, dim3(static_cast<unsigned>(groups) * kCluster), dim3(kThreads),
+                        Few<kTiles>::kSmem, stream, kCluster, a, a.out_type == kTypeF32 ? 3 : 2);
+}
+
+template <bool kWhole>
+cudaError_t launch_rank(const LoraArgs& a, cudaStream_t stream) {
+  if (a.r <= 16) return launch_few<2, kWhole>(a, stream);
+  if (a.r <= 32) return launch_few<4, kWhole>(a, stream);
+  if (a.r <= 64) return launch_few<8, kWhole>(a, stream);
+  return launch_few<16, kWhole>(a, stream);
 }
 
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
@@ -333,18 +361,25 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 
 size_t lora_workspace_bytes(int M, int r, int L) { return M > few_rows(r) ? lora_many_workspace(M, L) : 0; }
 
-cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream) {
-  // 16-byte pieces of every row
-  const bool whole = a.K % 8 == 0 && a.N % 8 == 0 && a.r % 8 == 0 && (a.M == 1 || a.ldx % 8 == 0) && aligned(a.x, 16) &&
-                     aligned(a.a, 16) && aligned(a.b, 16) && aligned(a.add, 16) && aligned(a.out, 16);
-  if (whole && a.M > few_rows(a.r)) return launch_lora_many(a, num_sms, stream);
-  if (whole) {
-    if (a.r <= 16) return launch_few<2>(a, stream);
-    if (a.r <= 32) return launch_few<4>(a, stream);
-    if (a.r <= 64) return launch_few<8>(a, stream);
-    return launch_few<16>(a, stream);
+cudaError_t launch_lora(const LoraArgs& args, int num_sms, cudaStream_t stream) {
+  LoraArgs a = args;
+  // 16-byte pieces of every row; for few rows 8 of b's will do
+  const bool pieces = a.K % 8 == 0 && a.N % 8 == 0 && (a.M == 1 || a.ldx % 8 == 0) && aligned(a.x, 16) && aligned(a.a, 16) &&
+                      aligned(a.b, 16) && aligned(a.add, 16) && aligned(a.out, 16);
+  const int most = few_rows(a.r);
+  if (a.M > most && pieces && a.r % 8 == 0) return launch_lora_many(a, num_sms, stream);
+  const bool whole = pieces && a.r % 4 == 0;
+  const long long add_row = a.add_type == kTypeF32 ? 4LL * a.N : 2LL * a.N, out_row = a.out_type == kTypeF32 ? 4LL * a.N : 2LL * a.N;
+  for (int m0 = 0; m0 < args.M; m0 += most) {
+    a.M = std::min(most, args.M - m0);
+    a.x = args.x + m0 * args.ldx;
+    a.index = args.index + m0;
+    if (args.add) a.add = static_cast<const char*>(args.add) + m0 * add_row;
+    a.out = static_cast<char*>(args.out) + m0 * out_row;
+    const cudaError_t e = whole ? launch_rank<true>(a, stream) : launch_rank<false>(a, stream);
+    if (e != cudaSuccess) return e;
   }
-  return launch_k(lora_plain_kernel, dim3(static_cast<unsigned>(a.M)), dim3(kThreads), 0, stream, true, a);
+  return cudaSuccess;
 }
 
 }  // namespace moe

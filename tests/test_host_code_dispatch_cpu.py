@@ -97,11 +97,13 @@ def test_adapters_take_the_kernel_of_their_size(lib):
         (s, _, _), (k, grid, cluster) = kernels(lib, lambda: lora(lib, M, r=r))
         assert "sort" in s and "lora_many" in k and grid[0] % cluster == 0
         assert grid[0] // cluster >= (M + 127) // 128
-    # what cannot be read in 16-byte pieces
-    for kw in (dict(K=513), dict(N=514), dict(r=12), dict(x=ODD), dict(out=ODD), dict(add=ODD)):
-        for M in (5, 5000):
-            (k, grid, _), = kernels(lib, lambda: lora(lib, M, **kw))
-            assert "lora_plain" in k and grid[0] == M
+    # what cannot be read in pieces goes value by value, as many rows at a time as few are
+    for kw, whole in ((dict(K=513), 0), (dict(N=514), 0), (dict(r=3), 0), (dict(r=12), 1), (dict(x=ODD), 0), (dict(out=ODD), 0),
+                      (dict(add=ODD), 0), (dict(r=100, N=514), 0)):
+        for M in (5, 768, 5000):
+            got = kernels(lib, lambda: lora(lib, M, **kw))
+            assert len(got) == -(-M // (384 if kw.get("r") == 100 else 768))
+            assert all("lora_few" in k and f"Lb{whole}E" in k and grid[0] % 8 == 0 for k, grid, _ in got)
     assert lib.moe_w4a16_lora_workspace_size(768, 512, 512, 64, 4) == 0
     assert lib.moe_w4a16_lora_workspace_size(769, 512, 512, 64, 4) > 0
 
