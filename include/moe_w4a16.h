@@ -428,10 +428,10 @@ int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, i
  * NaN where the formula gives infinity; rows of other adapters, and without one, are not
  * affected by such values.
  * 1 <= r <= 128 (a larger rank is two adapters, one call after the other), 1 <= L <= 1023, M
- * up to 2^29, K and N up to 2^22. One launch up to 768 rows (384 for r > 64), two above.
+ * up to 2^29, K and N up to 2^22. One launch up to 1,536 rows, two above.
  * Rows of x, a, add or out that are not whole 16-byte pieces (K, N or ldx no multiple of 8,
- * other addresses), and r that is no multiple of 4 (of 8 above those rows), take a slower
- * form, one launch for each 768 (384) rows. M == 0 is a no-op. No host synchronisation; the
+ * other addresses), and r that is no multiple of 4 (of 8 above 768 rows; 384 for r > 64),
+ * take a slower form, one launch for each 768 (384) rows. M == 0 is a no-op. No host synchronisation; the
  * same result in every run. A pipeline wait that gives up is reported by
  * moe_w4a16_fp8_status. */
 size_t moe_w4a16_lora_workspace_size(int M, int K, int N, int r, int L);

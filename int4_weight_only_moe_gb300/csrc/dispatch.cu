@@ -65,17 +65,6 @@ __device__ __forceinline__ int ld_shared_rank(const int* p, int rank) {
   return static_cast<int>(v);
 }
 
-// Lanes with the same bucket as this one's (-1: none has), bit by bit. (With many different
-// buckets in a warp the instruction that compares all lanes takes several times as long.)
-__device__ __forceinline__ unsigned lanes_of(int bucket, int bits) {
-  unsigned peers = __ballot_sync(0xffffffffu, bucket >= 0);
-  for (int k = 0; k < bits; ++k) {
-    const unsigned set = __ballot_sync(0xffffffffu, bucket >> k & 1);
-    peers &= bucket >> k & 1 ? set : ~set;
-  }
-  return peers;
-}
-
 // Stable counting sort by one cluster. Each warp owns a run of consecutive slots and
 // counts it by itself; prefix sums over the warps, the CTAs of the cluster and the buckets
 // give every warp the first row of its own slots of each bucket, and a second pass over the

@@ -327,6 +327,17 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
+// Lanes with the same bucket as this one's (-1: none has), bit by bit. (With many different
+// buckets in a warp the instruction that compares all lanes takes several times as long.)
+__device__ __forceinline__ unsigned lanes_of(int bucket, int bits) {
+  unsigned peers = __ballot_sync(0xffffffffu, bucket >= 0);
+  for (int k = 0; k < bits; ++k) {
+    const unsigned set = __ballot_sync(0xffffffffu, bucket >> k & 1);
+    peers &= bucket >> k & 1 ? set : ~set;
+  }
+  return peers;
+}
+
 // f16x2 arithmetic, round to nearest even.
 __device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
   uint32_t d;

@@ -153,7 +153,7 @@ def test_strides_and_alignment(M):
     check(x, wide, b, index, None, add, rows=rows)
 
 
-@pytest.mark.parametrize("M", [9, 1200])
+@pytest.mark.parametrize("M", [9, 1200, 2500])
 def test_same_bits_other_stream_workspace_and_graphs(M):
     x, a, b, index = problem(M, 1024, 512, 32, 7)
     index, add = dev(index), normal(M, 512, seed=1, dtype=F32)

@@ -93,7 +93,10 @@ def test_adapters_take_the_kernel_of_their_size(lib):
     for M, r, name in ((1, 16, "few"), (768, 64, "few"), (384, 128, "few"), (40, 8, "few")):
         (k, grid, cluster), = kernels(lib, lambda: lora(lib, M, r=r))
         assert "lora_few" in k and cluster == 8 and grid[0] % 8 == 0
-    for M, r in ((769, 64), (385, 128), (8192, 16), (100000, 64)):
+    for M, r in ((769, 64), (385, 128), (1536, 16)):
+        (k, grid, cluster), = kernels(lib, lambda: lora(lib, M, r=r))
+        assert "lora_many" in k and grid[0] % cluster == 0 and grid[0] // cluster >= (M + 127) // 128
+    for M, r in ((1537, 64), (8192, 16), (100000, 64)):
         (s, _, _), (k, grid, cluster) = kernels(lib, lambda: lora(lib, M, r=r))
         assert "sort" in s and "lora_many" in k and grid[0] % cluster == 0
         assert grid[0] // cluster >= (M + 127) // 128
@@ -104,8 +107,8 @@ def test_adapters_take_the_kernel_of_their_size(lib):
             got = kernels(lib, lambda: lora(lib, M, **kw))
             assert len(got) == -(-M // (384 if kw.get("r") == 100 else 768))
             assert all("lora_few" in k and f"Lb{whole}E" in k and grid[0] % 8 == 0 for k, grid, _ in got)
-    assert lib.moe_w4a16_lora_workspace_size(768, 512, 512, 64, 4) == 0
-    assert lib.moe_w4a16_lora_workspace_size(769, 512, 512, 64, 4) > 0
+    assert lib.moe_w4a16_lora_workspace_size(1536, 512, 512, 64, 4) == 0
+    assert lib.moe_w4a16_lora_workspace_size(1537, 512, 512, 64, 4) > 0
 
 
 def test_rows_of_an_adapter_alone_in_its_group_have_a_cluster(lib):
