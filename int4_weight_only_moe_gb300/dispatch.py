@@ -17,7 +17,7 @@ from typing import NamedTuple
 import torch
 
 from . import BF16, E4M3, F32, _check, _new, lib, moe_w4a16_dispatch_rows
-from .routing import _dense, _device, _handle, _rows
+from .routing import _dense, _device, _fast, _handle, _rows
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 _MOVED = {**_FLOATS, torch.float8_e4m3fn: E4M3, torch.uint8: E4M3}
@@ -116,6 +116,12 @@ def gather(x, order, out=None, stream=None):
     """``x`` [M, K] (bf16, fp32, e4m3 or bytes) in the order's rows: [rows, K]. Rows that fill
     up an expert's are 0, those behind the last expert's are left as they were (a new
     ``out`` is not cleared)."""
+    if out is not None and stream is None and (fast := _fast(x)):
+        calls, dev, handle = fast
+        rc = calls.gather(dev, handle, x, *order, out)
+        if rc is not None:
+            _check(rc)
+            return out
     M, K, stride = _rows(x, "x", _MOVED)
     dev = _device(x, "x")
     at, m, topk, E, cap, block = _parts(order, dev)
@@ -131,6 +137,12 @@ def gather(x, order, out=None, stream=None):
 
 def sort_gather(x, topk_ids, E, block=1, expert_range=None, out=None, order=None, stream=None):
     """``sort`` and ``gather`` in one call: ``(rows [rows, K], order)``."""
+    if out is not None and order is not None and expert_range is None and stream is None and (fast := _fast(x)):
+        calls, dev, handle = fast
+        rc = calls.sort_gather(dev, handle, x, topk_ids, E, 0, block, *order, out)
+        if rc is not None:
+            _check(rc)
+            return out, order
     M, K, stride = _rows(x, "x", _MOVED)
     dev = _device(x, "x")
     order, at, m, topk, begin, E, cap = _order_for(topk_ids, E, block, expert_range, order, dev, stream)
@@ -145,6 +157,12 @@ def sort_gather(x, topk_ids, E, block=1, expert_range=None, out=None, order=None
 
 
 def _combine(y, weights, order, add, out, out_dtype, stream):
+    if out is not None and stream is None and (fast := _fast(y)):
+        calls, dev, handle = fast
+        rc = calls.combine(dev, handle, y, weights, order[1], order[2], add, out)
+        if rc is not None:
+            _check(rc)
+            return out
     R, K, dev = _matrix(y, "y")
     _, slots, position = order
     if position.dim() != 2:
@@ -181,6 +199,12 @@ def combine_backward(dout, y, weights, order, dy=None, dweights=None, stream=Non
     """Gradient of ``combine`` for ``dout`` [M, K]: ``(dy [rows, K] of y's type, dweights fp32
     [M, topk])``. Rows of ``dy`` that fill up an expert's are 0, those behind the last
     expert's are left as they were. ``add`` has the gradient ``dout`` itself."""
+    if dy is not None and dweights is not None and stream is None and (fast := _fast(dout)):
+        calls, dev, handle = fast
+        rc = calls.combine_backward(dev, handle, dout, y, weights, *order, dy, dweights)
+        if rc is not None:
+            _check(rc)
+            return dy, dweights
     M, K, dev = _matrix(dout, "dout")
     at, m, topk, E, cap, block = _parts(order, dev)
     if m != M:

@@ -7,7 +7,7 @@ import functools
 import torch
 
 from . import BF16, F32, _check, _new, lib, moe_w4a16_lora_workspace_size
-from .routing import _dense, _device, _handle, _on, _rows
+from .routing import _dense, _device, _fast, _handle, _on, _rows
 
 _FLOATS = {torch.float32: F32, torch.bfloat16: BF16}
 _POOL_BYTES = 16 << 20
@@ -24,6 +24,12 @@ def apply(x, a, b, index, add=None, scale=None, out=None, out_dtype=torch.bfloat
     ``moe_w4a16_lora_workspace_size(M, K, N, r, L)`` bytes; where it is not given, up to 16
     MiB come from the library's stream-ordered pool, more from torch.
     """
+    if out is not None and workspace is None and stream is None and (fast := _fast(x)):
+        calls, dev, handle = fast
+        rc = calls.lora(dev, handle, x, a, b, index, add, scale, out, _POOL_BYTES)
+        if rc is not None:
+            _check(rc)
+            return out
     M, K, ldx = _rows(x, "x", (torch.bfloat16,))
     dev = _device(x, "x")
     if a.dim() != 3 or b.dim() != 3:

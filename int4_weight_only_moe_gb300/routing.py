@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from . import BF16, F32, SCORE_SIGMOID, SCORE_SOFTMAX, _check, _need, _new, lib
+from . import BF16, F32, SCORE_SIGMOID, SCORE_SOFTMAX, _calls, _check, _need, _new, lib
 
 _SCORES = {"sigmoid": SCORE_SIGMOID, "softmax": SCORE_SOFTMAX}
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -94,10 +94,26 @@ def route_scored(logits, topk, scoring="sigmoid", bias=None, n_group=1, topk_gro
     return ids, weights
 
 
+def _fast(t):
+    """``(compiled calls, device, current stream's handle)`` where ``t`` is on the current
+    device, else ``None``."""
+    calls = _calls.module or _calls.load()
+    dev = t.get_device()
+    if calls is None or dev < 0 or dev != torch._C._cuda_getDevice():
+        return None
+    return calls, dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
 def route_scored_backward(dweights, logits, ids, scoring="sigmoid", renormalize=True, scale=1.0, out=None, stream=None):
     """Gradient with regard to ``logits`` [M, E] (fp32 or bf16, and so is it) of the weights
     of ``route_scored``, for their gradient ``dweights`` fp32 [M, topk] and the chosen ``ids``
     int32 [M, topk]; ``scoring``, ``renormalize`` and ``scale`` as they were there."""
+    if out is not None and stream is None and scoring in _SCORES and (fast := _fast(logits)):
+        calls, dev, handle = fast
+        rc = calls.route_backward(dev, handle, dweights, logits, ids, _SCORES[scoring], renormalize, scale, out)
+        if rc is not None:
+            _check(rc)
+            return out
     M, E, stride = _rows(logits, "logits", _TYPES)
     dev = _device(logits, "logits")
     score = _SCORES.get(scoring)
