@@ -209,7 +209,7 @@ __device__ __forceinline__ void zero_filling(const int32_t* offsets, const int32
     for (int r = first; r < last; ++r) {
       if (slots[r] >= 0) continue;
       T* to = reinterpret_cast<T*>(out + r * row_bytes);
-      for (int v = threadIdx.x; v < n; v += kRowThreads) to[v] = T{};
+      for (int v = threadIdx.x; v < n; v += blockDim.x) to[v] = T{};
     }
   }
 }
@@ -218,6 +218,7 @@ __device__ __forceinline__ void zero_filling(const int32_t* offsets, const int32
 template <int kBytes>
 __global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherRowsArgs a, int parts, int fill) {
   using T = typename Piece<kBytes>::T;
+  const int threads = blockDim.x;
   __shared__ int row_of[kMaxTopk];
   pdl_wait();
   const long long cta = blockIdx.x;
@@ -234,25 +235,25 @@ __global__ void __launch_bounds__(kRowThreads) gather_kernel(const GatherRowsArg
   uint8_t* out = static_cast<uint8_t*>(a.out);
   constexpr int kOnce = 4;
   __syncthreads();
-  for (int v0 = lo + threadIdx.x; v0 < hi; v0 += kOnce * kRowThreads) {
+  for (int v0 = lo + threadIdx.x; v0 < hi; v0 += kOnce * threads) {
     T x[kOnce];
 #pragma unroll
     for (int i = 0; i < kOnce; ++i)
-      if (v0 + i * kRowThreads < hi) x[i] = from[v0 + i * kRowThreads];
+      if (v0 + i * threads < hi) x[i] = from[v0 + i * threads];
     for (int j = 0; j < a.topk; ++j) {
       const int r = row_of[j];
       if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(a.capacity)) continue;
       T* to = reinterpret_cast<T*>(out + r * a.row_bytes);
 #pragma unroll
       for (int i = 0; i < kOnce; ++i)
-        if (v0 + i * kRowThreads < hi) to[v0 + i * kRowThreads] = x[i];
+        if (v0 + i * threads < hi) to[v0 + i * threads] = x[i];
     }
   }
 }
 
 // Order and gather in one launch, for few slots: every CTA counts the slots of all experts
 // for itself (up to kFewSlots ids, from L2) and places its own token's. One token of 8 among
-// 384 experts takes 3.4 us, two launches 4.8.
+// 384 experts takes 2.7 us, two launches 4.8.
 constexpr int kFewSlots = 1024;
 template <int kBytes>
 __global__ void __launch_bounds__(kRowThreads) sort_gather_few_kernel(const SortArgs o, const GatherRowsArgs a, int parts, int fill) {
@@ -425,8 +426,11 @@ __device__ __forceinline__ void by_groups(int topk, F&& f) {
 
 // out[t] = sum_j w y[row of j] (+ add[t]); `parts` CTAs share a row. A choice without a row
 // reads row 0 in its place, which counts nothing.
+// (128 threads: 8,192 tokens of 1,024 columns take 24.5 us, 30 with 256; few tokens make six
+// CTAs to an SM.)
+constexpr int kSumThreads = 128;
 template <typename Ty, typename To, int n>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs a, int parts) {
+__global__ void __launch_bounds__(kSumThreads) combine_kernel(const CombineArgs a, int parts) {
   __shared__ int row_of[kMaxTopk];
   __shared__ float weight_of[kMaxTopk];
   pdl_wait();
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs 
   const int pieces = a.K / n, per = (pieces + parts - 1) / parts;
   const int lo = part * per, hi = min(pieces, lo + per);
   __syncthreads();
-  for (int v = lo + threadIdx.x; v < hi; v += kRowThreads) {
+  for (int v = lo + threadIdx.x; v < hi; v += kSumThreads) {
     float acc[n];
 #pragma unroll
     for (int i = 0; i < n; ++i) acc[i] = 0.f;
@@ -469,11 +473,12 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const CombineArgs 
 
 // One CTA to a token: each thread keeps its own part of the topk sums of products, which
 // the CTA joins at the end. Behind the tokens' CTAs those of the rows that fill up.
+constexpr int kBackThreads = 128, kBackWarps = kBackThreads / 32;  // (256: 4,000 tokens of 1,024 columns 44 us, 34 now)
 template <typename Tg, typename Ty, int n>
-__global__ void __launch_bounds__(kRowThreads, 2) combine_backward_kernel(const CombineBackwardArgs a, int fill) {
+__global__ void __launch_bounds__(kBackThreads, 4) combine_backward_kernel(const CombineBackwardArgs a, int fill) {
   __shared__ int row_of[kMaxTopk];
   __shared__ float weight_of[kMaxTopk];
-  __shared__ float part_of[kRowWarps][kMaxTopk];
+  __shared__ float part_of[kBackWarps][kMaxTopk];
   pdl_wait();
   if (blockIdx.x >= static_cast<unsigned>(a.M)) {
     zero_filling<n * sizeof(Ty) >= 16 ? 16 : n * static_cast<int>(sizeof(Ty))>(
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) combine_backward_kernel(const 
   by_groups(a.topk, [&](auto count, int j0) {
     constexpr int C = decltype(count)::value;
     float dot[C] = {};
-    for (int v = threadIdx.x; v < a.K / n; v += kRowThreads) {
+    for (int v = threadIdx.x; v < a.K / n; v += kBackThreads) {
       Values<Tg, n> g;
       Values<Ty, n> y[C];
       g.load(at<Tg>(a.g, t, a.K, v * n));
@@ -520,17 +525,18 @@ __global__ void __launch_bounds__(kRowThreads, 2) combine_backward_kernel(const 
   __syncthreads();
   if (threadIdx.x < a.topk) {
     float sum = 0.f;
-    for (int i = 0; i < kRowWarps; ++i) sum += part_of[i][threadIdx.x];
+    for (int i = 0; i < kBackWarps; ++i) sum += part_of[i][threadIdx.x];
     a.dweights[static_cast<long long>(t) * a.topk + threadIdx.x] = sum;
   }
 }
 
 bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 
-// CTAs to a row of `pieces` pieces: one, unless the tokens alone leave SMs without work.
-int row_parts(long long M, int pieces, int num_sms) {
-  const int most = (pieces + kRowThreads - 1) / kRowThreads;
-  const long long want = (2LL * num_sms + M - 1) / std::max(1LL, M);
+// CTAs of `threads` threads to a row of `pieces` pieces: one, unless the tokens alone make fewer
+// than `ctas`.
+int row_parts(long long M, int pieces, int threads, int ctas) {
+  const int most = (pieces + threads - 1) / threads;
+  const long long want = (ctas + M - 1) / std::max(1LL, M);
   return static_cast<int>(std::max(1LL, std::min<long long>(most, want)));
 }
 
@@ -558,8 +564,11 @@ cudaError_t launch_gather(const GatherRowsArgs& a, int num_sms, cudaStream_t str
   const int fill = fill_parts(a.block);
   auto go = [&](auto bytes) {
     constexpr int n = decltype(bytes)::value;
-    const int parts = row_parts(a.M, static_cast<int>(a.row_bytes / n), num_sms);
-    return launch_k(gather_kernel<n>, dim3(static_cast<unsigned>(static_cast<long long>(a.M) * parts + a.E * fill)), dim3(kRowThreads), 0,
+    // (short rows: 6,000 of 784 bytes, top-4, 11.4 us with 64 threads, 15.2 with 256; long ones the
+    // other way: 14,336 bytes, top-8, 170 and 178)
+    const int pieces = static_cast<int>(a.row_bytes / n), threads = pieces <= 128 ? 64 : kRowThreads;
+    const int parts = row_parts(a.M, pieces, threads, 2 * num_sms);
+    return launch_k(gather_kernel<n>, dim3(static_cast<unsigned>(static_cast<long long>(a.M) * parts + a.E * fill)), dim3(threads), 0,
                     stream, true, a, parts, fill);
   };
   const uintptr_t all = static_cast<uintptr_t>(a.row_bytes) | static_cast<uintptr_t>(a.stride_bytes) |
@@ -578,7 +587,7 @@ cudaError_t launch_sort_gather(const SortArgs& o, const GatherRowsArgs& a, int n
   const int fill = fill_parts(a.block);
   auto go = [&](auto bytes) {
     constexpr int n = decltype(bytes)::value;
-    const int parts = row_parts(a.M, static_cast<int>(a.row_bytes / n), num_sms);
+    const int parts = row_parts(a.M, static_cast<int>(a.row_bytes / n), kRowThreads, 2 * num_sms);
     return launch_k(sort_gather_few_kernel<n>, dim3(static_cast<unsigned>(a.M * parts + a.E * fill)), dim3(kRowThreads), 0, stream, true,
                     o, a, parts, fill);
   };
@@ -598,8 +607,8 @@ cudaError_t launch_combine(const CombineArgs& args, int num_sms, cudaStream_t st
     using Ty = decltype(ty);
     using To = decltype(to);
     auto with = [&](auto kernel, int n) {
-      const int parts = row_parts(a.M, a.K / n, num_sms);
-      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) * parts), dim3(kRowThreads), 0, stream, true, a, parts);
+      const int parts = row_parts(a.M, a.K / n, kSumThreads, 6 * num_sms);
+      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) * parts), dim3(kSumThreads), 0, stream, true, a, parts);
     };
     return wide ? with(combine_kernel<Ty, To, 8>, 8) : with(combine_kernel<Ty, To, 1>, 1);
   };
@@ -614,7 +623,7 @@ cudaError_t launch_combine_backward(const CombineBackwardArgs& a, int num_sms, c
     using Tg = decltype(tg);
     using Ty = decltype(ty);
     auto with = [&](auto kernel) {
-      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) + a.E * fill), dim3(kRowThreads), 0, stream, true, a, fill);
+      return launch_k(kernel, dim3(static_cast<unsigned>(a.M) + a.E * fill), dim3(kBackThreads), 0, stream, true, a, fill);
     };
     return wide ? with(combine_backward_kernel<Tg, Ty, 8>) : with(combine_backward_kernel<Tg, Ty, 1>);
   };

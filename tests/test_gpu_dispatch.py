@@ -4,7 +4,7 @@ definitions. Whole numbers and moved rows have to be equal.
 Tolerances. HALF is half a step of the output's type relative to the value. A sum of n fp32
 fused products, in any order, is off by at most n 2^-24 of the sum of its terms' magnitudes;
 combine adds topk products and an addend, a gradient of a weight K products: at most
-ceil(K / 256) + 8 of them one after another in a thread, 5 + 8 additions across the CTA, the
+ceil(K / 128) + 8 of them one after another in a thread (128 share a token), 5 + 8 additions across the CTA, the
 product's rounding taken up by the fused operation; two more for what was rounded before."""
 import numpy as np
 import pytest
@@ -237,7 +237,7 @@ def test_combine_backward(M, topk, E, block, K, y_type, g_type):
     dy, dw = dispatch.combine_backward(g, y, w, order, dy=before.clone())
     want, want_w, size = do.combine_backward(host(g), host(y), host(w), *map(host, order), host(before))
     close(dy, want, (HALF[y_type] + (2.0 ** -23 if y_type == BF16 else 0.0)) * np.abs(want))
-    close(dw, want_w, (-(-K // 256) + 8 + 13 + 2) * 2.0 ** -24 * size)
+    close(dw, want_w, (-(-K // 128) + 8 + 13 + 2) * 2.0 ** -24 * size)
 
 
 def test_gradients_against_differences():
