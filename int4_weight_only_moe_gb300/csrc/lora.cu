@@ -215,22 +215,23 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
   const int g = lane >> 2, t = lane & 3;
   const uint16_t* A = a.a + static_cast<long long>(l) * a.r * a.K;
   const uint16_t* B = a.b + static_cast<long long>(l) * a.N * a.r;
-  // what comes after the exchange is asked into L2: lines of b, lines of the addends
-  {
-    const int n0 = block0 * 32, n1 = min(a.N, block1 * 32);
-    const char* from = reinterpret_cast<const char*>(B + static_cast<long long>(n0) * a.r);
-    for (int i = tid * 128; i < (n1 - n0) * a.r * 2; i += kThreads * 128) prefetch_l2(from + i);
-    if (a.add && n1 > n0) {
-      const int item = a.add_type == kTypeF32 ? 4 : 2, lines = ((n1 - n0) * item + 127) / 128;
-      for (int i = tid; i < rows * lines; i += kThreads)
-        prefetch_l2(static_cast<const char*>(a.add) + (static_cast<long long>(row_of[i / lines]) * a.N + n0) * item + i % lines * 128);
-    }
-  }
   // ---- a[l] x: this CTA's part of the K columns in units of 32, dealt out to its warps
   float sum[kTiles][4] = {};
   {
     const int units = (a.K + 31) / 32, each = (units + kCluster - 1) / kCluster;
     const int u0 = rank * each, u1 = min(units, u0 + each);
+    // what comes after the exchange is asked into L2: lines of b, lines of the addends
+    {
+      const int n0 = block0 * 32, n1 = min(a.N, block1 * 32);
+      const char* from = reinterpret_cast<const char*>(B + static_cast<long long>(n0) * a.r);
+      for (int i = tid * 128; i < (n1 - n0) * a.r * 2; i += kThreads * 128) prefetch_l2(from + i);
+      if (a.add && n1 > n0) {
+        const int item = a.add_type == kTypeF32 ? 4 : 2, lines = ((n1 - n0) * item + 127) / 128;
+        for (int m = w; m < rows; m += kWarps)
+          for (int i = lane; i < lines; i += 32)
+            prefetch_l2(static_cast<const char*>(a.add) + (static_cast<long long>(row_of[m]) * a.N + n0) * item + i * 128);
+      }
+    }
     const uint16_t* x0 = a.x + static_cast<long long>(row_of[min(g, rows - 1)]) * a.ldx + 8 * t;
     const uint16_t* x1 = a.x + static_cast<long long>(row_of[min(g + 8, rows - 1)]) * a.ldx + 8 * t;
     constexpr int kOnce = !kWhole ? 1 : kTiles <= 2 ? 4 : kTiles <= 4 ? 2 : 1;  // units under way (more of them would cost a CTA)
