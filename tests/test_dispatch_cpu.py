@@ -64,7 +64,7 @@ def lib():
     return pkg.lib()
 
 
-BUF, BUF2 = ctypes.c_void_p(256), ctypes.c_void_p(512)  # never dereferenced: validation fails first
+BUF, BUF2 = ctypes.c_void_p(256), ctypes.c_void_p(1 << 40)  # never dereferenced: validation fails first
 ODD = ctypes.c_void_p(257)
 
 
@@ -93,31 +93,31 @@ def of_order(M, topk, E, block):
 
 
 def test_sort_refusals(lib):
-    good = [BUF, 4, 8, 0, 16, 1, BUF, BUF, BUF, None]
+    good = [BUF, 4, 8, 0, 16, 1, BUF, BUF2, BUF2, None]
     refused(lib.moe_w4a16_dispatch_sort, good, of_order(1, 2, 4, 5) + [
         (0, None, INVALID), (6, None, INVALID), (7, None, INVALID), (8, None, INVALID), (3, -1, INVALID),
         (0, ODD, INVALID), (6, ODD, INVALID), (7, ODD, INVALID), (8, ODD, INVALID)])
 
 
 def test_gather_refusals(lib):
-    good = [BUF, BF16, 64, BUF, BUF, BUF, BUF, 4, 64, 8, 16, 1, None]
+    good = [BUF, BF16, 64, BUF, BUF, BUF, BUF2, 4, 64, 8, 16, 1, None]
     refused(lib.moe_w4a16_dispatch_gather, good, of_order(7, 9, 10, 11) + [
         (0, None, INVALID), (1, 3, INVALID), (2, 63, INVALID), (3, None, INVALID), (4, None, INVALID), (5, None, INVALID),
         (6, None, INVALID), (8, 0, INVALID), (8, 1 << 23, SHAPE), (0, ODD, INVALID), (6, ODD, INVALID), (3, ODD, INVALID),
         (7, 0, OK)])
-    good = [BUF, BF16, 64, BUF, 4, 64, 8, 0, 16, 1, BUF, BUF, BUF, BUF, None]
+    good = [BUF, BF16, 64, BUF, 4, 64, 8, 0, 16, 1, BUF, BUF2, BUF2, BUF2, None]
     refused(lib.moe_w4a16_dispatch_sort_gather, good, of_order(4, 6, 8, 9) + [
         (0, None, INVALID), (1, -1, INVALID), (2, 63, INVALID), (3, None, INVALID), (5, 0, INVALID), (7, -1, INVALID),
         (10, None, INVALID), (11, None, INVALID), (12, None, INVALID), (13, None, INVALID), (13, ODD, INVALID)])
 
 
 def test_combine_refusals(lib):
-    good = [BUF, BF16, BUF, BUF, None, BUF, BF16, 4, 64, 8, 32, None]
+    good = [BUF, BF16, BUF, BUF, None, BUF2, BF16, 4, 64, 8, 32, None]
     refused(lib.moe_w4a16_combine, good, [
         (0, None, INVALID), (1, E4M3, INVALID), (2, ODD, INVALID), (3, None, INVALID), (3, ODD, INVALID), (4, ODD, INVALID),
         (5, None, INVALID), (5, ODD, INVALID), (6, 7, INVALID), (7, -1, INVALID), (8, 0, INVALID), (9, 0, INVALID),
         (10, -1, INVALID), (8, 1 << 23, SHAPE), (9, 33, SHAPE), (7, 1 << 28, SHAPE), (7, 0, OK)])
-    good = [BUF, BF16, BUF, BF16, BUF, BUF, BUF, BUF, BUF2, BUF, 4, 64, 8, 16, 1, None]
+    good = [BUF, BF16, BUF, BF16, BUF, BUF, BUF, BUF, BUF2, BUF2, 4, 64, 8, 16, 1, None]
     refused(lib.moe_w4a16_combine_backward, good, of_order(10, 12, 13, 14) + [
         (at, None, INVALID) for at in (0, 2, 4, 5, 6, 7, 8, 9)] + [(at, ODD, INVALID) for at in (0, 2, 4, 5, 6, 7, 8, 9)] + [
         (1, E4M3, INVALID), (3, E4M3, INVALID), (8, BUF, INVALID), (11, 0, INVALID), (11, 1 << 23, SHAPE), (10, 0, OK)])
@@ -134,14 +134,49 @@ def test_route_backward_refusals(lib):
 def test_lora_refusals(lib):
     size = lib.moe_w4a16_lora_workspace_size
     assert size(-1, 64, 64, 8, 3) == 0 and size(4, 64, 64, 129, 3) == 0 and size(4, 64, 64, 8, 1024) == 0
-    good = [BUF, 64, BUF, BUF, None, BUF, None, F32, BUF, BF16, 4, 64, 64, 8, 3, BUF, 1 << 40, None]
+    good = [BUF, 64, BUF, BUF, None, BUF, None, F32, BUF2, BF16, 4, 64, 64, 8, 3, BUF, 1 << 40, None]
     refused(lib.moe_w4a16_lora, good, [
         (at, None, INVALID) for at in (0, 2, 3, 5, 8)] + [(at, ODD, INVALID) for at in (0, 2, 3, 4, 5, 6, 8)] + [
         (1, 63, INVALID), (9, E4M3, INVALID), (10, -1, INVALID), (10, (1 << 29) + 1, SHAPE), (11, 0, INVALID),
         (11, 1 << 23, SHAPE), (12, 0, INVALID), (12, 1 << 23, SHAPE), (13, 0, INVALID), (13, 129, SHAPE), (14, 0, INVALID),
-        (14, 1024, SHAPE), (15, ctypes.c_void_p(272), INVALID), (6, BUF, INVALID), (10, 0, OK)])
+        (14, 1024, SHAPE), (15, ctypes.c_void_p(272), INVALID), (6, BUF2, INVALID), (10, 0, OK)])
     need = size(5000, 512, 512, 16, 4)
     if need:
         args = list(good)
         args[1], args[10], args[11], args[12], args[13], args[14], args[16] = 512, 5000, 512, 512, 16, 4, need - 1
         assert lib.moe_w4a16_lora(*args) == WORKSPACE
+
+
+def test_shared_memory_is_refused(lib):
+    """An output that lies in an input, at its first byte, its last, or behind its gaps."""
+    at = lambda a: ctypes.c_void_p(a)  # noqa: E731
+    base, far = 1 << 20, 1 << 40
+    n = 2 * 64 * 4  # of 4 rows of 64 bf16, 4 of them behind a gap of 64: span 7 * 64 * 2
+    cases = []
+    for out in (base, base + 7 * 128 - 2, base - 32 * 128 + 2):  # (32 rows of an order)
+        cases.append((lib.moe_w4a16_dispatch_gather,
+                      [at(base), BF16, 128, BUF, BUF, BUF, at(out), 4, 64, 8, 16, 1, None]))
+        cases.append((lib.moe_w4a16_dispatch_sort_gather,
+                      [at(base), BF16, 128, BUF, 4, 64, 8, 0, 16, 1, BUF, at(far), at(2 * far), at(out), None]))
+    for out in (base, base + 32 * 128 - 2, base - n + 2):
+        cases.append((lib.moe_w4a16_combine, [at(base), BF16, BUF, BUF, None, at(out), BF16, 4, 64, 8, 32, None]))
+    for out in (base + 2, base + n - 2, base - n + 2):
+        cases.append((lib.moe_w4a16_combine, [at(far), BF16, BUF, BUF, at(base), at(out), BF16, 4, 64, 8, 32, None]))
+        cases.append((lib.moe_w4a16_lora,
+                      [at(far), 64, BUF, BUF, None, BUF, at(base), BF16, at(out), BF16, 4, 64, 64, 8, 3, None, 0, None]))
+    for out in (base, base + 7 * 128 - 2, base - n + 2):
+        cases.append((lib.moe_w4a16_lora,
+                      [at(base), 128, BUF, BUF, None, BUF, None, BF16, at(out), BF16, 4, 64, 64, 8, 3, None, 0, None]))
+        cases.append((lib.moe_w4a16_route_scored_backward,
+                      [BUF, at(base), BF16, 128, BUF, 4, 64, 8, 1, 1, 1.0, at(out), None]))
+    for grad, y, w, dy, dw in ((base, far, BUF.value, base, 2 * far), (base, far, BUF.value, base + n - 2, 2 * far),
+                               (far, base, BUF.value, base - 32 * 128 + 2, 2 * far), (far, base, BUF.value, base, 2 * far),
+                               (far, 2 * far, base, base, base), (far, 2 * far, base, 3 * far, base + 4 * 32 - 4)):
+        cases.append((lib.moe_w4a16_combine_backward,
+                      [at(grad), BF16, at(y), BF16, at(w), BUF, BUF, BUF, at(dy), at(dw), 4, 64, 8, 16, 1, None]))
+    for slots, position in ((far, base), (base, far), (far, base + 4 * 31), (base - 4 * 31, far)):
+        cases.append((lib.moe_w4a16_dispatch_sort, [at(base), 4, 8, 0, 16, 1, BUF, at(slots), at(position), None]))
+        cases.append((lib.moe_w4a16_dispatch_sort_gather,
+                      [at(4 * far), BF16, 64, at(base), 4, 64, 8, 0, 16, 1, BUF, at(slots), at(position), at(2 * far), None]))
+    for call, args in cases:
+        assert call(*args) == INVALID, (call.__name__, args)

@@ -9,7 +9,8 @@ import pytest
 
 OBJECTS = ["route_scored.o", "fp8_quant.o", "fp8_matmul.o", "fp8_many.o", "ops_api.o", "dispatch.o", "route_backward.o", "lora.o",
            "lora_many.o", "dispatch_api.o"]
-BUF, BUF2, ODD = ctypes.c_void_p(4096), ctypes.c_void_p(8192), ctypes.c_void_p(4098)  # never read
+BUF, BUF2 = ctypes.c_void_p(4096), ctypes.c_void_p(1 << 45)  # of inputs and of outputs; never read
+ODD, ODD2 = ctypes.c_void_p(4098), ctypes.c_void_p((1 << 45) + 2)
 F32, BF16, E4M3 = 0, 1, 2
 DEVICES = (0, 1, 5, 0, 70)
 NAMES = [n for n in ("moe_w4a16_dispatch_sort", "moe_w4a16_dispatch_gather", "moe_w4a16_dispatch_sort_gather",
@@ -59,11 +60,11 @@ def lora(lib, M, K=512, N=512, r=16, L=4, add=BUF, add_type=BF16, out=BUF2, out_
 
 
 def sort(lib, M, topk, E, block=1):
-    return lib.moe_w4a16_dispatch_sort(BUF, M, topk, 0, E, block, BUF, BUF, BUF, None)
+    return lib.moe_w4a16_dispatch_sort(BUF, M, topk, 0, E, block, BUF2, BUF2, BUF2, None)
 
 
 def sort_gather(lib, M, topk, E, block=1, K=512, kind=BF16, x=BUF):
-    return lib.moe_w4a16_dispatch_sort_gather(x, kind, K, BUF, M, K, topk, 0, E, block, BUF, BUF, BUF, BUF2, None)
+    return lib.moe_w4a16_dispatch_sort_gather(x, kind, K, BUF, M, K, topk, 0, E, block, BUF2, BUF2, BUF2, BUF2, None)
 
 
 def test_every_device_is_set_up(lib):
@@ -101,7 +102,7 @@ def test_adapters_take_the_kernel_of_their_size(lib):
         assert "sort" in s and "lora_many" in k and grid[0] % cluster == 0
         assert grid[0] // cluster >= (M + 127) // 128
     # what cannot be read in pieces goes value by value, as many rows at a time as few are
-    for kw, whole in ((dict(K=513), 0), (dict(N=514), 0), (dict(r=3), 0), (dict(r=12), 1), (dict(x=ODD), 0), (dict(out=ODD), 0),
+    for kw, whole in ((dict(K=513), 0), (dict(N=514), 0), (dict(r=3), 0), (dict(r=12), 1), (dict(x=ODD), 0), (dict(out=ODD2), 0),
                       (dict(add=ODD), 0), (dict(r=100, N=514), 0)):
         for M in (5, 768, 5000):
             got = kernels(lib, lambda: lora(lib, M, **kw))
@@ -138,7 +139,7 @@ def test_combine_and_gradients_launch_once(lib):
             for K, wide in ((512, "Li8E"), (516, "Li1E")):
                 (k, grid, _), = kernels(lib, lambda: lib.moe_w4a16_combine(BUF, y, BUF, BUF, BUF, BUF2, out, M, K, 8, 99, None))
                 assert wide in k and grid[0] % M == 0
-                (k, grid, _), = kernels(lib, lambda: lib.moe_w4a16_combine_backward(BUF, out, BUF, y, BUF, BUF, BUF, BUF, BUF2, BUF, M, K, 8,
+                (k, grid, _), = kernels(lib, lambda: lib.moe_w4a16_combine_backward(BUF, out, BUF, y, BUF, BUF, BUF, BUF, BUF2, BUF2, M, K, 8,
                                                                                      64, 128, None))
                 assert wide in k and grid[0] == M + 64 * 8
         for topk, scoring, renorm, name in ((8, 1, 1, "Li8E"), (9, 1, 1, "Li16E"), (32, 0, 1, "Li32E"), (8, 0, 0, "plain"), (8, 1, 0, "Li8E")):
