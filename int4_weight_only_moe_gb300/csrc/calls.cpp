@@ -1,8 +1,12 @@
 // Python calls of the order, gather, combine, gradients and adapters without ctypes: tensors'
 // types, shapes and devices are read where they stand, and the C entry is called. A call that
-// is not plainly right (a wrong type, another device, a subclass of tensors) returns None: the
-// Python code that calls this checks it step by step and says what is wrong. A small call
-// takes 4 us, 3 of them the launch; 8 to 11 with the checks in Python.
+// is not plainly right (a wrong type, another device, a subclass of tensors, a function
+// transform's tensor without storage) returns None: the Python code that calls this checks it
+// step by step and says what is wrong. A small call takes 4 us, 3 of them the launch; 8 to 11
+// with the checks in Python.
+//
+// A tensor's methods may throw (its address, where it has no storage). They are called with
+// the interpreter's lock held, all of them in front of the C entry, which alone runs without it.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
@@ -89,11 +93,14 @@ PyObject* with(PyObject* const* args, Py_ssize_t n, Py_ssize_t want, F&& run) {
   return PyLong_FromLong(rc);
 }
 
-template <typename F>
-int unlocked(F&& f) {
-  int rc;
-  Py_BEGIN_ALLOW_THREADS rc = f();
-  Py_END_ALLOW_THREADS return rc;
+// `entry`, a C entry that knows nothing of Python, without the interpreter's lock.
+template <typename F, typename... Args>
+int unlocked(F* entry, Args... args) {
+  struct Lock {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Lock() { PyEval_RestoreThread(state); }
+  } lock;
+  return entry(args...);
 }
 
 int int_of(Call& c, PyObject* o) {
@@ -132,11 +139,9 @@ PyObject* gather(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (!x || !order_of(c, v[3], v[4], v[5], &o) || !c.need(Call::type_of(*x, true) >= 0 && x->size(0) == o.M && x->size(1) <= kInt)) return 0;
     void* out = c.dense<void>(v[6], x->scalar_type(), {o.rows, x->size(1)});
     if (!c.ok) return 0;
-    return unlocked([&] {
-      return moe_w4a16_dispatch_gather(x->data_ptr(), Call::type_of(*x, true), stride, o.offsets, o.slots, o.position, out,
-                                       static_cast<int>(o.M), static_cast<int>(x->size(1)), static_cast<int>(o.topk),
-                                       static_cast<int>(o.E), static_cast<int>(o.block), c.stream);
-    });
+    return unlocked(moe_w4a16_dispatch_gather, x->data_ptr(), Call::type_of(*x, true), stride, o.offsets, o.slots, o.position, out,
+                    static_cast<int>(o.M), static_cast<int>(x->size(1)), static_cast<int>(o.topk), static_cast<int>(o.E),
+                    static_cast<int>(o.block), c.stream);
   });
 }
 
@@ -158,10 +163,8 @@ PyObject* sort_gather(PyObject*, PyObject* const* v, Py_ssize_t n) {
     auto* position = c.dense<int32_t>(v[9], at::kInt, {M, topk});
     void* out = c.dense<void>(v[10], x->scalar_type(), {rows, x->size(1)});
     if (!c.ok) return 0;
-    return unlocked([&] {
-      return moe_w4a16_dispatch_sort_gather(x->data_ptr(), Call::type_of(*x, true), stride, at, M, static_cast<int>(x->size(1)), topk,
-                                            begin, E, block, offsets, slots, position, out, c.stream);
-    });
+    return unlocked(moe_w4a16_dispatch_sort_gather, x->data_ptr(), Call::type_of(*x, true), stride, at, M, static_cast<int>(x->size(1)),
+                    topk, begin, E, block, offsets, slots, position, out, c.stream);
   });
 }
 
@@ -176,10 +179,8 @@ PyObject* combine(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const auto* w = c.dense_or_none<float>(v[3], at::kFloat, {M, topk});
     const void* add = c.dense_or_none<void>(v[6], out->scalar_type(), {M, K});
     if (!c.ok) return 0;
-    return unlocked([&] {
-      return moe_w4a16_combine(y->data_ptr(), Call::type_of(*y), w, at, add, out->data_ptr(), Call::type_of(*out), static_cast<int>(M),
-                               static_cast<int>(K), static_cast<int>(topk), static_cast<int>(rows), c.stream);
-    });
+    return unlocked(moe_w4a16_combine, y->data_ptr(), Call::type_of(*y), w, at, add, out->data_ptr(), Call::type_of(*out),
+                    static_cast<int>(M), static_cast<int>(K), static_cast<int>(topk), static_cast<int>(rows), c.stream);
   });
 }
 
@@ -195,11 +196,9 @@ PyObject* combine_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     void* dy = c.dense<void>(v[8], y->scalar_type(), {o.rows, K});
     auto* dw = c.dense<float>(v[9], at::kFloat, {o.M, o.topk});
     if (!c.ok) return 0;
-    return unlocked([&] {
-      return moe_w4a16_combine_backward(g->data_ptr(), Call::type_of(*g), y->data_ptr(), Call::type_of(*y), w, o.offsets, o.slots,
-                                        o.position, dy, dw, static_cast<int>(o.M), static_cast<int>(K), static_cast<int>(o.topk),
-                                        static_cast<int>(o.E), static_cast<int>(o.block), c.stream);
-    });
+    return unlocked(moe_w4a16_combine_backward, g->data_ptr(), Call::type_of(*g), y->data_ptr(), Call::type_of(*y), w, o.offsets,
+                    o.slots, o.position, dy, dw, static_cast<int>(o.M), static_cast<int>(K), static_cast<int>(o.topk),
+                    static_cast<int>(o.E), static_cast<int>(o.block), c.stream);
   });
 }
 
@@ -218,10 +217,8 @@ PyObject* route_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
     const auto* g = c.dense<float>(v[2], at::kFloat, {M, topk});
     void* out = c.dense<void>(v[8], l->scalar_type(), {M, E});
     if (!c.ok) return 0;
-    return unlocked([&] {
-      return moe_w4a16_route_scored_backward(g, l->data_ptr(), Call::type_of(*l), stride, at, static_cast<int>(M), static_cast<int>(E),
-                                             static_cast<int>(topk), scoring, renormalize, static_cast<float>(scale), out, c.stream);
-    });
+    return unlocked(moe_w4a16_route_scored_backward, g, l->data_ptr(), Call::type_of(*l), stride, at, static_cast<int>(M),
+                    static_cast<int>(E), static_cast<int>(topk), scoring, renormalize, static_cast<float>(scale), out, c.stream);
   });
 }
 
@@ -242,11 +239,9 @@ PyObject* lora(PyObject*, PyObject* const* v, Py_ssize_t n) {
     if (!c.need(!add || (add->size(0) == M && add->size(1) == N)) || PyErr_Occurred()) return 0;
     const int m = static_cast<int>(M), k = static_cast<int>(K), nn = static_cast<int>(N), rr = static_cast<int>(r), l = static_cast<int>(L);
     if (!c.need(moe_w4a16_lora_workspace_size(m, k, nn, rr, l) <= most)) return 0;
-    return unlocked([&] {
-      return moe_w4a16_lora(static_cast<const uint16_t*>(x->data_ptr()), stride, pa, pb, scale, index, add ? add->data_ptr() : nullptr,
-                            add ? Call::type_of(*add) : MOE_W4A16_F32, out->data_ptr(), Call::type_of(*out), m, k, nn, rr, l, nullptr, 0,
-                            c.stream);
-    });
+    return unlocked(moe_w4a16_lora, static_cast<const uint16_t*>(x->data_ptr()), stride, pa, pb, scale, index,
+                    add ? add->data_ptr() : nullptr, add ? Call::type_of(*add) : MOE_W4A16_F32, out->data_ptr(), Call::type_of(*out), m,
+                    k, nn, rr, l, nullptr, size_t{0}, c.stream);
   });
 }
 
