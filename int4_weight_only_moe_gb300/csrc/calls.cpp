@@ -25,6 +25,8 @@ struct Call {
     if (!ok || !THPVariable_CheckExact(o)) return fail();
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.defined() || t.layout() != at::kStrided || !t.is_cuda() || t.get_device() != dev) return fail();
+    // (a null address would stand for an optional tensor that is not given)
+    if (!t.data_ptr() && t.numel() > 0) return fail();
     return &t;
   }
   const at::Tensor* fail() {

@@ -57,7 +57,10 @@ def _dense(t, dtype, shape, name, dev):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         _need(t, (str(dtype).removeprefix("torch."),), shape, name)
         _on(t, dev, name)
-    return t.data_ptr()
+    at = t.data_ptr()
+    if not at and t.numel():  # (which would stand for an optional tensor that is not given)
+        raise ValueError(f"{name}: a tensor without memory")
+    return at
 
 
 def _handle(stream, dev):

@@ -1,6 +1,6 @@
 """Tensors of torch's function transforms in the compiled Python calls, without a GPU. Such a
-tensor has the plain type, a shape and strides, but no storage: asking for its address raises.
-The calls have to hand it back like anything else that is not plainly right. The source is
+tensor has the plain type, a shape and strides, but no storage: asking for its address raises,
+or gives 0, which the C entries take for an optional tensor that is not given. The calls have to hand it back like anything else that is not plainly right. The source is
 compiled here without its device test, on C entries that only count their calls, and run in
 another process: a call that throws without the interpreter's lock ends it."""
 import os
@@ -57,18 +57,17 @@ args = dict(
 call = lambda args: getattr(calls, name)(-1, 0, *args)  # (-1: where a tensor of the host says it is)
 assert call(args) == 0
 APPLY = dict(vmap=lambda f, x: torch.vmap(f)(torch.stack([x, x])), grad=lambda f, x: torch.func.grad(f)(x),
-             vjp=lambda f, x: torch.func.vjp(f, x), jvp=lambda f, x: torch.func.jvp(f, (x,), (x,)))
+             vjp=lambda f, x: torch.func.vjp(f, x), jvp=lambda f, x: torch.func.jvp(f, (x,), (x,)),
+             functionalize=lambda f, x: torch.func.functionalize(f)(x))
 for how, apply in APPLY.items():
     tried = 0
     for at, arg in enumerate(args):
-        if not torch.is_tensor(arg) or not (arg.is_floating_point() or how == "vmap"):
+        if not torch.is_tensor(arg) or not (arg.is_floating_point() or how in ("vmap", "functionalize")):
             continue
         print(how, at, file=sys.stderr, flush=True)
-        # (combine takes the number of slots from their tensor, not its address)
-        want = 0 if name == "combine" and at == 2 else None
         def one(x):
             got = call([*args[:at], x, *args[at + 1:]])
-            assert got == want, got
+            assert got is None, got
             return x.sum()
         apply(one, arg)
         tried += 1
