@@ -423,10 +423,10 @@ int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, i
  *   workspace  >= moe_w4a16_lora_workspace_size(M, K, N, r, L) bytes (0 for sizes that are
  *          not supported, and where none is needed), 256-byte aligned; holds nothing between
  *          calls. NULL: as in moe_w4a16_shared_expert
- * Both products' sums are fp32. Between them the first one's are split into bf16 parts of
- * 16 bits together (24 for an fp32 output), so that an infinite or NaN value of b may make
- * NaN where the formula gives infinity; rows of other adapters, and without one, are not
- * affected by such values.
+ * Both products' sums are fp32. Between them the first one's are split into three bf16 parts
+ * of 24 bits together, so that nothing of them is lost (but what lies below 2^-133), and an
+ * infinite or NaN value of b may make NaN where the formula gives infinity; rows of other
+ * adapters, and without one, are not affected by such values.
  * 1 <= r <= 128 (a larger rank is two adapters, one call after the other), 1 <= L <= 1023, M
  * up to 2^29, K and N up to 2^22. One launch up to 1,536 rows, two above.
  * Rows of x, a, add or out that are not whole 16-byte pieces (K, N or ldx no multiple of 8,

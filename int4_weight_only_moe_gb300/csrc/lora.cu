@@ -19,9 +19,8 @@
 // value, many of them 768 rows to a launch: 2,000 rows of 7,168 x 4,090 take 0.2 ms, where
 // 4,096 columns take 34 us.
 //
-// The first product's sums stay 32 bits: they enter the second product as two bf16 parts
-// (of 16 bits together; three, of 24, for an fp32 output), so that what is lost stays below
-// the rounding of the output. All sums have a fixed order: the same bits in every run.
+// The first product's sums stay 32 bits: they enter the second product as three bf16 parts,
+// 24 bits together. All sums have a fixed order: the same bits in every run.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -109,7 +108,7 @@ struct Few {
   static constexpr int kRank = 8 * kTiles;               // a multiple of 16
   static constexpr int kSums = kGroup * kRank;           // fp32
   static constexpr int kRow = kRank + 8;                 // bf16 of a row of parts
-  static constexpr int kSmem = (kWarps + kCluster) * kSums * 4 + 3 * kGroup * kRow * 2;
+  static constexpr int kSmem = (kWarps + kCluster) * kSums * 4 + kParts * kGroup * kRow * 2;
 };
 
 // Sums of 16 rows and up to 8 kTiles ranks. The order of the reduction's elements is free
@@ -117,12 +116,12 @@ struct Few {
 // the words 0, 1 make one MMA's elements (2t, 2t + 1, 2t + 8, 2t + 9) and 2, 3 the next's.
 // kWhole: rows of whole, aligned pieces.
 template <int kTiles, bool kWhole>
-__global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 1) lora_few_kernel(const LoraArgs a, int parts) {
+__global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 1) lora_few_kernel(const LoraArgs a) {
   using F = Few<kTiles>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* warp_sums = reinterpret_cast<float*>(smem);                                       // [warps][16][kRank]
   float* arrived = warp_sums + kWarps * F::kSums;                                          // [CTAs][16][kRank]
-  uint16_t* part_of = reinterpret_cast<uint16_t*>(arrived + kCluster * F::kSums);          // [parts][16][kRow]
+  uint16_t* part_of = reinterpret_cast<uint16_t*>(arrived + kCluster * F::kSums);          // [kParts][16][kRow]
   __shared__ int index_of[kFewRows];
   __shared__ int count_of[kMaxAdapters + 1];
   __shared__ int row_of[kGroup];
@@ -285,7 +284,8 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
     for (int c = 0; c < kCluster; ++c) s += arrived[c * F::kSums + i];
     s = i % F::kRank < a.r ? s * scale : 0.f;  // (an infinite x times the zeros behind r)
     const int at = i / F::kRank * F::kRow + i % F::kRank;
-    for (int p = 0; p < parts; ++p) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
       const uint16_t h = bf16_part(s);
       part_of[p * kGroup * F::kRow + at] = h;
       s = isfinite(s) ? s - bf16_value(h) : 0.f;
@@ -310,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, kTiles <= 4 ? 3 : kTiles <= 8 ? 2 : 
         const int row = n0 + 8 * (g >> 1) + 2 * j + (g & 1), i = 16 * s + 4 * t;
         y[j][s] = bf16x4<kWhole>(B + static_cast<long long>(row) * a.r + i, row < a.N ? a.r - i : 0);
       }
-    for (int p = parts - 1; p >= 0; --p) {  // (the small parts first)
+#pragma unroll
+    for (int p = kParts - 1; p >= 0; --p) {  // (the small parts first)
       const uint16_t* v = part_of + p * kGroup * F::kRow;
 #pragma unroll
       for (int s = 0; s < kTiles / 2; ++s) {
@@ -345,7 +346,7 @@ cudaError_t launch_few(const LoraArgs& a, cudaStream_t stream) {
   }
   const int groups = std::min(a.M, a.L + 1 + (a.M + kGroup - 1) / kGroup);
   return launch_cluster(lora_few_kernel<kTiles, kWhole>, dim3(static_cast<unsigned>(groups) * kCluster), dim3(kThreads),
-                        Few<kTiles>::kSmem, stream, kCluster, a, a.out_type == kTypeF32 ? 3 : 2);
+                        Few<kTiles>::kSmem, stream, kCluster, a);
 }
 
 template <bool kWhole>

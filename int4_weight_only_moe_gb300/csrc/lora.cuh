@@ -1,4 +1,4 @@
-// Addends and outputs of the low-rank adapters.
+// Addends and outputs of the low-rank adapters, and the parts of a sum.
 #pragma once
 #include <cuda_bf16.h>
 
@@ -13,6 +13,12 @@ __device__ __forceinline__ uint16_t bf16_part(float s) {
   const uint16_t h = __bfloat16_as_ushort(__float2bfloat16_rn(s));
   return (h & 0x7FFFu) == 0x7F80u && isfinite(s) ? static_cast<uint16_t>(h - 1) : h;
 }
+// The first product's fp32 sums enter the second one as so many bf16 parts, whatever the
+// output's type: each takes 8 of the 24 bits, and what is left behind the third is 0 (the parts
+// below 2^-133 apart). With two parts, 16 bits, a sum is off by up to 2^-17 of itself, which is
+// far below a bf16 output's rounding unless an addend, or another of the r terms, cancels
+// it: addends that leave 2^-12 of the adapter's term gave errors of 1e-2 of the result.
+constexpr int kParts = 3;
 __device__ __forceinline__ float addend(const LoraArgs& a, long long at) {
   if (!a.add) return 0.f;
   return a.add_type == kTypeF32 ? static_cast<const float*>(a.add)[at] : bf16_value(static_cast<const uint16_t*>(a.add)[at]);

@@ -9,8 +9,8 @@
 //      copied from wherever they lie;
 //   2. joins the sums with the cluster's other CTAs: each sends its sums of a row to the
 //      row's CTA, which adds them in the order of the ranks, scales them, splits them into
-//      bf16 parts (two, three for an fp32 output: 16 and 24 bits of the sum) and hands them
-//      to all CTAs, straight into the second product's operand;
+//      three bf16 parts (all 24 bits of the sum) and hands them to all CTAs, straight into
+//      the second product's operand;
 //   3. computes its share of the N columns: MMAs of 128 rows x 128 columns over the parts,
 //      one after another against the same tile of b[l], two accumulators in turn, taken out
 //      of tensor memory by eight warps that add the addends, which each thread has copied
@@ -63,10 +63,10 @@ constexpr int kSmemLeast = 96 * 1024;
 
 struct ManyPlan {
   int ctas;         // to a tile
-  int parts;        // bf16 parts of a sum
   int rank16;       // r, up to a multiple of 16
   int stages, stage_bytes, smem;
-  int b_stages;     // tiles of b under way
+  int b_stages;     // tiles of b under way,
+  int b_early;      // and those of them whose place is free while the sums are joined
   int deep;         // pieces of addends under way
   int tiles;        // at most
 };
@@ -191,10 +191,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   int* row_of = reinterpret_cast<int*>(gbase + 1024);  // [128] the tile's rows, -1 behind the last
   // Arriving sums: [CTA][r / 4][row] of four; then the stages of x and a. When those are done,
   // at the end of their place the second product's operand (blocks of 128 rows x 64 columns),
-  // in front of it tiles of b; and when the sums are joined, up to there addends.
+  // in front of it tiles of b (the last ones partly in the sums' place, and copied when those
+  // are joined); and when the sums are joined, up to there addends.
   const uint32_t sums_at = base + kHead, ring = sums_at + kTile * plan.rank16 * 4, adds_at = sums_at;
   const int wide = plan.rank16 > kChunk ? 2 : 1;  // boxes of a row of b
-  const uint32_t parts_at = base + plan.smem - 1024 - (plan.parts * plan.rank16 + kChunk - 1) / kChunk * kBox;
+  const uint32_t parts_at = base + plan.smem - 1024 - (kParts * plan.rank16 + kChunk - 1) / kChunk * kBox;
   const uint32_t b_ring = parts_at - plan.b_stages * wide * kBox;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   auto slot_of = [&](int i) { return ring + (i % S) * plan.stage_bytes; };
   const int SB = plan.b_stages;
-  auto b_slot_of = [&](int j) { return b_ring + (j % SB) * wide * kBox; };
+  auto b_slot_of = [&](int j) { return parts_at - (j % SB + 1) * wide * kBox; };
   const int piece = lane & 7;  // the 16 bytes of a 128-byte row that this lane copies
   // the copying warp's part of tile j of b: 32 columns at a time, rows in their order
   const uint16_t* b_from = a.b + static_cast<long long>(l) * a.N * a.r;
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     ok = ok && __all_sync(0xffffffffu, mbar_wait(summed, 0, abort_flag, status, kStatusTimeout, limit));
     cluster_wait();
     cluster_arrive();  // (the join goes on without this warp, which has tiles of b to copy)
-    for (; ok && issued < min(nn, SB); ++issued) ok = copy_b(issued);
+    for (; ok && issued < min(nn, plan.b_early); ++issued) ok = copy_b(issued);
   } else if (warp == kWarpMma) {
     const uint32_t idesc = idesc_bf16_f32(kTile, plan.rank16);
     const bool leader = elect_one();
@@ -475,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[j] = 8 * q < a.r ? s[j] * scale : 0.f;  // (infinite x times the zeros behind r)
-      for (int p = 0; p < plan.parts; ++p) {
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (leader) {
         // (the small parts first)
         uint32_t more = 0;
-        for (int p = plan.parts - 1; p >= 0; --p)
+        for (int p = kParts - 1; p >= 0; --p)
           for (int k = 0; k < plan.rank16; k += 16) {
             const int at = p * plan.rank16 + k;
             const uint64_t ad = sw128_kmajor_desc(parts_at + at / kChunk * kBox) + (at % kChunk) / 8;
@@ -619,11 +621,10 @@ int order_rows(int M, int L) {  // rows of the sorted order, whole tiles
 
 ManyPlan plan_many(const LoraArgs& a, int num_sms) {
   ManyPlan p{};
-  p.parts = a.out_type == kTypeF32 ? 3 : 2;
   p.rank16 = (a.r + 15) / 16 * 16;
   p.stage_bytes = kBox + (p.rank16 > kChunk ? kBox : p.rank16 * 128);
   const int fixed = kHead + 1024 + kTile * p.rank16 * 4;
-  const int operand = (p.parts * p.rank16 + kChunk - 1) / kChunk * kBox, b_tile = p.rank16 > kChunk ? 2 * kBox : kBox;
+  const int operand = (kParts * p.rank16 + kChunk - 1) / kChunk * kBox, b_tile = p.rank16 > kChunk ? 2 * kBox : kBox;
   // two CTAs to an SM if at least three stages, and the second product's operands in their
   // place, fit a half
   int room = kSmemHalf - fixed;
@@ -631,9 +632,11 @@ ManyPlan plan_many(const LoraArgs& a, int num_sms) {
   p.stages = std::min(kMaxStages, room / p.stage_bytes);  // (five at the least where one CTA has the SM)
   const bool half = room <= kSmemHalf - fixed;
   const int piece = kEpiThreads * 32 * (a.add_type == kTypeF32 ? 2 : 1);
-  p.b_stages = room >= operand + 2 * b_tile && room + kTile * p.rank16 * 4 >= operand + 2 * b_tile + 2 * piece ? 2 : 1;
-  const int ring = std::max(p.stages * p.stage_bytes, operand + p.b_stages * b_tile);
+  const int sums = kTile * p.rank16 * 4;
+  p.b_stages = room + sums >= operand + 2 * b_tile + 2 * piece ? 2 : 1;
+  const int ring = std::max(p.stages * p.stage_bytes, std::min(room, operand + p.b_stages * b_tile));
   p.smem = std::max(kSmemLeast, fixed + ring);
+  p.b_early = std::min(p.b_stages, (p.smem - fixed - operand) / b_tile);
   // (the sums' place and what the ring has left are at least a piece of addends: 8 KB, fp32 16)
   p.deep = std::max(1, std::min(kMaxDeep, (p.smem - kHead - 1024 - operand - p.b_stages * b_tile) / piece));
   const int per_sm = half ? 2 : 1;
