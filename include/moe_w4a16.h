@@ -340,6 +340,11 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
 
 /* Tokens sorted by expert, for expert products of the caller's own, and back.
  *
+ * Here, in the router's gradient and the low-rank adapters below, outputs have memory of
+ * their own: a call in which an output shares a byte with an input is refused
+ * (MOE_W4A16_INVALID_ARG), but that `add` may be `out`. Outputs that share memory with one
+ * another or with a workspace are not looked for: the caller keeps those apart.
+ *
  * The order of the experts' rows. Slot i = t * topk + j is token t's j-th choice, its
  * expert topk_ids[i] - expert_begin; ids outside [expert_begin, expert_begin + E) are
  * nobody's here (another part's experts, or -1 for a dropped choice). The rows are the
@@ -348,7 +353,7 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
  *             n = M topk: as many as there can be (-1: sizes that are not supported)
  *   offsets   int32 [E + 1]   out: where each expert's rows begin, and the end of the last's
  *   slots     int32 [rows]    out: the slot of a row; -1 in rows that fill up and behind the last
- *   position  int32 [M, topk] out: the row of a slot; -1 for nobody's (none of them in topk_ids' memory)
+ *   position  int32 [M, topk] out: the row of a slot; -1 for nobody's
  * The same expert may stand twice among a token's choices. 1 <= E <= 1024, topk <= 32, at
  * most 2^30 rows. M == 0 gives offsets of 0. One launch, no host synchronisation; the same
  * result in every run.
@@ -356,7 +361,7 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
  * gather: out[position[t, j]] = x[t]; 0 in rows that fill up an expert's; rows behind
  * offsets[E] are left as they were.
  *   x    fp32, bf16 or bytes (type) [M, K], rows row_stride elements apart
- *   out  [rows, K] of the same type, of its own memory
+ *   out  [rows, K] of the same type
  * K <= 2^22. Its gradient is moe_w4a16_combine without weights. One launch.
  *
  * sort_gather: both, in one launch up to 1,024 choices, two above.
@@ -367,7 +372,7 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
  *   y        fp32 or bf16 (y_type) [rows, K]
  *   weights  fp32 [M, topk], or NULL for weights of 1
  *   add      [M, K] of out's type, or NULL; may be out
- *   out      fp32 or bf16 (out_type) [M, K], not in y's memory
+ *   out      fp32 or bf16 (out_type) [M, K]
  * One launch.
  *
  * combine_backward: the gradient of combine (with weights) for grad = dL/dout:
@@ -375,7 +380,7 @@ int moe_w4a16_shared_expert(const uint16_t* hidden, const uint8_t* w1, const flo
  *                                                 offsets[E] are left as they were)
  *   dweights[t, j] = <grad[t], y[position[t, j]]>   in fp32; 0 where there is no row
  *   grad  fp32 or bf16 (grad_type) [M, K];  y, dy  fp32 or bf16 (y_type) [rows, K];
- *   dweights fp32 [M, topk];  dy and dweights in memory of their own
+ *   dweights fp32 [M, topk]
  * (The gradient of add is grad itself.) One launch. */
 long long moe_w4a16_dispatch_rows(int M, int topk, int E, int block);
 int moe_w4a16_dispatch_sort(const int32_t* topk_ids, int M, int topk, int expert_begin, int E, int block,
@@ -405,7 +410,7 @@ int moe_w4a16_combine_backward(const void* grad, int grad_type, const void* y, i
  * largest), also where 32 bits round the scores themselves to 0.
  *   dweights fp32 [M, topk], topk_ids int32 [M, topk]
  *   logits   fp32 or bf16 (logits_type) [M, E], rows row_stride elements apart
- *   dlogits  [M, E] of the same type, not in the logits' memory    out
+ *   dlogits  [M, E] of the same type    out
  * One launch on `stream`, no host synchronisation. */
 int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, int logits_type, long long row_stride,
                                     const int32_t* topk_ids, int M, int E, int topk, int scoring, int renormalize,
@@ -419,7 +424,7 @@ int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, i
  *          smaller rank are filled up with zeros
  *   add    fp32 or bf16 (add_type) [M, N], or NULL for 0; may be out where the types are
  *          the same (rows without an adapter are then not touched)
- *   out    fp32 or bf16 (out_type) [M, N], rounded once; not in x's memory
+ *   out    fp32 or bf16 (out_type) [M, N], rounded once
  *   workspace  >= moe_w4a16_lora_workspace_size(M, K, N, r, L) bytes (0 for sizes that are
  *          not supported, and where none is needed), 256-byte aligned; holds nothing between
  *          calls. NULL: as in moe_w4a16_shared_expert

@@ -1,6 +1,8 @@
 // C entry points of the operators between the router and the experts (order, gather,
 // combine, their gradients, the router's) and of the low-rank adapters: argument checks and
 // launches.
+#include <initializer_list>
+
 #include "../../include/moe_w4a16.h"
 #include "ops.cuh"
 
@@ -21,14 +23,31 @@ bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t
 bool float_type(int t) { return t == MOE_W4A16_F32 || t == MOE_W4A16_BF16; }
 int item(int type) { return type == MOE_W4A16_F32 ? 4 : type == MOE_W4A16_BF16 ? 2 : 1; }
 
-// Whether arrays of so many bytes share any (a null or an empty one shares none).
-bool share(const void* p, long long p_bytes, const void* q, long long q_bytes) {
-  const auto a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && p_bytes > 0 && q_bytes > 0 &&
-         (a <= b ? b - a < static_cast<uintptr_t>(p_bytes) : a - b < static_cast<uintptr_t>(q_bytes));
+// An array, of rows `stride` bytes apart where it has more than one.
+struct Array {
+  const void* p;
+  long long bytes;  // of a row
+  long long rows = 1, stride = 0;
+};
+Array matrix(const void* p, int rows, long long stride, int cols, int bytes) {
+  return {p, static_cast<long long>(cols) * bytes, rows, stride * bytes};
 }
-// Bytes from the first value of a matrix to behind its last.
-long long span(int rows, long long stride, int cols, int bytes) { return ((rows - 1) * stride + cols) * bytes; }
+// Whether it shares a byte with the array `q`, of one row (a null or an empty one shares none).
+bool share(const Array& x, const Array& q) {
+  if (!x.p || !q.p || x.bytes <= 0 || x.rows <= 0 || q.bytes <= 0) return false;
+  const auto a = static_cast<__int128>(reinterpret_cast<uintptr_t>(x.p)), b = static_cast<__int128>(reinterpret_cast<uintptr_t>(q.p));
+  // the first row that ends behind q's begin
+  const __int128 row = b < a + x.bytes ? 0 : x.rows == 1 ? 1 : (b - a - x.bytes) / x.stride + 1;
+  return row < x.rows && a + row * x.stride < b + q.bytes;
+}
+// Every output against every input that the same launches read.
+bool share(std::initializer_list<Array> inputs, std::initializer_list<Array> outputs) {
+  for (const Array& in : inputs)
+    for (const Array& out : outputs)
+      if (share(in, out)) return true;
+  return false;
+}
+constexpr const char* kShared = "an output may not share memory with an input";
 
 // Rows of an order, or -1 for sizes that are not supported.
 long long rows_of(int M, int topk, int E, int block) {
@@ -43,11 +62,6 @@ int check_order(int M, int topk, int E, int block) {
   if (topk > kMaxTopk || E > 1024) return shape("at most 32 choices a token and 1,024 experts");
   if (rows_of(M, topk, E, block) < 0) return shape("too many rows (at most 2^30, block at most 2^22)");
   return MOE_W4A16_OK;
-}
-
-bool ids_share(const int32_t* topk_ids, const int32_t* slots, const int32_t* position, int M, int topk, int E, int block) {
-  const long long n = 4LL * M * topk;
-  return share(topk_ids, n, position, n) || share(topk_ids, n, slots, 4 * rows_of(M, topk, E, block));
 }
 
 int check_order_out(const int32_t* offsets, const int32_t* slots, const int32_t* position) {
@@ -80,7 +94,8 @@ int moe_w4a16_dispatch_sort(const int32_t* topk_ids, int M, int topk, int expert
   if (!offsets || (M > 0 && (!topk_ids || !slots || !position))) return bad("null pointer argument");
   if (misaligned(topk_ids, 4) || misaligned(offsets, 4) || misaligned(slots, 4) || misaligned(position, 4))
     return bad("a pointer is not aligned to its type");
-  if (ids_share(topk_ids, slots, position, M, topk, E, block)) return bad("an output may not share memory with topk_ids");
+  const long long n = 4LL * M * topk;
+  if (share({{topk_ids, n}}, {{offsets, 4LL * (E + 1)}, {slots, 4 * rows_of(M, topk, E, block)}, {position, n}})) return bad(kShared);
   const SortArgs a{topk_ids, M * topk, expert_begin, E, 0, block, offsets, slots,
                    static_cast<int>(rows_of(M, topk, E, block)), position};
   return done(launch_sort(a, static_cast<cudaStream_t>(stream)));
@@ -93,13 +108,15 @@ int moe_w4a16_dispatch_gather(const void* x, int type, long long row_stride, con
   if (int rc = check_rows(x, type, row_stride, M, K, out)) return rc;
   if (M == 0) return MOE_W4A16_OK;
   if (int rc = check_order_out(offsets, slots, position)) return rc;
-  if (share(x, span(M, row_stride, K, item(type)), out, rows_of(M, topk, E, block) * K * item(type)))
-    return bad("out may not share memory with x");
+  const long long rows = rows_of(M, topk, E, block);
+  if (share({matrix(x, M, row_stride, K, item(type)), {offsets, 4LL * (E + 1)}, {slots, 4 * rows}, {position, 4LL * M * topk}},
+            {{out, rows * K * item(type)}}))
+    return bad(kShared);
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
   const GatherRowsArgs g{x, M > 1 ? row_stride * item(type) : 0, static_cast<long long>(K) * item(type), offsets, slots,
-                         position, out, M, topk, E, block, static_cast<int>(rows_of(M, topk, E, block))};
+                         position, out, M, topk, E, block, static_cast<int>(rows)};
   return done(launch_gather(g, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -112,13 +129,14 @@ int moe_w4a16_dispatch_sort_gather(const void* x, int type, long long row_stride
   if (M == 0) return moe_w4a16_dispatch_sort(topk_ids, M, topk, expert_begin, E, block, offsets, slots, position, stream);
   if (int rc = check_order_out(offsets, slots, position)) return rc;
   if (!topk_ids || misaligned(topk_ids, 4)) return bad("topk_ids is null or not aligned to its type");
-  if (share(x, span(M, row_stride, K, item(type)), out, rows_of(M, topk, E, block) * K * item(type)))
-    return bad("out may not share memory with x");
-  if (ids_share(topk_ids, slots, position, M, topk, E, block)) return bad("an output may not share memory with topk_ids");
+  const int rows = static_cast<int>(rows_of(M, topk, E, block));
+  const long long n = 4LL * M * topk;
+  if (share({matrix(x, M, row_stride, K, item(type)), {topk_ids, n}},
+            {{offsets, 4LL * (E + 1)}, {slots, 4LL * rows}, {position, n}, {out, static_cast<long long>(rows) * K * item(type)}}))
+    return bad(kShared);
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
-  const int rows = static_cast<int>(rows_of(M, topk, E, block));
   const SortArgs o{topk_ids, M * topk, expert_begin, E, 0, block, offsets, slots, rows, position};
   const GatherRowsArgs g{x, M > 1 ? row_stride * item(type) : 0, static_cast<long long>(K) * item(type), offsets, slots,
                          position, out, M, topk, E, block, rows};
@@ -136,9 +154,10 @@ int moe_w4a16_combine(const void* y, int y_type, const float* weights, const int
   if (misaligned(y, item(y_type)) || misaligned(weights, 4) || misaligned(position, 4) ||
       misaligned(add, item(out_type)) || misaligned(out, item(out_type)))
     return bad("a pointer is not aligned to its type");
-  const long long bytes = static_cast<long long>(M) * K * item(out_type);
-  if (share(y, static_cast<long long>(rows) * K * item(y_type), out, bytes)) return bad("out may not share memory with y");
-  if (add != out && share(add, bytes, out, bytes)) return bad("add and out may be one array or two, and not overlap");
+  const Array to{out, static_cast<long long>(M) * K * item(out_type)};
+  const long long n = 4LL * M * topk;
+  if (share({{y, static_cast<long long>(rows) * K * item(y_type)}, {weights, n}, {position, n}}, {to})) return bad(kShared);
+  if (add != out && share({add, to.bytes}, to)) return bad("add and out may be one array or two, and not overlap");
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
@@ -159,15 +178,16 @@ int moe_w4a16_combine_backward(const void* grad, int grad_type, const void* y, i
   if (misaligned(grad, item(grad_type)) || misaligned(y, item(y_type)) || misaligned(dy, item(y_type)) ||
       misaligned(weights, 4) || misaligned(dweights, 4))
     return bad("a pointer is not aligned to its type");
-  const long long bytes = rows_of(M, topk, E, block) * K * item(y_type), choices = 4LL * M * topk;
-  if (share(y, bytes, dy, bytes) || share(grad, static_cast<long long>(M) * K * item(grad_type), dy, bytes) ||
-      share(weights, choices, dweights, choices))
-    return bad("dy and dweights may not share memory with grad, y or weights");
+  const long long rows = rows_of(M, topk, E, block), bytes = rows * K * item(y_type), n = 4LL * M * topk;
+  if (share({{grad, static_cast<long long>(M) * K * item(grad_type)}, {y, bytes}, {weights, n}, {offsets, 4LL * (E + 1)}, {slots, 4 * rows},
+             {position, n}},
+            {{dy, bytes}, {dweights, n}}))
+    return bad(kShared);
   cudaError_t e;
   const int sms = num_sms(&e);
   if (e != cudaSuccess) return done(e);
   const CombineBackwardArgs c{grad, grad_type, y, y_type, weights, offsets, slots, position, dy, dweights,
-                              M, K, topk, E, block, static_cast<int>(rows_of(M, topk, E, block))};
+                              M, K, topk, E, block, static_cast<int>(rows)};
   return done(launch_combine_backward(c, sms, static_cast<cudaStream_t>(stream)));
 }
 
@@ -186,8 +206,10 @@ int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, i
   if (misaligned(logits, item(logits_type)) || misaligned(dlogits, item(logits_type)) || misaligned(dweights, 4) ||
       misaligned(topk_ids, 4))
     return bad("a pointer is not aligned to its type");
-  if (share(logits, span(M, row_stride, E, item(logits_type)), dlogits, static_cast<long long>(M) * E * item(logits_type)))
-    return bad("dlogits may not share memory with logits");
+  const long long n = 4LL * M * topk;
+  if (share({matrix(logits, M, row_stride, E, item(logits_type)), {dweights, n}, {topk_ids, n}},
+            {{dlogits, static_cast<long long>(M) * E * item(logits_type)}}))
+    return bad(kShared);
   const RouteBackwardArgs a{dweights, logits, logits_type, row_stride, topk_ids, M, E, topk,
                             scoring == MOE_W4A16_SCORE_SOFTMAX, renormalize != 0, scale, dlogits};
   return done(launch_route_backward(a, static_cast<cudaStream_t>(stream)));
@@ -217,9 +239,10 @@ int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const ui
       misaligned(out, item(out_type)) || (add && misaligned(add, item(add_type))))
     return bad("a pointer is not aligned to its type");
   if (add == out && add_type != out_type) return bad("add may be out only where they are of one type");
-  const long long bytes = static_cast<long long>(M) * N * item(out_type);
-  if (share(x, span(M, ldx, K, 2), out, bytes)) return bad("out may not share memory with x");
-  if (add != out && share(add, static_cast<long long>(M) * N * item(add_type), out, bytes))
+  const Array to{out, static_cast<long long>(M) * N * item(out_type)};
+  if (share({matrix(x, M, ldx, K, 2), {a, 2LL * L * r * K}, {b, 2LL * L * N * r}, {scale, 4LL * L}, {index, 4LL * M}}, {to}))
+    return bad(kShared);
+  if (add != out && share({add, static_cast<long long>(M) * N * item(add_type)}, to))
     return bad("add and out may be one array or two, and not overlap");
   if (misaligned(workspace, 256)) return bad("workspace must be 256-byte aligned");
   const size_t need = lora_workspace_bytes(M, r, L);
