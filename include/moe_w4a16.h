@@ -426,8 +426,9 @@ int moe_w4a16_route_scored_backward(const float* dweights, const void* logits, i
  *          the same (rows without an adapter are then not touched)
  *   out    fp32 or bf16 (out_type) [M, N], rounded once
  *   workspace  >= moe_w4a16_lora_workspace_size(M, K, N, r, L) bytes (0 for sizes that are
- *          not supported, and where none is needed), 256-byte aligned; holds nothing between
- *          calls. NULL: as in moe_w4a16_shared_expert
+ *          not supported, and where none is needed: up to 1,536 rows, and in the slower form
+ *          below, which a call may also take by its addresses and ldx), 256-byte aligned;
+ *          holds nothing between calls. NULL: as in moe_w4a16_shared_expert
  * Both products' sums are fp32. Between them the first one's are split into three bf16 parts
  * of 24 bits together, so that nothing of them is lost (but what lies below 2^-133), and an
  * infinite or NaN value of b may make NaN where the formula gives infinity; rows of other

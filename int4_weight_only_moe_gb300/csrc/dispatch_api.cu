@@ -223,7 +223,9 @@ bool lora_shape_ok(int M, int K, int N, int r, int L) {
 }  // namespace
 
 size_t moe_w4a16_lora_workspace_size(int M, int K, int N, int r, int L) {
-  return lora_shape_ok(M, K, N, r, L) ? lora_workspace_bytes(M, r, L) : 0;
+  if (!lora_shape_ok(M, K, N, r, L)) return 0;
+  return lora_workspace_bytes(LoraArgs{nullptr, K, nullptr, nullptr, nullptr, nullptr, nullptr, MOE_W4A16_F32, nullptr, MOE_W4A16_F32, M, K, N,
+                                       r, L, nullptr});
 }
 
 int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const uint16_t* b, const float* scale,
@@ -245,7 +247,8 @@ int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const ui
   if (add != out && share({add, static_cast<long long>(M) * N * item(add_type)}, to))
     return bad("add and out may be one array or two, and not overlap");
   if (misaligned(workspace, 256)) return bad("workspace must be 256-byte aligned");
-  const size_t need = lora_workspace_bytes(M, r, L);
+  LoraArgs args{x, ldx, a, b, scale, index, add, add_type, out, out_type, M, K, N, r, L, workspace};
+  const size_t need = lora_workspace_bytes(args);
   if (workspace && workspace_bytes < need)
     return report_error(MOE_W4A16_WORKSPACE_TOO_SMALL, "workspace too small (moe_w4a16_lora_workspace_size)");
   cudaError_t e;
@@ -258,8 +261,8 @@ int moe_w4a16_lora(const uint16_t* x, long long ldx, const uint16_t* a, const ui
     if (e == cudaSuccess) e = cudaMallocFromPoolAsync(&scratch, need, pool, s);
     if (e != cudaSuccess) return done(e);
   }
-  e = launch_lora(LoraArgs{x, ldx, a, b, scale, index, add, add_type, out, out_type, M, K, N, r, L,
-                           workspace ? workspace : scratch}, sms, s);
+  if (scratch) args.workspace = scratch;
+  e = launch_lora(args, sms, s);
   if (scratch) {
     const cudaError_t freed = cudaFreeAsync(scratch, s);
     if (e == cudaSuccess) e = freed;

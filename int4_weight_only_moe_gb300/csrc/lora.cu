@@ -361,16 +361,23 @@ bool aligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p
 
 }  // namespace
 
-size_t lora_workspace_bytes(int M, int r, int L) { return M > few_rows(r) ? lora_many_workspace(M, L) : 0; }
+namespace {
+// 16-byte pieces of every row.
+bool in_pieces(const LoraArgs& a) {
+  return a.K % 8 == 0 && a.N % 8 == 0 && (a.M == 1 || a.ldx % 8 == 0) && aligned(a.x, 16) && aligned(a.a, 16) && aligned(a.b, 16) &&
+         aligned(a.add, 16) && aligned(a.out, 16);
+}
+// Whether the kernel for many rows takes the call.
+bool takes_many(const LoraArgs& a) { return a.M > few_rows(a.r) && in_pieces(a) && a.r % 8 == 0; }
+}  // namespace
+
+size_t lora_workspace_bytes(const LoraArgs& a) { return takes_many(a) ? lora_many_workspace(a.M, a.L) : 0; }
 
 cudaError_t launch_lora(const LoraArgs& args, int num_sms, cudaStream_t stream) {
   LoraArgs a = args;
-  // 16-byte pieces of every row; for few rows 8 of b's will do
-  const bool pieces = a.K % 8 == 0 && a.N % 8 == 0 && (a.M == 1 || a.ldx % 8 == 0) && aligned(a.x, 16) && aligned(a.a, 16) &&
-                      aligned(a.b, 16) && aligned(a.add, 16) && aligned(a.out, 16);
+  if (takes_many(a)) return launch_lora_many(a, num_sms, stream);
   const int most = few_rows(a.r);
-  if (a.M > most && pieces && a.r % 8 == 0) return launch_lora_many(a, num_sms, stream);
-  const bool whole = pieces && a.r % 4 == 0;
+  const bool whole = in_pieces(a) && a.r % 4 == 0;  // (8 bytes of b's rows will do)
   const long long add_row = a.add_type == kTypeF32 ? 4LL * a.N : 2LL * a.N, out_row = a.out_type == kTypeF32 ? 4LL * a.N : 2LL * a.N;
   for (int m0 = 0; m0 < args.M; m0 += most) {
     a.M = std::min(most, args.M - m0);

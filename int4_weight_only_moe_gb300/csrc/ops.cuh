@@ -172,7 +172,9 @@ struct LoraArgs {
   void* workspace;  // lora_workspace_bytes()
 };
 constexpr int kMaxRank = 128;
-size_t lora_workspace_bytes(int M, int r, int L);
+// What the call needs: an order of the rows, where the kernel that reads one runs (null
+// pointers count as aligned).
+size_t lora_workspace_bytes(const LoraArgs& a);
 cudaError_t launch_lora(const LoraArgs& a, int num_sms, cudaStream_t stream);
 
 // Its kernel for many rows (lora_many.cu): rows of whole, aligned 16-byte pieces.
