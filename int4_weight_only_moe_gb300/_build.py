@@ -1,17 +1,19 @@
 """Build the CUDA library ``libmoe_w4a16.so`` in-tree for sm_103a with nvcc.
 
 The translation units are compiled in parallel and linked into a shared
-library next to this file (``int4_weight_only_moe_gb300/lib/``), and beside it the
-extension module ``moe_w4a16_calls.so`` of the Python calls. A rebuild is
-skipped when both are newer than every source and header.
+library next to this file (``int4_weight_only_moe_gb300/lib/``). That takes nvcc alone.
+Beside it stands the extension module ``moe_w4a16_calls.so`` of the Python calls, where
+torch is installed: the package works without it, small calls a few microseconds slower.
+What is newer than its sources is not built again.
 """
 from __future__ import annotations
 
-import os
 import importlib.util
+import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -37,17 +39,26 @@ def nvcc() -> str:
     return cand
 
 
-def _inputs():
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh", ".cpp"))]
+def _inputs(*kinds):
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(kinds)]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
     return files + [os.path.abspath(__file__)]
 
 
+def _newer(target, inputs) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in inputs)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, _inputs(".cu", ".cuh"))
+
+
+def _calls_up_to_date() -> bool:
+    return _torch() is None or _newer(CALLS, _inputs(".cpp"))
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return _library_up_to_date() and _calls_up_to_date()
 
 
 def _run(cmd):
@@ -57,19 +68,39 @@ def _run(cmd):
     return p.stdout
 
 
-def _torch() -> str:
+def _torch():
+    """Where torch is installed, or None."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("torch is needed to build the Python calls")
-    return list(spec.submodule_search_locations)[0]
+    return list(spec.submodule_search_locations)[0] if spec else None
+
+
+def _build_calls(torch: str) -> None:
+    """The extension module, against the library that stands there."""
+    inc, obj, tmp = os.path.join(torch, "include"), os.path.join(BUILD, "calls.o"), CALLS + ".tmp"
+    _run(["g++", "-std=c++17", "-O2", "-fPIC", "-w", "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+          "-I", sysconfig.get_path("include"), "-c", os.path.join(CSRC, "calls.cpp"), "-o", obj])
+    _run(["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lmoe_w4a16", "-L", os.path.join(torch, "lib"), "-ltorch_python",
+          "-ltorch_cpu", "-ltorch", "-lc10", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile the library if needed; return its path."""
-    if not force and up_to_date():
-        return LIB
+    """Compile what is needed; return the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
+    if force or not _library_up_to_date():
+        _build_library(verbose, ptxas_info)
+    if (torch := _torch()) and (force or not _calls_up_to_date()):
+        try:
+            _build_calls(torch)
+        except (RuntimeError, OSError) as e:
+            if os.path.exists(CALLS):
+                os.remove(CALLS)
+            warnings.warn(f"the compiled Python calls could not be built, the Python steps are taken: {e}")
+    return LIB
+
+
+def _build_library(verbose: bool, ptxas_info: bool) -> None:
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
@@ -78,17 +109,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         out = _run([cc, *ARCH, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj])
         return obj, out
 
-    calls = os.path.join(BUILD, "calls.o")
-
-    def compile_calls():
-        inc = os.path.join(_torch(), "include")
-        _run(["g++", "-std=c++17", "-O2", "-fPIC", "-w", "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
-              "-I", sysconfig.get_path("include"), "-c", os.path.join(CSRC, "calls.cpp"), "-o", calls])
-
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(compile_calls)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        module.result()
     if verbose or ptxas_info:
         for _, out in results:
             if out.strip():
@@ -96,11 +118,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     tmp = LIB + ".tmp"
     _run([cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-lcudart"])
     os.replace(tmp, LIB)
-    tmp = CALLS + ".tmp"
-    _run(["g++", "-shared", "-o", tmp, calls, "-L", LIBDIR, "-lmoe_w4a16", "-L", os.path.join(_torch(), "lib"), "-ltorch_python",
-          "-ltorch_cpu", "-ltorch", "-lc10", "-Wl,-rpath,$ORIGIN"])
-    os.replace(tmp, CALLS)
-    return LIB
 
 
 if __name__ == "__main__":
