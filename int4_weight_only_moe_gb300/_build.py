@@ -54,7 +54,14 @@ def _library_up_to_date() -> bool:
 
 
 def _calls_up_to_date() -> bool:
-    return _torch() is None or _newer(CALLS, _inputs(".cpp"))
+    torch = _torch()
+    if torch is None:
+        return True
+    try:
+        with open(CALLS + ".txt") as f:
+            return _newer(CALLS, _inputs(".cpp")) and f.read() == built_for(_version(torch))
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
@@ -74,6 +81,19 @@ def _torch():
     return list(spec.submodule_search_locations)[0] if spec else None
 
 
+def _version(torch: str) -> str:
+    """torch.__version__, without the import."""
+    spec = importlib.util.spec_from_file_location("torch_version", os.path.join(torch, "version.py"))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return str(module.__version__)
+
+
+def built_for(torch_version: str) -> str:
+    """What the extension holds for: written beside it when it is built."""
+    return f"torch {torch_version}, Python {sysconfig.get_config_var('EXT_SUFFIX')}\n"
+
+
 def _build_calls(torch: str) -> None:
     """The extension module, against the library that stands there."""
     inc, obj, tmp = os.path.join(torch, "include"), os.path.join(BUILD, "calls.o"), CALLS + ".tmp"
@@ -81,6 +101,8 @@ def _build_calls(torch: str) -> None:
           "-I", sysconfig.get_path("include"), "-c", os.path.join(CSRC, "calls.cpp"), "-o", obj])
     _run(["g++", "-shared", "-o", tmp, obj, "-L", LIBDIR, "-lmoe_w4a16", "-L", os.path.join(torch, "lib"), "-ltorch_python",
           "-ltorch_cpu", "-ltorch", "-lc10", "-Wl,-rpath,$ORIGIN"])
+    with open(CALLS + ".txt", "w") as f:
+        f.write(built_for(_version(torch)))
     os.replace(tmp, CALLS)
 
 

@@ -69,3 +69,77 @@ def test_each_is_built_for_its_own_sources(commands):
         assert not _build.up_to_date()
         _build.build()
         assert set(compilers(commands)) == want and _build.up_to_date()
+
+
+def test_another_torch_or_python_builds_the_extension_again(commands, monkeypatch):
+    import torch
+    assert _build._version(os.path.dirname(torch.__file__)) == torch.__version__
+    _build.build()
+    with open(_build.CALLS + ".txt") as f:
+        assert torch.__version__ in f.read()
+    for name, what in (("_version", lambda path: "1.2.3"), ("built_for", lambda version: f"{version}, another Python")):
+        commands.clear()
+        monkeypatch.setattr(_build, name, what)
+        assert not _build.up_to_date()
+        _build.build()
+        assert compilers(commands) == ["g++", "g++"] and _build.up_to_date()
+
+
+# ---------------------------------------------------------------- loading what was built
+
+
+@pytest.fixture
+def extension(monkeypatch, tmp_path):
+    """A file in the extension's place, of a text that is no library."""
+    from int4_weight_only_moe_gb300 import _calls
+    monkeypatch.setattr(_calls, "module", None)
+    monkeypatch.setattr(_calls, "_refused", None, raising=False)
+    monkeypatch.setattr(_calls, "PATH", str(tmp_path / "moe_w4a16_calls.so"))
+    with open(_calls.PATH, "w") as f:
+        f.write("no library")
+    return _calls
+
+
+def gather_by_steps(monkeypatch):
+    """A call with a given output, which asks for the extension, on tensors that only say where
+    they are: whether it has gone to the C entry of the Python steps."""
+    from int4_weight_only_moe_gb300 import dispatch
+    from tests import test_dispatch_devices_cpu as t
+    launched = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: launched.append(name) or 0
+
+    monkeypatch.setattr(dispatch, "lib", Lib)
+    monkeypatch.setattr(dispatch, "_order_rows", lambda m, k, e, b: m * k + min(e, m * k) * (b - 1))
+    monkeypatch.setattr(t.torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(t.torch._C, "_cuda_getCurrentRawStream", lambda dev: 7, raising=False)
+    t.CALLS["gather"][0](t.new("gather"))
+    return launched == ["moe_w4a16_dispatch_gather"]
+
+
+@pytest.mark.parametrize("note", [None, "torch 1.2.3, Python .so\n", "right"])
+def test_an_extension_that_does_not_load_leaves_the_python_steps(extension, monkeypatch, note):
+    import torch
+    if note:
+        with open(extension.PATH + ".txt", "w") as f:
+            f.write(extension.built_for(torch.__version__) if note == "right" else note)
+    with pytest.warns(UserWarning, match="Python steps"):
+        assert extension.load() is None
+    import warnings
+    with warnings.catch_warnings():  # (said once)
+        warnings.simplefilter("error")
+        assert extension.load() is None and extension.module is None
+        assert gather_by_steps(monkeypatch)
+    os.utime(extension.PATH, ns=(1, 1))  # another file there is tried
+    with pytest.warns(UserWarning, match="Python steps"):
+        assert extension.load() is None
+
+
+def test_what_was_built_here_is_loaded(monkeypatch):
+    import __graft_entry__
+    from int4_weight_only_moe_gb300 import _calls
+    __graft_entry__.build()
+    monkeypatch.setattr(_calls, "module", None)
+    assert _calls.load() is not None and _calls.load() is _calls.module
