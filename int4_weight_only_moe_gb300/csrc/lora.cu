@@ -17,7 +17,7 @@
 //
 // Rows that are not whole, aligned pieces of 16 bytes (8 of b) are read and written value by
 // value, many of them 768 rows to a launch: 2,000 rows of 7,168 x 4,090 take 0.2 ms, where
-// 4,096 columns take 34 us.
+// 4,096 columns take 38 us.
 //
 // The first product's sums stay 32 bits: they enter the second product as three bf16 parts,
 // 24 bits together. All sums have a fixed order: the same bits in every run.
@@ -35,9 +35,10 @@ constexpr int kThreads = 256;
 
 constexpr int kCluster = 8, kWarps = kThreads / 32;
 constexpr int kGroup = 16;      // rows of a cluster
-// Rows of a call up to which this kernel takes less time than the one for many rows: 512 rows,
-// 7,168 to 4,096 wide, 4 adapters of rank 32 or 64 14 and 18 us (there 29 and 32), 1,024 of 4 or
-// 48 27 (29) and 53 (60), of 32 37 (33); of rank 128, 512 rows 45 (37).
+// Rows of a call up to which this kernel takes less time than the one for many rows. At 7,168 to
+// 4,096 wide (no other width was measured): 512 rows of 4 adapters of rank 32 and 64 14.5 and 18.5
+// us (there 20.0 and 23.6); 900 rows of 8 of rank 64 37.5 (24.8); 1,024 rows of 4, 32 and 48 of rank
+// 64 37.8 (25.6), 52.5 (38.9) and 55.7 (56.7); 512 rows of 4 of rank 128 58.6 (29.6).
 constexpr int kFewRows = 768, kFewRowsWide = 384;
 int few_rows(int r) { return r <= 64 ? kFewRows : kFewRowsWide; }
 constexpr int kMaxAdapters = 1023;

@@ -2,9 +2,9 @@
 //
 // The rows of an adapter make tiles of 128 (rows without one are the last adapter's). Up to
 // 1,536 rows each CTA finds its tile's rows itself: it counts the rows of every adapter and
-// looks its own tile's up. Above, they are sorted first (the order of dispatch.cu). (900 rows:
-// 24.6 us, 26.7 sorted first; 2,048: 35.1 and 34.3; 4,096: 49.7 and 43.) A cluster of CTAs
-// takes a tile. Each CTA
+// looks its own tile's up. Above, they are sorted first (the order of dispatch.cu). (8 adapters
+// of rank 64, 900 rows: 24.7 us, 28.2 sorted first; 1,200: 32.2 and 33.1; 1,500: 35.6 and 35.0;
+// 2,048: 38.5 and 38.2; 4,096: 58.6 and 55.0.) A cluster of CTAs takes a tile. Each CTA
 //   1. sums its share of a[l] x's columns: tcgen05 MMAs of 128 rows x r, whose x rows are
 //      copied from wherever they lie;
 //   2. joins the sums with the cluster's other CTAs: each sends its sums of a row to the
