@@ -8,6 +8,7 @@ What is newer than its sources is not built again.
 """
 from __future__ import annotations
 
+import fcntl
 import importlib.util
 import os
 import shutil
@@ -107,18 +108,23 @@ def _build_calls(torch: str) -> None:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile what is needed; return the library's path."""
+    """Compile what is needed; return the library's path. One process at a time: another one
+    that builds here meanwhile waits, and finds it built."""
+    if not force and up_to_date():
+        return LIB
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
-    if force or not _library_up_to_date():
-        _build_library(verbose, ptxas_info)
-    if (torch := _torch()) and (force or not _calls_up_to_date()):
-        try:
-            _build_calls(torch)
-        except (RuntimeError, OSError) as e:
-            if os.path.exists(CALLS):
-                os.remove(CALLS)
-            warnings.warn(f"the compiled Python calls could not be built, the Python steps are taken: {e}")
+    with open(os.path.join(BUILD, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)  # (given back when the file is closed)
+        if force or not _library_up_to_date():
+            _build_library(verbose, ptxas_info)
+        if (torch := _torch()) and (force or not _calls_up_to_date()):
+            try:
+                _build_calls(torch)
+            except (RuntimeError, OSError) as e:
+                if os.path.exists(CALLS):
+                    os.remove(CALLS)
+                warnings.warn(f"the compiled Python calls could not be built, the Python steps are taken: {e}")
     return LIB
 
 

@@ -1,6 +1,8 @@
 """What the build makes where torch or its headers are not there: the compiler's commands are
 only written down, and what they would have written is there afterwards."""
 import os
+import time
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 
@@ -83,6 +85,33 @@ def test_another_torch_or_python_builds_the_extension_again(commands, monkeypatc
         assert not _build.up_to_date()
         _build.build()
         assert compilers(commands) == ["g++", "g++"] and _build.up_to_date()
+
+
+def test_builds_at_once_wait_for_one_another(commands, monkeypatch):
+    run, here = _build._run, []
+
+    def slowly(cmd):
+        linking = cmd[0] != "g++" and "-shared" in cmd
+        if linking:
+            here.append(1)
+            time.sleep(0.2)
+            assert len(here) == 1, "two builds link into one file"
+        out = run(cmd)
+        if linking:
+            here.pop()
+        return out
+
+    monkeypatch.setattr(_build, "_run", slowly)
+    with ThreadPoolExecutor(4) as pool:
+        for made in [pool.submit(_build.build) for _ in range(4)]:
+            assert made.result() == _build.LIB
+    assert len(commands) == len(_build.SOURCES) + 3  # (one of them built)
+
+
+def test_what_is_up_to_date_writes_nothing(commands, monkeypatch, tmp_path):
+    _build.build()
+    monkeypatch.setattr(_build, "BUILD", str(tmp_path / "nowhere"))
+    assert _build.build() == _build.LIB and not os.path.exists(_build.BUILD)
 
 
 # ---------------------------------------------------------------- loading what was built
